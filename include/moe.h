@@ -59,7 +59,9 @@ typedef enum {
   MOE_ERR_DEVICE_BOUNDS = 6   /* an expert index outside [0, E) was seen and skipped */
 } moe_status;
 
-typedef enum { MOE_BF16 = 0, MOE_E4M3 = 1, MOE_F32 = 2 } moe_dtype;
+/* MOE_MXFP4: 4-bit e2m1 codes with one scale byte per 32 values (see
+ * moe_mx_quantise); routed weights of moe_forward_few only. */
+typedef enum { MOE_BF16 = 0, MOE_E4M3 = 1, MOE_F32 = 2, MOE_MXFP4 = 3 } moe_dtype;
 
 typedef enum {
   /* top-k of the logits (descending, lowest index first on ties), softmax
@@ -369,6 +371,117 @@ moe_status moe_forward_profiled(const moe_shape* shape, const void* x, const voi
                                 const float* s2, const void* W1s, const void* W3s, const void* W2s, void* y,
                                 int32_t* topk_idx_out, float* topk_w_out, int32_t* counts_out, void* ws,
                                 size_t ws_bytes, void* stream, void* const* stage_events);
+
+/* The whole layer for a few tokens, T <= MOE_FEW_MAX_TOKENS, in one kernel: for
+ * serving, where a batch of one to a few tokens is a stream of the chosen
+ * experts' weights and moe_forward's launches and 128-row tiles cost more than
+ * they carry.  The same layer, with differences in precision only:
+ *   - the logits are summed in fp64 and rounded to fp32; in group mode the
+ *     sigmoid, the selection scores and the group scores are fp64 values of the
+ *     fp32 logits (a NaN score ranks last, the lowest index first among equals);
+ *   - h = silu(x W1) * (x W3) and every expert's output stay fp32 (moe_forward
+ *     rounds both to bf16); y is rounded once, to shape->y_dtype.
+ *   shape: as moe_forward; w_dtype may also be MOE_MXFP4.
+ *   W1, W3, W2, s1, s3, s2: bf16 and e4m3 weights (with fp32 block scales) as
+ *     moe_grouped_swiglu; MOE_MXFP4 weights with the contraction innermost, as
+ *     moe_mx_quantise_weights writes them from the bf16 layout: codes W1, W3
+ *     [E, inter, d/2], W2 [E, d, inter/2] and scale bytes s1, s3 [E, inter,
+ *     d/32], s2 [E, d, inter/32].  The shared expert is bf16.
+ *   Other arguments as moe_forward.
+ *   ws: moe_few_workspace_size(shape) bytes, 256-byte aligned; scratch and the
+ *     status word, as for the other calls.
+ * The kernel is launched cooperatively (its CTAs, one per SM, wait for one
+ * another), which a stream capture records like any other launch.
+ * Errors as moe_forward; MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_TOKENS, and
+ * for layers of 2^24 and more 128 x 128 blocks of routed weights that T tokens
+ * may choose. */
+#define MOE_FEW_MAX_TOKENS 16
+size_t moe_few_workspace_size(const moe_shape* shape);
+moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg, const float* bias, const void* W1,
+                           const void* W3, const void* W2, const void* s1, const void* s3, const void* s2,
+                           const void* W1s, const void* W3s, const void* W2s, void* y, int32_t* topk_idx_out,
+                           float* topk_w_out, int32_t* counts_out, void* ws, size_t ws_bytes, void* stream);
+
+/* MXFP4 (OCP microscaling formats, MXFP4): 32 consecutive values along the
+ * innermost dimension share a scale 2^(s - 127), one byte s (255: NaN), and
+ * each value is a 4-bit e2m1 code: sign, two exponent bits, one mantissa bit,
+ * magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.  Two codes to a byte, the even index
+ * in the low half.
+ *
+ * moe_mx_quantise: rows of `cols` values (fp32 or bf16, row r at src + r * ld
+ * elements) to codes [rows, cols/2] and scales [rows, cols/32].  With m the
+ * block's largest magnitude, s = floor(log2 m) - 2 + 127, at least 0 (127 where
+ * m = 0); a value becomes the nearest code, ties to the even one, magnitudes
+ * over 6 scales become 6.  A block with a NaN or an infinity gets s = 255 and
+ * codes 0: all of it reads back as NaN.
+ *   up: optional second source of the same type, ld and shape; the values
+ *     quantised are then silu(src) * up, computed in fp32 (the step between an
+ *     expert's two products).
+ *   cols a multiple of 32, ld >= cols; src and up aligned to their element (16
+ *   bytes and ld * size a multiple of 16 for the wide loads), codes and scales
+ *   16-byte aligned. */
+moe_status moe_mx_quantise(const void* src, const void* up, int src_dtype, int64_t rows, int cols, int64_t ld,
+                           void* codes, void* scales, void* stream);
+
+/* Weight matrices W [E, K, N] (fp32 or bf16, the layout of W1, W3 and W2) to
+ * codes [E, N, K/2] and scales [E, N, K/32]: blocks along the contraction K,
+ * which becomes the innermost dimension.  K a multiple of 32, any N >= 1, E <=
+ * 65535. */
+moe_status moe_mx_quantise_weights(const void* W, int src_dtype, int E, int K, int N, void* codes, void* scales,
+                                   void* stream);
+
+/* The values of codes [rows, cols/2] with scales [rows, cols/32] in dst [rows,
+ * cols], fp32 or bf16 (both hold every value that quantisation leaves of
+ * finite data exactly). */
+moe_status moe_mx_dequantise(const void* codes, const void* scales, int64_t rows, int cols, void* dst, int dst_dtype,
+                             void* stream);
+
+/* Grouped product of MXFP4 rows with MXFP4 expert weights:
+ *   Y[r, n] = sum_k A[r, k] W[e, n, k]  for offsets[e] <= r < offsets[e+1],
+ * accumulated in fp32 and rounded once to y_dtype (MOE_F32 or MOE_BF16).
+ *   A codes [rows, K/2], scales [rows, K/32] (moe_mx_quantise of permuted rows);
+ *   offsets [E+1] int32 (moe_permute); W codes [E, N, K/2], scales [E, N, K/32]
+ *   (moe_mx_quantise_weights of [E, K, N]); Y [rows, N].
+ * Rows behind offsets[E] (and before offsets[0]) are left as they are.  An
+ * expert whose offsets descend or leave [0, rows] gets no rows and raises
+ * MOE_ERR_DEVICE_BOUNDS in the workspace status word.
+ *   K and N multiples of 128, 1 <= E <= 1024, rows and E * N below 2^31;
+ *   ws: moe_mx_product_workspace_size(rows, E) bytes, 256-byte aligned. */
+size_t moe_mx_product_workspace_size(int64_t rows, int E);
+moe_status moe_mx_grouped_product(int64_t rows, int E, int K, int N, const void* A, const void* A_scales,
+                                  const int32_t* offsets, const void* W, const void* W_scales, void* Y, int y_dtype,
+                                  void* ws, size_t ws_bytes, void* stream);
+
+/* One gradient (or other) tensor of a set: `count` elements of dtype (MOE_F32
+ * or MOE_BF16) at data, aligned to the element.  out: where moe_grad_clip
+ * writes (the same type and count), NULL for in place. */
+typedef struct {
+  void* data;
+  void* out;
+  int64_t count;
+  int32_t dtype;
+} moe_tensor;
+#define MOE_GRAD_MAX_TENSORS 1024
+
+/* Global norm of a set of gradients: norm_out[0] = sqrt(sum of squares of all
+ * elements of all n tensors), summed in fp64, rounded once to fp32.  A NaN or
+ * an infinity among the elements shows in it; an empty set has norm 0.  The
+ * gradients of moe_backward are such a set.  `tensors` is a host array, read
+ * before the call returns.  n <= MOE_GRAD_MAX_TENSORS (MOE_ERR_UNSUPPORTED
+ * beyond); ws: moe_grad_workspace_size(n) bytes of device memory, 256-byte
+ * aligned, scratch (no status word). */
+size_t moe_grad_workspace_size(int n);
+moe_status moe_grad_norm(const moe_tensor* tensors, int n, float* norm_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Clipping by the global norm: out = data * min(1, max_norm / (norm + 1e-6)),
+ * one fp32 product rounded to the tensor's type; norm_out as moe_grad_norm
+ * (may be NULL).  An infinite norm gives the factor 0 and a NaN norm a NaN
+ * factor, so norm_out tells whether a step is to be skipped.  In place and with
+ * factor 1 the tensors are not written.  max_norm >= 0.  No written range may
+ * overlap another tensor's range, or its own source other than exactly in place
+ * (MOE_ERR_INVALID_ARG). */
+moe_status moe_grad_clip(const moe_tensor* tensors, int n, float max_norm, float* norm_out, void* ws, size_t ws_bytes,
+                         void* stream);
 
 /* Synchronises `stream`, reads the status word of `ws` written by the last
  * call that used this workspace and returns MOE_OK, MOE_ERR_DEVICE_TIMEOUT or

@@ -18,7 +18,9 @@ LIB_PATH = os.path.join(_PKG, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, \
     MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_DEVICE_BOUNDS = range(7)
-MOE_BF16, MOE_E4M3, MOE_F32 = 0, 1, 2
+MOE_BF16, MOE_E4M3, MOE_F32, MOE_MXFP4 = 0, 1, 2, 3
+MOE_FEW_MAX_TOKENS = 16
+MOE_GRAD_MAX_TENSORS = 1024
 MOE_ROUTE_TOPK_SOFTMAX, MOE_ROUTE_SIGMOID_GROUP = 0, 1
 
 EXPORTED = ("moe_workspace_size", "moe_router_topk", "moe_permute", "moe_grouped_swiglu", "moe_combine",
@@ -26,7 +28,9 @@ EXPORTED = ("moe_workspace_size", "moe_router_topk", "moe_permute", "moe_grouped
             "moe_permute_noalloc", "moe_router_topk_limited", "moe_expert_utilisation", "moe_forward_ep",
             "moe_forward_launches", "moe_combine_backward", "moe_router_backward", "moe_backward_workspace_size",
             "moe_backward", "moe_shared_expert", "moe_ep_regroup_layout", "moe_gather_rows", "moe_forward_train",
-            "moe_backward_saved")
+            "moe_backward_saved", "moe_few_workspace_size", "moe_forward_few", "moe_mx_quantise",
+            "moe_mx_quantise_weights", "moe_mx_dequantise", "moe_mx_product_workspace_size", "moe_mx_grouped_product",
+            "moe_grad_workspace_size", "moe_grad_norm", "moe_grad_clip")
 NUM_STAGE_EVENTS = 6
 STAGES = ("router", "dispatch", "experts_up", "experts_down", "combine")
 
@@ -42,6 +46,11 @@ class MoeShape(ctypes.Structure):
                 ("inter", ctypes.c_int32), ("shared_inter", ctypes.c_int32), ("route", ctypes.c_int32),
                 ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32), ("group_topn", ctypes.c_int32),
                 ("route_scale", ctypes.c_float), ("w_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32)]
+
+
+class MoeTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
 
 
 def make_shape(T, d, E, k, inter, shared_inter, route=0, n_group=1, topk_group=1, group_topn=2,
@@ -95,11 +104,27 @@ def lib() -> ctypes.CDLL:
         L.moe_backward.argtypes = [S] + [P] * 18 + [P, sz, P]
         L.moe_forward_train.argtypes = [S] + [P] * 10 + [P, sz, P]
         L.moe_backward_saved.argtypes = [S] + [P] * 17 + [P, sz, P]
+        L.moe_few_workspace_size.argtypes = [S]
+        L.moe_few_workspace_size.restype = sz
+        L.moe_forward_few.argtypes = [S] + [P] * 16 + [P, sz, P]
+        i64 = ctypes.c_int64
+        L.moe_mx_quantise.argtypes = [P, P, I, i64, I, i64, P, P, P]
+        L.moe_mx_quantise_weights.argtypes = [P, I, I, I, I, P, P, P]
+        L.moe_mx_dequantise.argtypes = [P, P, i64, I, P, I, P]
+        L.moe_mx_product_workspace_size.argtypes = [i64, I]
+        L.moe_mx_product_workspace_size.restype = sz
+        L.moe_mx_grouped_product.argtypes = [i64, I, I, I, P, P, P, P, P, P, I, P, sz, P]
+        L.moe_grad_workspace_size.argtypes = [I]
+        L.moe_grad_workspace_size.restype = sz
+        L.moe_grad_norm.argtypes = [P, I, P, P, sz, P]
+        L.moe_grad_clip.argtypes = [P, I, ctypes.c_float, P, P, sz, P]
         L.moe_check_device_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_uint32)]
         for fn in ("moe_router_topk", "moe_permute", "moe_grouped_swiglu", "moe_combine", "moe_combine_backward",
                    "moe_router_backward", "moe_forward",
                    "moe_forward_profiled", "moe_forward_ep", "moe_backward", "moe_shared_expert", "moe_ep_regroup_layout", "moe_gather_rows",
-                   "moe_forward_train", "moe_backward_saved", "moe_check_device_status"):
+                   "moe_forward_train", "moe_backward_saved", "moe_forward_few", "moe_mx_quantise",
+                   "moe_mx_quantise_weights", "moe_mx_dequantise", "moe_mx_grouped_product", "moe_grad_norm",
+                   "moe_grad_clip", "moe_check_device_status"):
             getattr(L, fn).restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_status_string.restype = ctypes.c_char_p
@@ -294,6 +319,197 @@ def backward_saved(shape, x, Wg, W1, W3, W2, W1s, W3s, W2s, dy, dx, dWg, dW1, dW
                                     _ptr(W3s), _ptr(W2s), _ptr(dy), _ptr(dx), _ptr(dWg), _ptr(dW1), _ptr(dW3),
                                     _ptr(dW2), _ptr(dW1s), _ptr(dW3s), _ptr(dW2s), _ptr(ws),
                                     ws.numel() if ws is not None else 0, _stream(stream)), "moe_backward_saved")
+
+
+# ------------------------------------------------------------------ few tokens, MXFP4, gradients
+# The calls below run on the device of their tensors, whichever is current, and
+# by default on that device's current stream.
+_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _on(device, stream, call):
+    if device.type != "cuda":
+        raise ValueError(f"libmoe works on CUDA tensors, got one on {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if stream.device != device:
+        raise ValueError(f"stream on {stream.device} for tensors on {device}")
+    if device.index == torch.cuda.current_device():
+        return call(stream.cuda_stream)
+    with torch.cuda.device(device):
+        return call(stream.cuda_stream)
+
+
+def _adr(t, device):
+    """Address of a contiguous tensor on `device` (None stays None)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libmoe must be contiguous")
+    if t.device != device:
+        raise ValueError(f"tensors on {t.device} and {device} in one call")
+    return t.data_ptr()
+
+
+def _dtype(t):
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"fp32 or bf16 tensors only, got {t.dtype}") from None
+
+
+def _sized(t, n, what):
+    if t.numel() != n:
+        raise ValueError(f"{what} has {t.numel()} elements, {n} needed")
+
+
+def few_workspace_size(shape: MoeShape) -> int:
+    return int(lib().moe_few_workspace_size(ctypes.byref(shape)))
+
+
+def alloc_few_workspace(shape: MoeShape, device="cuda") -> torch.Tensor:
+    n = few_workspace_size(shape)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_few_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def forward_few(shape, x, Wg, bias, W1, W3, W2, s1, s3, s2, W1s, W3s, W2s, y, ws, topk_idx=None, topk_w=None,
+                counts=None, stream=None):
+    """The layer for at most MOE_FEW_MAX_TOKENS tokens (moe_forward_few), bf16,
+    e4m3 or MXFP4 experts; arguments as forward()."""
+    dev = x.device
+    a = [_adr(t, dev) for t in (x, Wg, bias, W1, W3, W2, s1, s3, s2, W1s, W3s, W2s, y, topk_idx, topk_w, counts, ws)]
+    fn, size = lib().moe_forward_few, ws.numel()
+    _check(_on(dev, stream, lambda st: fn(ctypes.byref(shape), *a, size, st)), "moe_forward_few")
+
+
+def mx_quantise(src, codes, scales, up=None, stream=None):
+    """MXFP4 codes and scale bytes of rows (moe_mx_quantise): src [..., cols]
+    fp32 or bf16, innermost dimension contiguous and the rows evenly spaced;
+    codes [..., cols/2] and scales [..., cols/32] uint8.  up: quantise
+    silu(src) * up instead."""
+    cols = src.shape[-1]
+    rows = src.numel() // cols if cols else 0
+    ld = _row_stride(src)
+    if up is not None and (up.shape != src.shape or up.dtype != src.dtype or _row_stride(up) != ld):
+        raise ValueError("src and up must have the same shape, type and strides")
+    _sized(codes, rows * cols // 2, "codes")
+    _sized(scales, rows * cols // 32, "scales")
+    dev, dt = src.device, _dtype(src)
+    c, s = _adr(codes, dev), _adr(scales, dev)
+    u = None
+    if up is not None:
+        if up.device != dev:
+            raise ValueError(f"tensors on {up.device} and {dev} in one call")
+        u = up.data_ptr()
+    fn = lib().moe_mx_quantise
+    _check(_on(dev, stream, lambda st: fn(src.data_ptr(), u, dt, rows, cols, ld, c, s, st)), "moe_mx_quantise")
+
+
+def _row_stride(t):
+    """Elements between neighbouring rows of a tensor whose rows are evenly spaced."""
+    if t.dim() == 0 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError("rows must be contiguous")
+    if t.is_contiguous():
+        return t.shape[-1]
+    if t.dim() == 2:
+        ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+        if ld >= t.shape[1]:
+            return ld
+    raise ValueError("rows must be evenly spaced and must not overlap")
+
+
+def mx_quantise_weights(W, codes, scales, stream=None):
+    """MXFP4 codes [E, N, K/2] and scale bytes [E, N, K/32] of weights [E, K, N]
+    (moe_mx_quantise_weights); a matrix [K, N] is one expert."""
+    if W.dim() not in (2, 3):
+        raise ValueError("weights are [E, K, N] or [K, N]")
+    E, (K, N) = (W.shape[0] if W.dim() == 3 else 1), W.shape[-2:]
+    _sized(codes, E * N * K // 2, "codes")
+    _sized(scales, E * N * K // 32, "scales")
+    dev, dt = W.device, _dtype(W)
+    w, c, s = _adr(W, dev), _adr(codes, dev), _adr(scales, dev)
+    fn = lib().moe_mx_quantise_weights
+    _check(_on(dev, stream, lambda st: fn(w, dt, E, K, N, c, s, st)), "moe_mx_quantise_weights")
+
+
+def mx_dequantise(codes, scales, dst, stream=None):
+    """The values of MXFP4 codes (moe_mx_dequantise) in dst [..., cols], fp32 or bf16."""
+    cols = dst.shape[-1]
+    rows = dst.numel() // cols if cols else 0
+    _sized(codes, rows * cols // 2, "codes")
+    _sized(scales, rows * cols // 32, "scales")
+    dev, dt = dst.device, _dtype(dst)
+    c, s, d = _adr(codes, dev), _adr(scales, dev), _adr(dst, dev)
+    fn = lib().moe_mx_dequantise
+    _check(_on(dev, stream, lambda st: fn(c, s, rows, cols, d, dt, st)), "moe_mx_dequantise")
+
+
+def alloc_mx_product_workspace(rows: int, E: int, device="cuda") -> torch.Tensor:
+    n = int(lib().moe_mx_product_workspace_size(int(rows), int(E)))
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_mx_product_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def mx_grouped_product(A, A_scales, offsets, W, W_scales, Y, ws, stream=None):
+    """Y[r] = A[r] W[e]^T for the rows of each expert (moe_mx_grouped_product):
+    A codes [rows, K/2], scales [rows, K/32]; offsets [E + 1] int32; W codes
+    [E, N, K/2], scales [E, N, K/32]; Y [rows, N] fp32 or bf16."""
+    rows, K = A.shape[0], 2 * A.shape[1]
+    E, N = W.shape[0], W.shape[1]
+    if W.shape[2] * 2 != K or Y.shape != (rows, N) or offsets.dtype != torch.int32:
+        raise ValueError("shapes of A, W, Y or the type of offsets do not fit together")
+    _sized(offsets, E + 1, "offsets")
+    _sized(A_scales, rows * K // 32, "A_scales")
+    _sized(W_scales, E * N * K // 32, "W_scales")
+    dev, dt = A.device, _dtype(Y)
+    a = [_adr(t, dev) for t in (A, A_scales, offsets, W, W_scales, Y)]
+    w, size = _adr(ws, dev), ws.numel()
+    fn = lib().moe_mx_grouped_product
+    _check(_on(dev, stream, lambda st: fn(rows, E, K, N, *a, dt, w, size, st)), "moe_mx_grouped_product")
+
+
+def alloc_grad_workspace(n: int, device="cuda") -> torch.Tensor:
+    size = int(lib().moe_grad_workspace_size(int(n)))
+    if size == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_grad_workspace_size")
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def _tensor_list(grads, out, device):
+    arr = (MoeTensor * max(1, len(grads)))()
+    if out is not None and len(out) != len(grads):
+        raise ValueError(f"{len(out)} outputs for {len(grads)} tensors")
+    for i, g in enumerate(grads):
+        o = None
+        if out is not None:
+            if out[i].dtype != g.dtype or out[i].shape != g.shape:
+                raise ValueError("an output differs from its tensor in type or shape")
+            o = _adr(out[i], device)
+        arr[i] = (_adr(g, device), o, g.numel(), _dtype(g))
+    return arr
+
+
+def grad_norm(grads, norm, ws, stream=None):
+    """norm [1] fp32 = the global norm of the tensors of `grads` (moe_grad_norm)."""
+    dev = norm.device
+    arr, n = _tensor_list(grads, None, dev), len(grads)
+    o, w, size = _adr(norm, dev), _adr(ws, dev), ws.numel()
+    fn = lib().moe_grad_norm
+    _check(_on(dev, stream, lambda st: fn(arr, n, o, w, size, st)), "moe_grad_norm")
+
+
+def grad_clip(grads, max_norm, norm, ws, out=None, stream=None):
+    """Scale the tensors of `grads` by min(1, max_norm / (norm + 1e-6)) of their
+    global norm (moe_grad_clip), in place or into the tensors of `out`; norm [1]
+    fp32 receives the norm before clipping (None: not returned)."""
+    dev = ws.device
+    arr, n = _tensor_list(grads, out, dev), len(grads)
+    o, w, size = _adr(norm, dev), _adr(ws, dev), ws.numel()
+    fn = lib().moe_grad_clip
+    _check(_on(dev, stream, lambda st: fn(arr, n, max_norm, o, w, size, st)), "moe_grad_clip")
 
 
 def check_device_status(ws, stream=None) -> tuple[int, int]:

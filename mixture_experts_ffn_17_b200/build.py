@@ -18,8 +18,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 
 SOURCES = ["moe_api.cu", "router.cu", "permute.cu", "grouped_gemm.cu", "combine.cu", "monitor.cu", "backward.cu",
-           "grouped_gemm_bwd.cu", "ep.cu"]
-HEADERS = ["ptx.cuh", "common.cuh", "moe_internal.h", "backward.h"]
+           "grouped_gemm_bwd.cu", "ep.cu", "ops_api.cu", "few.cu", "mx.cu", "mx_gemm.cu", "grad.cu"]
+HEADERS = ["ptx.cuh", "common.cuh", "moe_internal.h", "backward.h", "api_internal.h", "few.h", "mx.h", "grad.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-O3",

@@ -1,0 +1,44 @@
+// few.h -- host-side declarations of the few-token layer kernel.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace moe {
+
+constexpr int kFewMaxTokens = 16;
+constexpr int kFewMaxSms = 256;  // the workspace holds partial sums for this many CTAs
+constexpr int kFewCols = 128;    // output columns of a segment
+constexpr int kFewStep = 128;    // contraction length of a work unit
+
+// How a call's routed expert weights are held.
+enum FewWeights : int { kFewBf16 = 0, kFewE4m3 = 1, kFewMxfp4 = 2 };
+
+struct FewParams {
+  int T, d, E, k, I, S;  // S = 0: no shared expert
+  int route, n_group, topk_group, group_topn;
+  float route_scale;
+  int y_bf16;
+  const uint16_t* x;
+  const uint16_t* Wg;
+  const float* bias;  // may be null
+  const uint8_t *W1, *W3, *W2;
+  const uint8_t *s1, *s3, *s2;  // fp32 block scales or scale bytes
+  const uint8_t *W1s, *W3s, *W2s;
+  void* y;
+  int32_t* idx_out;    // may be null
+  float* w_out;        // may be null
+  int32_t* counts_out; // may be null
+  uint32_t* status;
+  uint32_t* bar;       // arrivals at each of the grid's barriers, zero before the launch
+  float* logits;       // [T, E]
+  float *up_r, *up_s, *dn_r, *dn_s;  // partial sums, [segment + CTA][row][kFewCols]
+  uint16_t* h;         // [T * k + T][3][ld_h] bf16 terms of the activations
+  int ld_h;
+};
+
+size_t few_smem_bytes(const FewParams& p, int weights);
+cudaError_t launch_few(const FewParams& p, int weights, int sms, cudaStream_t stream);
+
+}  // namespace moe

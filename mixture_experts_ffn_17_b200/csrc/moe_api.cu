@@ -917,6 +917,25 @@ moe_status zero_weight_grads(const moe_shape& s, void* dWg, void* dW1, void* dW3
 }
 
 }  // namespace
+
+// What the entry points of ops_api.cu share with the ones below.
+moe_status check_shape(const moe_shape* shape) { return validate_shape(shape); }
+
+int device_sms() { return num_sms(); }
+
+// Bytes, row-major [outer, inner]; box [box_outer x 128], 128-byte swizzle.
+bool map_bytes(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_outer) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {inner};
+  cuuint32_t box[2] = {128, box_outer};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace moe
 
 using namespace moe;

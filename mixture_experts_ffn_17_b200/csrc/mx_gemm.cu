@@ -1,0 +1,381 @@
+// mx_gemm.cu -- grouped product of MXFP4 rows with MXFP4 expert weights.
+//
+//   Y[r, n] = sum_k A[r, k] W[e, n, k]   for offsets[e] <= r < offsets[e + 1],
+//
+// both operands as 4-bit codes with a scale byte per 32 values of k, on
+// tcgen05.mma kind::mxf4 (64 steps of k an instruction, scales applied by the
+// tensor core, fp32 accumulation in TMEM).
+//
+// The operands change sides: 128 rows of W (output columns) are the M = 128
+// side and up to 192 token rows the N side, in multiples of 16.  A decode batch
+// has one or two rows an expert, and a tile then costs its weights' bytes and
+// 16 columns of tensor work instead of a 128-row tile of padding; and lane i of
+// the accumulator holds output column i, so a warp's store of one token's
+// values is one contiguous run.
+//
+// Persistent CTAs, one per SM, over tiles (token tile of an expert, 128 output
+// columns), the column blocks of one token tile next to each other: the tokens
+// stay in L2 and the weights stream.  Roles: a producer thread (TMA, 256 steps
+// of k = 128 bytes a row and stage, 128-byte swizzle), four warps that bring the
+// scale bytes from their row-major arrays into the 512-byte blocks which
+// tcgen05.cp spreads over TMEM (row r of 128 at byte (r % 32) * 16 + (r / 32) * 4,
+// four blocks of 32 steps next to each other), an MMA thread, and four warps
+// that drain the accumulators (two, so that draining overlaps the next tile).
+// TMEM: 2 x 192 accumulator columns and 24 columns of scales a stage.
+//
+// Bound: HBM by the weights (17/32 byte a value) up to several hundred rows an
+// expert.
+#include <algorithm>
+#include <cstdint>
+
+#include "common.cuh"
+#include "mx.h"
+
+namespace moe {
+namespace {
+
+constexpr int kStages = 5;
+constexpr int kTok = kMxTileTokens;  // token rows of a tile
+constexpr int kM = 128;              // output columns of a tile
+constexpr int kK = 256;              // steps of k of a stage
+constexpr uint32_t kWBytes = kM * kK / 2;
+constexpr uint32_t kTBytes = kTok * kK / 2;
+constexpr uint32_t kSfW = 2 * 512;      // two 128-step halves of 128 rows
+constexpr uint32_t kSfT = 2 * 2 * 512;  // two halves of 2 x 128 rows
+constexpr uint32_t kStageBytes = kWBytes + kTBytes + kSfW + kSfT;
+static_assert(kStageBytes % 1024 == 0, "stages stay aligned for the 128-byte swizzle");
+constexpr int kSfCols = 8 + 16;  // TMEM columns of a stage's scales
+constexpr int kTmemCols = 512;
+static_assert(2 * kTok + kStages * kSfCols <= kTmemCols, "TMEM columns");
+constexpr size_t kSmem = kStages * kStageBytes + 1024 + 256;
+constexpr int kThreads = 320;  // 4 epilogue warps, 4 scale warps, producer, MMA
+constexpr uint32_t kOne4 = 0x7f7f7f7fu;  // four scales of 1
+
+struct Tile {
+  int64_t row0;
+  int e, nb, rows;
+};
+
+// kind::mxf4 instruction descriptor: A and B e2m1 (bits 7-9 and 10-11 = 1),
+// N >> 3 at bits 17-22, ue8m0 scales (bit 23), M >> 7 at bits 27-28, and which
+// pair of a TMEM word's four scale bytes to use, bits 29-30 (A) and 4-5 (B).
+__device__ __forceinline__ uint32_t idesc_mxf4(int N, uint32_t pair) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) | ((pair * 2) << 29) |
+         ((pair * 2) << 4);
+}
+
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// 512 bytes of scales to four TMEM columns, the 32 lanes' words in all four
+// lane quarters.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+struct Shared {
+  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], done;
+  uint32_t tmem, abort, never;
+  int tiles;                          // token tiles
+  int first[kMxMaxExperts + 1];       // first token tile of each expert
+};
+
+// Rows of expert e, with offsets outside [0, R] or descending read as none.
+__device__ __forceinline__ int64_t segment(const MxProduct& p, int e, int64_t* start) {
+  const int64_t a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
+  *start = a;
+  return a < 0 || b > p.rows || b < a ? 0 : b - a;
+}
+
+__device__ bool tile_at(const MxProduct& p, const Shared& sh, int t, Tile& out) {
+  const int nb = p.N / kM;
+  const int tt = t / nb;
+  int lo = 0, hi = p.E - 1;  // the expert whose tiles hold tt
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sh.first[mid] <= tt) lo = mid; else hi = mid - 1;
+  }
+  int64_t start;
+  const int64_t rows = segment(p, lo, &start);
+  const int64_t skip = (int64_t)(tt - sh.first[lo]) * kTok;
+  out.e = lo;
+  out.nb = t - tt * nb;
+  out.row0 = start + skip;
+  out.rows = (int)min((int64_t)kTok, rows - skip);
+  return out.rows > 0;
+}
+
+__device__ __forceinline__ int padded(int rows) { return (rows + 15) & ~15; }
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    mx_product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA16,
+                      const __grid_constant__ CUtensorMap tmA64, const __grid_constant__ MxProduct p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  uint8_t* stage0 = align_1024(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&sh.full[s], 1 + 128);
+      ptx::mbar_init(&sh.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&sh.tfull[b], 1);
+      ptx::mbar_init(&sh.tempty[b], 128);
+    }
+    ptx::mbar_init(&sh.done, 1);
+    sh.abort = 0u;
+    sh.never = 0u;
+    ptx::fence_barrier_init();
+    ptx::fence_proxy_async();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(&sh.tmem, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  grid_dependency_wait();  // offsets and codes come from earlier kernels
+  // token tiles of each expert, then their running sum
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    int64_t start;
+    sh.first[e] = (int)((segment(p, e, &start) + kTok - 1) / kTok);
+    if (blockIdx.x == 0) {
+      const int64_t b = __ldg(p.offsets + e + 1);
+      if (start < 0 || b > p.rows || b < start) atomicOr(p.status, kStatusBounds);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int base = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int n = e0 + lane < p.E ? sh.first[e0 + lane] : 0;
+      int sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (e0 + lane < p.E) sh.first[e0 + lane] = base + sum - n;
+      base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) sh.tiles = base;
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  volatile uint32_t* abort = &sh.abort;
+  const int total = sh.tiles * (p.N / kM);
+  const int nk = (p.K + kK - 1) / kK;
+
+  if (warp == 8) {
+    // ------------------------------------------------ producer
+    if (lane == 0) {
+      const uint64_t pol_w = ptx::policy_evict_first(), pol_t = ptx::policy_evict_normal();
+      int kg = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+        Tile ti;
+        if (!tile_at(p, sh, t, ti)) continue;
+        const int wrow = ti.e * p.N + ti.nb * kM;
+        const bool small = ti.rows <= 48;  // boxes of 16 rows, else of 64
+        const int boxes = small ? (ti.rows + 15) / 16 : (ti.rows + 63) / 64;
+        const uint32_t box_bytes = (small ? 16 : 64) * kK / 2;
+        for (int kb = 0; kb < nk; ++kb, ++kg) {
+          const int s = kg % kStages;
+          if (!ptx::wait_bounded(&sh.empty[s], ((kg / kStages) & 1) ^ 1, abort)) {
+            raise_status(p.status, abort, kStatusTimeout);
+            ok = false;
+            break;
+          }
+          uint8_t* st = stage0 + s * kStageBytes;
+          ptx::mbar_arrive_expect_tx(&sh.full[s], kWBytes + boxes * box_bytes);
+          ptx::tma_load_2d(st, &tmW, &sh.full[s], kb * (kK / 2), wrow, pol_w);
+          for (int b = 0; b < boxes; ++b)
+            ptx::tma_load_2d(st + kWBytes + b * box_bytes, small ? &tmA16 : &tmA64, &sh.full[s], kb * (kK / 2),
+                             (int)ti.row0 + b * (small ? 16 : 64), pol_t);
+        }
+      }
+      // every issued copy must land before the CTA may exit
+      for (int j = (kg > kStages ? kg - kStages : 0); j < kg; ++j)
+        if (!ptx::wait_bounded(&sh.full[j % kStages], (j / kStages) & 1, &sh.never))
+          raise_status(p.status, abort, kStatusTimeout);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------ MMA
+    if (lane == 0) {
+      int kg = 0, use = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+        Tile ti;
+        if (!tile_at(p, sh, t, ti)) continue;
+        const int b = use & 1;
+        if (!ptx::wait_bounded(&sh.tempty[b], ((use >> 1) & 1) ^ 1, abort)) {
+          raise_status(p.status, abort, kStatusTimeout);
+          break;
+        }
+        ptx::tc_fence_after();
+        const int N = padded(ti.rows);
+        const uint32_t d = tmem + b * kTok;
+        for (int kb = 0; kb < nk; ++kb, ++kg) {
+          const int s = kg % kStages;
+          if (!ptx::wait_bounded(&sh.full[s], (kg / kStages) & 1, abort)) {
+            raise_status(p.status, abort, kStatusTimeout);
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t w0 = ptx::smem_u32(stage0 + s * kStageBytes);
+          const uint32_t t0 = w0 + kWBytes, sw0 = t0 + kTBytes, st0 = sw0 + kSfW;
+          const uint32_t sf = tmem + 2 * kTok + s * kSfCols;
+          const int halves = p.K - kb * kK > kK / 2 ? 2 : 1;  // 128-step halves that hold data
+          for (int h = 0; h < halves; ++h) {
+            copy_scales(sf + 4 * h, ptx::sdesc(sw0 + 512 * h, 16, 128, 0));
+            copy_scales(sf + 8 + 8 * h, ptx::sdesc(st0 + 1024 * h, 16, 128, 0));
+            if (N > 128) copy_scales(sf + 12 + 8 * h, ptx::sdesc(st0 + 1024 * h + 512, 16, 128, 0));
+          }
+          for (int kk = 0; kk < 2 * halves; ++kk)
+            mma_mxf4(d, ptx::sdesc_sw128(w0 + 32 * kk, 16, 1024), ptx::sdesc_sw128(t0 + 32 * kk, 16, 1024),
+                     idesc_mxf4(N, kk & 1), sf + 4 * (kk >> 1), sf + 8 + 8 * (kk >> 1), (kb | kk) != 0 ? 1u : 0u);
+          ptx::mma_commit(&sh.empty[s]);
+        }
+        if (!ok) break;
+        ptx::mma_commit(&sh.tfull[b]);
+        ++use;
+      }
+      ptx::mma_commit(&sh.done);
+      if (!ptx::wait_bounded(&sh.done, 0, &sh.never)) raise_status(p.status, abort, kStatusTimeout);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------ scales
+    // Thread r takes row r of the weights and rows r and r + 128 of the
+    // tokens.  Words of four scales; a group of four stages is read while the
+    // one before it is handed over, so a load has a group's time to arrive.
+    constexpr int kG = 4;
+    const int r = threadIdx.x - 128;
+    const uint32_t at = (uint32_t)(r & 31) * 16 + (uint32_t)(r >> 5) * 4;
+    const int words = p.K / 128;  // of a row
+    int kg = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      Tile ti;
+      if (!tile_at(p, sh, t, ti)) continue;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(p.w_scales) +
+                          ((int64_t)ti.e * p.N + ti.nb * kM + r) * words;
+      const uint32_t* a = reinterpret_cast<const uint32_t*>(p.a_scales) + (ti.row0 + r) * words;
+      const uint32_t* a2 = a + 128 * (int64_t)words;
+      const bool in = r < ti.rows, in2 = r + 128 < ti.rows;
+      uint32_t q[kG][2][3];
+      auto fetch = [&](int kb0) {
+#pragma unroll
+        for (int i = 0; i < kG; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int k = (kb0 + i) * 2 + h;
+            const bool have = k < words;
+            q[i][h][0] = have ? __ldg(w + k) : kOne4;
+            q[i][h][1] = have && in ? __ldg(a + k) : kOne4;
+            q[i][h][2] = have && in2 ? __ldg(a2 + k) : kOne4;
+          }
+      };
+      fetch(0);
+      for (int kb0 = 0; ok && kb0 < nk; kb0 += kG) {
+        uint32_t now[kG][2][3];
+#pragma unroll
+        for (int i = 0; i < kG; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 3; ++j) now[i][h][j] = q[i][h][j];
+        if (kb0 + kG < nk) fetch(kb0 + kG);
+#pragma unroll
+        for (int i = 0; i < kG; ++i) {
+          if (ok && kb0 + i < nk) {
+            const int s = kg % kStages;
+            if (!ptx::wait_bounded(&sh.empty[s], ((kg / kStages) & 1) ^ 1, abort)) {
+              raise_status(p.status, abort, kStatusTimeout);
+              ok = false;
+            } else {
+              uint8_t* sw = stage0 + s * kStageBytes + kWBytes + kTBytes;
+              uint8_t* st = sw + kSfW;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                *reinterpret_cast<uint32_t*>(sw + 512 * h + at) = now[i][h][0];
+                *reinterpret_cast<uint32_t*>(st + 1024 * h + at) = now[i][h][1];
+                *reinterpret_cast<uint32_t*>(st + 1024 * h + 512 + at) = now[i][h][2];
+              }
+              ptx::fence_proxy_async();
+              ptx::mbar_arrive(&sh.full[s]);
+              ++kg;
+            }
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------ epilogue
+    int use = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+      Tile ti;
+      if (!tile_at(p, sh, t, ti)) continue;
+      const int b = use & 1;
+      if (!ptx::wait_bounded(&sh.tfull[b], (use >> 1) & 1, abort)) {
+        raise_status(p.status, abort, kStatusTimeout);
+        break;
+      }
+      ptx::tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(warp * 32) << 16) + b * kTok;
+      const int64_t col = ti.nb * kM + warp * 32 + lane;
+      for (int c0 = 0; c0 < ti.rows; c0 += 32) {
+        uint32_t v[32];
+        ptx::tmem_ld32(acc + c0, v);
+        ptx::tmem_ld_wait(v);
+        if (c0 + 32 >= ti.rows) {
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&sh.tempty[b]);
+        }
+        const int n = ti.rows - c0;
+        const int64_t to = (ti.row0 + c0) * (int64_t)p.N + col;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (j < n) {
+            if (BF16)
+              static_cast<uint16_t*>(p.Y)[to + j * (int64_t)p.N] =
+                  (uint16_t)ptx::pack_bf16x2(__uint_as_float(v[j]), 0.0f);
+            else
+              static_cast<float*>(p.Y)[to + j * (int64_t)p.N] = __uint_as_float(v[j]);
+          }
+        }
+      }
+      ++use;
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_mx_product(const CUtensorMap& tmW, const CUtensorMap& tmA16, const CUtensorMap& tmA64,
+                              const MxProduct& p, bool y_bf16, int sms, cudaStream_t stream) {
+  auto kernel = y_bf16 ? mx_product_kernel<true> : mx_product_kernel<false>;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (err != cudaSuccess) return err;
+  return launch_chained(kernel, dim3(sms), dim3(kThreads), kSmem, stream, tmW, tmA16, tmA64, p);
+}
+
+}  // namespace moe

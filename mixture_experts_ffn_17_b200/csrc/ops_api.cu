@@ -1,0 +1,342 @@
+// ops_api.cu -- host side of the few-token layer, the MXFP4 operators and the
+// gradient norm: argument checks, workspace layouts and launch sequences.
+#include <algorithm>
+#include <cstdint>
+
+#include "api_internal.h"
+#include "few.h"
+#include "grad.h"
+#include "moe.h"
+#include "moe_internal.h"
+#include "mx.h"
+
+namespace moe {
+namespace {
+
+constexpr size_t kAlign = 256;
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+bool ws_ok(const void* ws, size_t bytes, size_t need) { return ws && bytes >= need && aligned(ws, kAlign); }
+
+template <typename P>
+P* at(void* ws, size_t off) {
+  return reinterpret_cast<P*>(static_cast<uint8_t*>(ws) + off);
+}
+
+#define MOE_CUDA(call)                              \
+  do {                                              \
+    if ((call) != cudaSuccess) return MOE_ERR_CUDA; \
+  } while (0)
+
+// ------------------------------------------------------------ few tokens
+struct FewLayout {
+  size_t logits, up_r, up_s, dn_r, dn_s, h, total;
+  int ld_h;
+};
+
+moe_status check_few(const moe_shape* shape) {
+  if (!shape) return MOE_ERR_INVALID_ARG;
+  moe_shape s = *shape;
+  if (s.w_dtype == MOE_MXFP4) s.w_dtype = MOE_BF16;  // the other limits are the same
+  const moe_status v = check_shape(&s);
+  if (v != MOE_OK) return v;
+  if (s.T > kFewMaxTokens) return MOE_ERR_UNSUPPORTED;
+  // the lines of work units times the CTAs have to fit 32 bits
+  const int64_t experts = std::max<int64_t>(1, std::min<int64_t>(s.E, s.T * s.k));
+  const int64_t wide = std::max(s.inter, s.shared_inter);
+  const int64_t units = experts * 2 * (wide / kFewCols) * (s.d / kFewStep);
+  if (units * (kFewMaxSms + 1) >= (int64_t)1 << 32) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+FewLayout few_layout(const moe_shape& s) {
+  FewLayout L{};
+  const int64_t T = s.T, experts = std::min<int64_t>(s.E, T * s.k);
+  size_t off = kAlign;  // the status word and the barriers' counters
+  auto take = [&](size_t bytes) {
+    const size_t here = off;
+    off += (bytes + kAlign - 1) / kAlign * kAlign;
+    return here;
+  };
+  auto slots = [&](int64_t segs) { return (size_t)(segs + kFewMaxSms) * T * kFewCols * 4; };
+  L.ld_h = std::max(s.inter, s.shared_inter);
+  L.logits = take((size_t)T * s.E * 4);
+  L.up_r = take(slots(experts * 2 * (s.inter / kFewCols)));
+  L.up_s = take(s.shared_inter ? slots(2 * (s.shared_inter / kFewCols)) : 0);
+  L.dn_r = take(slots(experts * (s.d / kFewCols)));
+  L.dn_s = take(s.shared_inter ? slots(s.d / kFewCols) : 0);
+  L.h = take((size_t)(T * s.k + T) * 3 * L.ld_h * 2);
+  L.total = off;
+  return L;
+}
+
+// ------------------------------------------------------------ gradients
+// Ranges that a clipping call writes must be disjoint from all others.
+bool ranges_overlap(const moe_tensor* t, int n) {
+  struct Range {
+    uintptr_t begin, end;
+    bool write;
+  };
+  Range r[2 * kGradMaxTensors];
+  int m = 0;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].count == 0) continue;
+    const uintptr_t bytes = (uintptr_t)t[i].count * (t[i].dtype == MOE_BF16 ? 2 : 4);
+    const uintptr_t src = reinterpret_cast<uintptr_t>(t[i].data);
+    const uintptr_t dst = t[i].out ? reinterpret_cast<uintptr_t>(t[i].out) : src;
+    r[m++] = Range{dst, dst + bytes, true};
+    if (dst != src) r[m++] = Range{src, src + bytes, false};
+  }
+  std::sort(r, r + m, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t written = 0, used = 0;  // furthest ends so far
+  for (int i = 0; i < m; ++i) {
+    if (r[i].begin < (r[i].write ? used : written)) return true;
+    used = std::max(used, r[i].end);
+    if (r[i].write) written = std::max(written, r[i].end);
+  }
+  return false;
+}
+
+moe_status check_tensors(const moe_tensor* t, int n, bool clip) {
+  if (n < 0 || (n > 0 && !t)) return MOE_ERR_INVALID_ARG;
+  if (n > kGradMaxTensors) return MOE_ERR_UNSUPPORTED;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].count < 0 || (t[i].dtype != MOE_F32 && t[i].dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+    if (t[i].count > (int64_t)1 << 40) return MOE_ERR_UNSUPPORTED;
+    if (t[i].count == 0) continue;
+    const uintptr_t size = t[i].dtype == MOE_BF16 ? 2 : 4;
+    if (!t[i].data || !aligned(t[i].data, size)) return MOE_ERR_INVALID_ARG;
+    if (clip && t[i].out && !aligned(t[i].out, size)) return MOE_ERR_INVALID_ARG;
+  }
+  return clip && ranges_overlap(t, n) ? MOE_ERR_INVALID_ARG : MOE_OK;
+}
+
+int grad_batches(int n) { return std::max(1, (n + kGradBatch - 1) / kGradBatch); }
+
+size_t grad_ws_bytes(int n) { return (size_t)grad_batches(n) * kGradMaxSms * kGradCtasPerSm * sizeof(double); }
+
+bool fill_batch(GradBatch& b, const moe_tensor* t, int n, int first) {
+  b.n = std::min(kGradBatch, n - first);
+  int64_t chunks = 0;
+  for (int i = 0; i < b.n; ++i) {
+    const moe_tensor& x = t[first + i];
+    b.src[i] = x.data;
+    b.dst[i] = x.out ? x.out : x.data;
+    b.count[i] = x.count;
+    b.bf16[i] = x.dtype == MOE_BF16;
+    b.first[i] = (uint32_t)chunks;
+    chunks += grad_chunks(x.count, x.dtype == MOE_BF16);
+    if (chunks >= (int64_t)1 << 31) return false;
+  }
+  b.first[b.n] = (uint32_t)chunks;
+  return true;
+}
+
+// The norm's partial sums of every batch; *parts receives their number.
+moe_status grad_squares(const moe_tensor* t, int n, double* part, int sms, int* parts, cudaStream_t st) {
+  *parts = 0;
+  for (int b = 0; b < grad_batches(n); ++b) {
+    GradBatch batch;
+    if (!fill_batch(batch, t, n, b * kGradBatch)) return MOE_ERR_UNSUPPORTED;
+    const int grid = grad_grid(batch.first[batch.n], sms);
+    MOE_CUDA(launch_grad_squares(batch, part + *parts, grid, st));
+    *parts += grid;
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_few_workspace_size(const moe_shape* shape) {
+  if (check_few(shape) != MOE_OK) return 0;
+  return few_layout(*shape).total;
+}
+
+moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg, const float* bias, const void* W1,
+                           const void* W3, const void* W2, const void* s1, const void* s3, const void* s2,
+                           const void* W1s, const void* W3s, const void* W2s, void* y, int32_t* topk_idx_out,
+                           float* topk_w_out, int32_t* counts_out, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status v = check_few(shape);
+  if (v != MOE_OK) return v;
+  const moe_shape& s = *shape;
+  if (!x || !Wg || !W1 || !W3 || !W2 || !y) return MOE_ERR_INVALID_ARG;
+  if (s.shared_inter > 0 && (!W1s || !W3s || !W2s)) return MOE_ERR_INVALID_ARG;
+  if (s.w_dtype != MOE_BF16 && (!s1 || !s3 || !s2)) return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {x, Wg, bias, W1, W3, W2, s1, s3, s2, W1s, W3s, W2s, y, topk_idx_out, topk_w_out, counts_out};
+  for (const void* p : ptrs)
+    if (!aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+  const FewLayout L = few_layout(s);
+  if (!ws_ok(ws, ws_bytes, L.total)) return MOE_ERR_WORKSPACE;
+  if (s.T == 0) return MOE_OK;
+  FewParams p{};
+  p.T = (int)s.T;
+  p.d = s.d;
+  p.E = s.E;
+  p.k = s.k;
+  p.I = s.inter;
+  p.S = s.shared_inter;
+  p.route = s.route;
+  p.n_group = s.n_group;
+  p.topk_group = s.topk_group;
+  p.group_topn = s.group_topn;
+  p.route_scale = s.route_scale;
+  p.y_bf16 = s.y_dtype == MOE_BF16;
+  auto bytes = [](const void* q) { return static_cast<const uint8_t*>(q); };
+  p.x = static_cast<const uint16_t*>(x);
+  p.Wg = static_cast<const uint16_t*>(Wg);
+  p.bias = s.route == MOE_ROUTE_SIGMOID_GROUP ? bias : nullptr;
+  p.W1 = bytes(W1);
+  p.W3 = bytes(W3);
+  p.W2 = bytes(W2);
+  p.s1 = bytes(s1);
+  p.s3 = bytes(s3);
+  p.s2 = bytes(s2);
+  p.W1s = bytes(W1s);
+  p.W3s = bytes(W3s);
+  p.W2s = bytes(W2s);
+  p.y = y;
+  p.idx_out = topk_idx_out;
+  p.w_out = topk_w_out;
+  p.counts_out = counts_out;
+  p.status = at<uint32_t>(ws, 0);
+  p.bar = at<uint32_t>(ws, 64);
+  p.logits = at<float>(ws, L.logits);
+  p.up_r = at<float>(ws, L.up_r);
+  p.up_s = at<float>(ws, L.up_s);
+  p.dn_r = at<float>(ws, L.dn_r);
+  p.dn_s = at<float>(ws, L.dn_s);
+  p.h = at<uint16_t>(ws, L.h);
+  p.ld_h = L.ld_h;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MOE_CUDA(cudaMemsetAsync(ws, 0, kAlign, st));
+  MOE_CUDA(launch_few(p, s.w_dtype == MOE_BF16 ? kFewBf16 : s.w_dtype == MOE_E4M3 ? kFewE4m3 : kFewMxfp4,
+                      device_sms(), st));
+  return MOE_OK;
+}
+
+moe_status moe_mx_quantise(const void* src, const void* up, int src_dtype, int64_t rows, int cols, int64_t ld,
+                           void* codes, void* scales, void* stream) {
+  if (rows < 0 || cols <= 0 || ld < cols || (src_dtype != MOE_F32 && src_dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+  if (cols % kMxBlock != 0) return MOE_ERR_UNSUPPORTED;
+  if (rows > ((int64_t)1 << 56) / ld) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  const uintptr_t size = src_dtype == MOE_BF16 ? 2 : 4;
+  if (!src || !codes || !scales || !aligned(src, size) || !aligned(up, size) || !aligned(codes, 16) ||
+      !aligned(scales, 16))
+    return MOE_ERR_INVALID_ARG;
+  MOE_CUDA(launch_mx_quantise(src, up, src_dtype == MOE_BF16, rows, cols, ld, static_cast<uint8_t*>(codes),
+                              static_cast<uint8_t*>(scales), device_sms(), static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_mx_quantise_weights(const void* W, int src_dtype, int E, int K, int N, void* codes, void* scales,
+                                   void* stream) {
+  if (E < 0 || K <= 0 || N <= 0 || (src_dtype != MOE_F32 && src_dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+  if (K % kMxBlock != 0 || E > 65535 || K > (1 << 23)) return MOE_ERR_UNSUPPORTED;
+  if (E == 0) return MOE_OK;
+  if (!W || !codes || !scales || !aligned(W, src_dtype == MOE_BF16 ? 2 : 4) || !aligned(codes, 16) ||
+      !aligned(scales, 16))
+    return MOE_ERR_INVALID_ARG;
+  MOE_CUDA(launch_mx_quantise_weights(W, src_dtype == MOE_BF16, E, K, N, static_cast<uint8_t*>(codes),
+                                      static_cast<uint8_t*>(scales), static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_mx_dequantise(const void* codes, const void* scales, int64_t rows, int cols, void* dst, int dst_dtype,
+                             void* stream) {
+  if (rows < 0 || cols <= 0 || (dst_dtype != MOE_F32 && dst_dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+  if (cols % kMxBlock != 0 || rows > ((int64_t)1 << 56) / cols) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!codes || !scales || !dst || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(dst, 16))
+    return MOE_ERR_INVALID_ARG;
+  MOE_CUDA(launch_mx_dequantise(static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), rows, cols,
+                                dst, dst_dtype == MOE_BF16, device_sms(), static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+size_t moe_mx_product_workspace_size(int64_t rows, int E) {
+  if (rows < 0 || rows >= (int64_t)1 << 31 || E <= 0 || E > kMxMaxExperts) return 0;
+  return kAlign;
+}
+
+moe_status moe_mx_grouped_product(int64_t rows, int E, int K, int N, const void* A, const void* A_scales,
+                                  const int32_t* offsets, const void* W, const void* W_scales, void* Y, int y_dtype,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  if (rows < 0 || E <= 0 || K <= 0 || N <= 0 || (y_dtype != MOE_F32 && y_dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+  if (K % 128 != 0 || N % 128 != 0 || E > kMxMaxExperts || rows >= (int64_t)1 << 31 ||
+      (int64_t)E * N >= (int64_t)1 << 31 ||
+      (rows / kMxTileTokens + E) * (N / 128) >= (int64_t)1 << 31)
+    return MOE_ERR_UNSUPPORTED;
+  const void* ptrs[] = {A, A_scales, offsets, W, W_scales, Y};
+  for (const void* p : ptrs)
+    if (!aligned(p, 16) || (rows > 0 && !p)) return MOE_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, moe_mx_product_workspace_size(rows, E))) return MOE_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MOE_CUDA(cudaMemsetAsync(ws, 0, 4, st));
+  if (rows == 0) return MOE_OK;
+  CUtensorMap w, a16, a64;
+  if (!map_bytes(&w, W, K / 2, (uint64_t)E * N, 128) || !map_bytes(&a16, A, K / 2, rows, 16) ||
+      !map_bytes(&a64, A, K / 2, rows, 64))
+    return MOE_ERR_CUDA;
+  MxProduct p{};
+  p.rows = rows;
+  p.E = E;
+  p.K = K;
+  p.N = N;
+  p.a_scales = static_cast<const uint8_t*>(A_scales);
+  p.w_scales = static_cast<const uint8_t*>(W_scales);
+  p.offsets = offsets;
+  p.Y = Y;
+  p.status = at<uint32_t>(ws, 0);
+  MOE_CUDA(launch_mx_product(w, a16, a64, p, y_dtype == MOE_BF16, device_sms(), st));
+  return MOE_OK;
+}
+
+size_t moe_grad_workspace_size(int n) {
+  if (n < 0 || n > kGradMaxTensors) return 0;
+  return grad_ws_bytes(n);
+}
+
+moe_status moe_grad_norm(const moe_tensor* tensors, int n, float* norm_out, void* ws, size_t ws_bytes, void* stream) {
+  const moe_status v = check_tensors(tensors, n, false);
+  if (v != MOE_OK) return v;
+  if (!norm_out || !aligned(norm_out, 4)) return MOE_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, grad_ws_bytes(n))) return MOE_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int parts = 0;
+  double* part = at<double>(ws, 0);
+  const moe_status r = grad_squares(tensors, n, part, std::min(device_sms(), kGradMaxSms), &parts, st);
+  if (r != MOE_OK) return r;
+  MOE_CUDA(launch_grad_norm(part, parts, norm_out, st));
+  return MOE_OK;
+}
+
+moe_status moe_grad_clip(const moe_tensor* tensors, int n, float max_norm, float* norm_out, void* ws, size_t ws_bytes,
+                         void* stream) {
+  const moe_status v = check_tensors(tensors, n, true);
+  if (v != MOE_OK) return v;
+  if (!(max_norm >= 0.0f) || !aligned(norm_out, 4)) return MOE_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, grad_ws_bytes(n))) return MOE_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int parts = 0;
+  double* part = at<double>(ws, 0);
+  const int sms = std::min(device_sms(), kGradMaxSms);
+  const moe_status r = grad_squares(tensors, n, part, sms, &parts, st);
+  if (r != MOE_OK) return r;
+  // the last batch first: the norm read it last
+  for (int b = grad_batches(n) - 1; b >= 0; --b) {
+    GradBatch batch;
+    fill_batch(batch, tensors, n, b * kGradBatch);
+    MOE_CUDA(launch_grad_scale(batch, part, parts, max_norm, b == 0 ? norm_out : nullptr,
+                               grad_grid(batch.first[batch.n], sms), st));
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"
