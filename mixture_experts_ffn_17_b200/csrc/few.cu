@@ -7,35 +7,39 @@
 // With at most 16 tokens an expert sees one or two rows, so the layer is a
 // stream of the chosen experts' weights through the SMs (bound by HBM: 3 d I
 // weights an expert against 2 T operations a weight) and everything else is
-// latency.  One CTA per SM walks all steps, with grid barriers between them:
-//   0  logits of a share of the experts; then, before waiting, this CTA's
-//      share of the shared expert's up projections, which need no routing
-//   1  top-k in every CTA (redundantly), the list of chosen experts and their
-//      rows; this CTA's share of the routed up projections
-//   2  h = silu(g) * u from the partial sums, as three bf16 terms
-//   3  this CTA's share of the down projections
-//   4  y from the partial sums
+// latency to be kept out of the stream's way.  One CTA per SM, three roles:
+//   consumers (16 warps)  logits of a share of the experts, then the products
+//                         and the two joins, with grid barriers between them;
+//   producer (1 warp)     fills a ring of stages with weight tiles (TMA) and the
+//                         matching columns of activations (bulk copies), ahead
+//                         of the consumers and across the ends of pieces and
+//                         phases: the shared expert's up projections need no
+//                         routing and stream while it is found, and the first
+//                         tiles of the down projections are in the ring before
+//                         the barriers that the activations wait for;
+//   router (4 warps)      waits for all logits, finds the top-k (in every CTA)
+//                         and the list of chosen experts and their rows.
 //
 // Split of the work.  A segment is 128 output columns of one matrix of one
-// expert, a unit 128 steps of its contraction.  The units of all segments lie
-// on one line that is cut into equal shares, one a CTA, so every SM streams the
-// same number of bytes whatever the number of experts; a share's part of one
-// segment is a piece, and its sums go to slot (segment + CTA) of a buffer
-// (unique: along the line each piece raises one of the two by one).  Who
+// expert, a unit the part of its contraction that one stage holds (16 KB of
+// weights: 64 steps of bf16, 128 of e4m3, 256 of MXFP4).  The units of all
+// segments lie on one line that is cut into equal shares, one a CTA, so every
+// SM streams the same number of bytes whatever the number of experts; a share's
+// part of one segment is a piece, and its sums go to slot (segment + CTA) of a
+// buffer (unique: along the line each piece raises one of the two by one).  Who
 // consumes a segment adds its pieces in CTA order: no atomics, and equal inputs
 // give equal bits.
 //
 // Arithmetic: mma.sync m16n8k16 with the weights as the A operand (16 output
-// columns by 16 steps) taken from global memory straight into registers, and
-// the tokens as the 8 columns of B.  The order of the 16 steps inside an MMA is
-// free as long as A and B agree, so lane (g, c) takes steps 4c..4c+3 of columns
-// 8g..8g+7: one wide load a step, and pairs of steps are joined by byte
-// permutes.  (tcgen05 would need the weights in shared memory and at least 8
-// more columns; the tensor work here is a few percent either way.)  e4m3 and
-// MXFP4 codes become bf16 exactly: their exponent and mantissa bits are moved
-// to bf16's and the exponent's offset is made up by an exact multiplication
-// with a power of two.  x is bf16; h is fp32 and goes in as three bf16 terms
-// (8 bits each: 24 in all), so its rounding costs nothing against fp32.
+// columns by 16 steps, ldmatrix from the stage) and the activations as B's
+// columns, 8 at a time.  (tcgen05 would pad the columns to 16 and could not take
+// these codes unconverted; the tensor pipe is idle either way.)  Consumer warp w
+// takes columns 16 (w % 8) of a tile and one half of its steps (w / 8).  e4m3
+// and MXFP4 codes become bf16 exactly: their exponent and mantissa bits are
+// moved to bf16's and the exponent's offset is made up by an exact
+// multiplication with a power of two.  x is bf16; h is fp32 and goes in as three
+// bf16 terms (8 bits each: 24 in all), so its rounding costs nothing against
+// fp32.
 #include <algorithm>
 #include <cstdint>
 
@@ -45,12 +49,32 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 16;  // consumers
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRouterWarps = 4;
+constexpr int kAllThreads = kThreads + 32 + 32 * kRouterWarps;
 constexpr int kMaxNT = 3;       // 8-column B tiles of one pass
-constexpr int kRedPitch = 129;  // floats of one B column in the CTA's reduction buffer
+constexpr int kMaxCols = 8 * kMaxNT;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxRows = kFewMaxTokens * 32;  // T * k
+constexpr uint32_t kTileBytes = 16384;
+
+// Steps of the contraction that a stage holds, the distance of its B columns in
+// bytes (2 steps + a pad that keeps their reads off each other's banks), and the
+// stages that fit beside the rest.
+template <int WT>
+struct Unit {
+  static constexpr int kSteps = few_unit_steps(WT);
+  static constexpr int kPitch = WT == kFewMxfp4 ? 2 * kSteps + 64 : 2 * kSteps + 16;
+  static constexpr uint32_t kBytes = (kTileBytes + kMaxCols * kPitch + 1023) / 1024 * 1024;
+  static constexpr int kStages = WT == kFewBf16 ? 8 : WT == kFewE4m3 ? 7 : 5;
+};
+
+// Router warps that choose experts at the same time (a key per expert each).
+__host__ __device__ constexpr int choosers(int E) { return E <= 512 ? kRouterWarps : kRouterWarps / 2; }
+
+constexpr int kRedPitch = 17;  // floats of one B column of a warp pair's 16 output columns
+constexpr int kRedFloats = 2 * kMaxCols * kRedPitch;  // of a pair of warps
 
 struct Lists {  // what the routing leaves in shared memory
   int32_t idx[kMaxRows];      // [T][k]
@@ -62,35 +86,50 @@ struct Lists {  // what the routing leaves in shared memory
   int16_t seg_of[kMaxExperts];  // place of an expert among the distinct ones
   int32_t counts[kMaxExperts];
   int n;                      // distinct experts
-  uint32_t abort;
 };
 
+struct Control {
+  uint64_t full[9], empty[9];
+  uint64_t routed;  // the lists are there
+  uint64_t ready;   // h is there, in all CTAs
+  uint32_t abort, never;
+};
+
+__device__ __forceinline__ void consumer_sync() { ptx::named_barrier(9, kThreads); }
+__device__ __forceinline__ void router_sync() { ptx::named_barrier(10, 32 * kRouterWarps); }
+
 // ------------------------------------------------------------ grid barrier
+// The consumers' writes so far are visible to who waits.
 __device__ __forceinline__ void grid_arrive(uint32_t* bar) {
-  __syncthreads();
+  consumer_sync();
   if (threadIdx.x == 0) {
     __threadfence();
     atomicAdd(bar, 1u);
   }
 }
 
-__device__ bool grid_wait(uint32_t* bar, uint32_t* status, uint32_t* abort) {
-  if (threadIdx.x == 0) {
-    const uint64_t t0 = ptx::globaltimer();
-    uint32_t n = 0;
-    uint32_t seen;
-    while (true) {
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(bar) : "memory");
-      if (seen >= gridDim.x) break;
-      if ((++n & 63u) == 0 && ptx::globaltimer() - t0 > kWaitLimitNs) {
-        atomicOr(status, kStatusTimeout);
-        *abort = 1u;
-        break;
+// One thread's wait for all CTAs' arrivals.
+__device__ __forceinline__ bool grid_poll(const uint32_t* bar, uint32_t* status, volatile uint32_t* abort) {
+  const uint64_t t0 = ptx::globaltimer();
+  uint32_t n = 0, seen;
+  while (true) {
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(bar) : "memory");
+    if (seen >= gridDim.x) break;
+    if ((++n & 63u) == 0) {
+      if (*abort) return false;
+      if (ptx::globaltimer() - t0 > kWaitLimitNs) {
+        raise_status(status, abort, kStatusTimeout);
+        return false;
       }
     }
-    __threadfence();
   }
-  __syncthreads();
+  __threadfence();
+  return true;
+}
+
+__device__ bool grid_wait(const uint32_t* bar, uint32_t* status, volatile uint32_t* abort) {
+  if (threadIdx.x == 0) grid_poll(bar, status, abort);
+  consumer_sync();
   return *abort == 0;
 }
 
@@ -121,7 +160,7 @@ __device__ __forceinline__ float4 sum_pieces(const float* buf, const Line& L, ui
   return a;
 }
 
-// ------------------------------------------------------------ matrix pieces
+// ------------------------------------------------------------ tiles and columns
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -130,24 +169,37 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void lds(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
-__device__ __forceinline__ uint4 load_stream(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
-}
-
-__device__ __forceinline__ uint2 load_stream8(const void* p) {
-  uint2 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-  return r;
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+               : "memory");
 }
 
 // Two e4m3 codes in bytes 1 and 3 to bf16x2: sign to bit 15, the seven other
@@ -173,290 +225,349 @@ __device__ __forceinline__ uint32_t mx_pair(uint32_t w, uint32_t scale) {
   return mul_bf16x2((s & 0x80008000u) | (m & 0x01c001c0u), scale);
 }
 
-// The B operand's columns of this lane: for column tile j, lane (g, c) reads
-// column 8 j + g; null where there is none.
-struct Columns {
-  const uint16_t* p[kMaxNT];
-};
-
-// This warp's part of a piece for weights [K, N] (bf16 or e4m3): units of 128
-// rows by 128 columns; the warp takes 64 of the columns and 16 of the rows.
-template <int WT, int NT>
-__device__ __forceinline__ void rows_piece(const uint8_t* W, int64_t N, int col0, int step0, int step1,
-                                           const float* scale, int64_t scale_ld, const Columns& B,
-                                           float (&acc)[4][NT][4]) {
-  constexpr int U = NT == 1 ? 4 : 2;  // units in flight, as registers allow
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, c = lane & 3;
-  const int k_in = (warp >> 1) * 16 + 4 * c;
-  const int64_t size = WT == kFewBf16 ? 2 : 1;
-  const uint8_t* base = W + ((int64_t)k_in * N + col0 + (warp & 1) * 64 + 8 * g) * size;
-  for (int s0 = step0; s0 < step1; s0 += U) {
-    uint4 a4[WT == kFewBf16 ? U : 1][4];
-    uint2 a2[WT == kFewBf16 ? 1 : U][4];
-    uint2 b[U][NT];
-    float sc[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (s0 + u < step1) {
-        const uint8_t* p = base + (int64_t)(s0 + u) * kFewStep * N * size;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (WT == kFewBf16)
-            a4[u][r] = load_stream(p + r * N * size);
-          else
-            a2[u][r] = load_stream8(p + r * N * size);
-        }
-        if (WT == kFewE4m3) sc[u] = __ldg(scale + (s0 + u) * scale_ld);
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          b[u][j] = B.p[j] ? *reinterpret_cast<const uint2*>(B.p[j] + (s0 + u) * kFewStep + k_in) : make_uint2(0u, 0u);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (s0 + u < step1) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          uint32_t f[4];
-          if (WT == kFewBf16) {
-            const uint32_t w0 = (&a4[u][0].x)[t], w1 = (&a4[u][1].x)[t], w2 = (&a4[u][2].x)[t], w3 = (&a4[u][3].x)[t];
-            f[0] = __byte_perm(w0, w1, 0x5410);
-            f[1] = __byte_perm(w0, w1, 0x7632);
-            f[2] = __byte_perm(w2, w3, 0x5410);
-            f[3] = __byte_perm(w2, w3, 0x7632);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) mma(acc[t][j], f, b[u][j].x, b[u][j].y);
-          } else {
-            const uint32_t w0 = t < 2 ? a2[u][0].x : a2[u][0].y, w1 = t < 2 ? a2[u][1].x : a2[u][1].y;
-            const uint32_t w2 = t < 2 ? a2[u][2].x : a2[u][2].y, w3 = t < 2 ? a2[u][3].x : a2[u][3].y;
-            const uint32_t lo = (t & 1) ? 0x6020u : 0x4000u, hi = (t & 1) ? 0x7030u : 0x5010u;
-            f[0] = e4m3_pair(__byte_perm(w0, w1, lo));
-            f[1] = e4m3_pair(__byte_perm(w0, w1, hi));
-            f[2] = e4m3_pair(__byte_perm(w2, w3, lo));
-            f[3] = e4m3_pair(__byte_perm(w2, w3, hi));
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              mma(part, f, b[u][j].x, b[u][j].y);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[t][j][i] = fmaf(part[i], sc[u], acc[t][j][i]);
-            }
-          }
-        }
-      }
-    }
-  }
-}
-
-// The same for MXFP4 weights [N, K / 2]: the warp takes 16 of the 128 output
-// columns (rows of W) and every second unit; lane (g, c) reads scale block c
-// of the unit for columns g and g + 8.
+// One stage of a piece: this warp's sums over its half of the steps.
+// bf16: two boxes of 64 columns, [steps][64 columns].
 template <int NT>
-__device__ __forceinline__ void codes_piece(const uint8_t* W, const uint8_t* scales, int64_t K, int col0, int step0,
-                                            int step1, const Columns& B, float (&acc)[NT][4]) {
-  constexpr int U = NT == 1 ? 4 : 2;
+__device__ __forceinline__ void stage_bf16(uint32_t tile, uint32_t cols, float (&acc)[NT][4]) {
+  constexpr int P = Unit<kFewBf16>::kPitch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, c = lane & 3;
-  const int64_t n = col0 + (warp & 7) * 16 + g;
-  const uint8_t* base = W + n * (K / 2) + c * 16;
-  const uint8_t* sbase = scales + n * (K / 32) + c;
-  for (int s0 = step0 + (warp >> 3); s0 < step1; s0 += 2 * U) {
-    uint4 a[U][2];
-    uint32_t sc[U][2];
+  const int i = lane >> 3, r = lane & 7;
+  const int k0 = (warp >> 3) * 32;
+  uint32_t b[NT][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int s = s0 + 2 * u;
-      if (s < step1) {
+  for (int j = 0; j < NT; ++j) ldsm(b[j], cols + (8 * j + r) * P + (k0 + 8 * i) * 2);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          a[u][r] = load_stream(base + (int64_t)r * 8 * (K / 2) + (int64_t)s * (kFewStep / 2));
-          sc[u][r] = __ldg(sbase + (int64_t)r * 8 * (K / 32) + (int64_t)s * (kFewStep / 32));
+  for (int q = 0; q < 2; ++q) {
+    const int k = k0 + 16 * q + (i >> 1) * 8 + r;
+    const int chunk = (warp & 3) * 2 + (i & 1);
+    uint32_t a[4];
+    ldsm_t(a, tile + ((warp >> 2) & 1) * 8192 + k * 128 + ((chunk ^ (k & 7)) << 4));
+#pragma unroll
+    for (int j = 0; j < NT; ++j) mma(acc[j], a, b[j][2 * q], b[j][2 * q + 1]);
+  }
+}
+
+// e4m3: [steps][128 columns] codes; a 16-bit unit of ldmatrix is two columns of
+// one step, so a register holds columns 2g and 2g + 1 of steps 2c and 2c + 1.
+template <int NT>
+__device__ __forceinline__ void stage_e4m3(uint32_t tile, uint32_t cols, float scale, float (&acc)[NT][4]) {
+  constexpr int P = Unit<kFewE4m3>::kPitch;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i = lane >> 3, r = lane & 7;
+  float part[NT][4] = {};
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int k0 = (warp >> 3) * 64 + 32 * q;
+    const int k = k0 + 8 * i + r;
+    uint32_t w[4];
+    ldsm_t(w, tile + k * 128 + (((warp & 7) ^ (k & 7)) << 4));
+    uint32_t a0[4] = {e4m3_pair(w[0] << 8), e4m3_pair(w[0]), e4m3_pair(w[1] << 8), e4m3_pair(w[1])};
+    uint32_t a1[4] = {e4m3_pair(w[2] << 8), e4m3_pair(w[2]), e4m3_pair(w[3] << 8), e4m3_pair(w[3])};
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      uint32_t b[4];
+      ldsm(b, cols + (8 * j + r) * P + (k0 + 8 * i) * 2);
+      mma(part[j], a0, b[0], b[1]);
+      mma(part[j], a1, b[2], b[3]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(part[j][e], scale, acc[j][e]);
+}
+
+// MXFP4: [128 columns][steps / 2] codes; lane (g, c) holds the eight codes 8c of
+// a scale block for columns g and g + 8, whose scale bytes are in s[0], s[1].
+template <int NT>
+__device__ __forceinline__ void stage_mxfp4(uint32_t tile, uint32_t cols, const uint32_t (&s)[2], float (&acc)[NT][4]) {
+  constexpr int P = Unit<kFewMxfp4>::kPitch;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i = lane >> 3, r = lane & 7, g = lane >> 2, c = lane & 3;
+  const int half = warp >> 3;
+  const int n = (warp & 7) * 16 + (i & 1) * 8 + r;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {  // two scale blocks
+    uint32_t w[4];
+    const int chunk = half * 4 + 2 * p + (i >> 1);
+    ldsm(w, tile + n * 128 + ((chunk ^ (n & 7)) << 4));
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int blk = 2 * p + q;
+      // 2^(byte - 127 + 126) as bf16x2; a scale of 4 or more would leave
+      // bf16's range there and takes a second multiplication by 2^(byte - 128)
+      const uint32_t v0 = (s[0] >> (8 * blk)) & 255u, v1 = (s[1] >> (8 * blk)) & 255u;
+      const uint32_t m0 = (min(v0, 128u) + 126u) * 0x00800080u, m1 = (min(v1, 128u) + 126u) * 0x00800080u;
+      const uint32_t x = w[2 * q], y = w[2 * q + 1];
+      uint32_t a0[4] = {mx_pair<0>(x, m0), mx_pair<0>(y, m1), mx_pair<1>(x, m0), mx_pair<1>(y, m1)};
+      uint32_t a1[4] = {mx_pair<2>(x, m0), mx_pair<2>(y, m1), mx_pair<3>(x, m0), mx_pair<3>(y, m1)};
+      if (__any_sync(0xffffffffu, max(v0, v1) > 128u)) {
+        const uint32_t n0 = v0 == 255u ? 0x7fff7fffu : ((v0 > 128u ? v0 - 128u : 0u) + 127u) * 0x00800080u;
+        const uint32_t n1 = v1 == 255u ? 0x7fff7fffu : ((v1 > 128u ? v1 - 128u : 0u) + 127u) * 0x00800080u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          a0[e] = mul_bf16x2(a0[e], (e & 1) ? n1 : n0);
+          a1[e] = mul_bf16x2(a1[e], (e & 1) ? n1 : n0);
         }
       }
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int s = s0 + 2 * u;
-      if (s < step1) {
-        // 2^(byte - 127 + 126) as bf16x2; a scale of 4 or more would leave
-        // bf16's range there and takes a second multiplication by 2^(byte - 128)
-        uint32_t m[2], over = 0;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint32_t first = min(sc[u][r], 128u);
-          const uint32_t e = first + 126u;  // exponent field of 2^(first - 127 + 126)
-          m[r] = (e << 7) | (e << 23);
-          over |= sc[u][r] > 128u ? 1u : 0u;
-        }
-        const bool big = __any_sync(0xffffffffu, over != 0);
-        uint32_t m2[2] = {0x3f803f80u, 0x3f803f80u};
-        if (big) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint32_t v = sc[u][r];
-            const uint32_t e = v == 255u ? 0xffu : (v > 128u ? v - 128u : 0u) + 127u;
-            m2[r] = v == 255u ? 0x7fff7fffu : (e << 7) | (e << 23);
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t w0 = (&a[u][0].x)[q], w1 = (&a[u][1].x)[q];
-          uint32_t f0[4] = {mx_pair<0>(w0, m[0]), mx_pair<0>(w1, m[1]), mx_pair<1>(w0, m[0]), mx_pair<1>(w1, m[1])};
-          uint32_t f1[4] = {mx_pair<2>(w0, m[0]), mx_pair<2>(w1, m[1]), mx_pair<3>(w0, m[0]), mx_pair<3>(w1, m[1])};
-          if (big) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              f0[i] = mul_bf16x2(f0[i], m2[i & 1]);
-              f1[i] = mul_bf16x2(f1[i], m2[i & 1]);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const uint4 b = B.p[j] ? *reinterpret_cast<const uint4*>(B.p[j] + (int64_t)s * kFewStep + c * 32 + q * 8)
-                                   : make_uint4(0u, 0u, 0u, 0u);
-            mma(acc[j], f0, __byte_perm(b.x, b.z, 0x5410), __byte_perm(b.x, b.z, 0x7632));
-            mma(acc[j], f1, __byte_perm(b.y, b.w, 0x5410), __byte_perm(b.y, b.w, 0x7632));
-          }
-        }
+      for (int j = 0; j < NT; ++j) {
+        uint32_t b[4];
+        lds(b, cols + (8 * j + g) * P + (half * 128 + blk * 32 + 8 * c) * 2);
+        mma(acc[j], a0, __byte_perm(b[0], b[2], 0x5410), __byte_perm(b[0], b[2], 0x7632));
+        mma(acc[j], a1, __byte_perm(b[1], b[3], 0x5410), __byte_perm(b[1], b[3], 0x7632));
       }
     }
   }
 }
 
-// One matrix as a piece sees it.
-struct Matrix {
-  const uint8_t* W;  // bf16 / e4m3 [K, N], MXFP4 [N, K / 2]
-  const uint8_t* s;
-  int64_t K, N;
+// ------------------------------------------------------------ shares and pieces
+// One pass over a piece: units [step0, step1) of 128 output columns of one
+// matrix, for `rows` rows of `group` B columns each.
+struct Piece {
+  int mat;     // 0: W1, 1: W3, 2: W2
+  int expert;  // slice of the routed weights
+  int col0, step0, step1;
+  int first;   // up: place of the first row in the list; down: row of h
+  int rows, group;
+  bool again;  // the weights are read by another pass too
+  float* out;  // [rows][128]
 };
 
-// A piece for `cols` columns of B, its sums to out [cols / group][128]: every
-// `group` columns (the terms of one row) are added.
-template <int WT, int NT>
-__device__ __noinline__ void piece(const Matrix& M, int col0, int step0, int step1, const Columns& B, int rows,
-                                   int group, float* out, float* red) {
+// Calls f for every pass of this CTA's share, in order, until it returns false.
+// Up projections: segments are (expert, W1 or W3, column block), the shared
+// expert sees every token in order.  Down projections: segments are (expert,
+// column block) and B holds the three terms of each row's h, at most 8 rows a
+// pass (more read the weights again, from L2 mostly: only the shared expert and
+// crowded small layers have them).
+template <int WT, bool SHARED, bool DOWN, typename F>
+__device__ __forceinline__ bool for_pieces(const FewParams& p, const Lists& ls, F f) {
+  const int inner = SHARED ? p.S : p.I;
+  const int K = DOWN ? inner : p.d;
+  const int blocks = (DOWN ? p.d : inner) / kFewCols;
+  const int per_expert = DOWN ? blocks : 2 * blocks;
+  float* buf = SHARED ? (DOWN ? p.dn_s : p.up_s) : (DOWN ? p.dn_r : p.up_r);
+  const Line L((SHARED ? 1 : ls.n) * per_expert, (K + Unit<WT>::kSteps - 1) / Unit<WT>::kSteps);
+  const uint32_t end = L.begin(blockIdx.x + 1);
+  for (uint32_t u = L.begin(blockIdx.x); u < end;) {
+    const uint32_t seg = u / L.steps;
+    Piece q;
+    q.step0 = (int)(u - seg * L.steps);
+    q.step1 = (int)min(L.steps, q.step0 + (end - u));
+    u += q.step1 - q.step0;
+    const int ei = (int)(seg / per_expert), in = (int)seg - ei * per_expert;
+    q.mat = DOWN ? 2 : in >= blocks ? 1 : 0;
+    q.col0 = (in - (q.mat == 1 ? blocks : 0)) * kFewCols;
+    q.expert = SHARED ? 0 : ls.expert[ei];
+    const int first = SHARED ? (DOWN ? p.T * p.k : 0) : ls.start[ei];
+    const int all = SHARED ? p.T : ls.start[ei + 1] - ls.start[ei];
+    float* out = buf + (int64_t)(seg + blockIdx.x) * p.T * kFewCols;
+    constexpr int kPass = DOWN ? kMaxCols / 3 : kFewMaxTokens;
+    q.group = DOWN ? 3 : 1;
+    q.again = all > kPass;
+    for (int r0 = 0; r0 < all; r0 += kPass) {
+      q.first = first + r0;
+      q.rows = min(kPass, all - r0);
+      q.out = out + r0 * kFewCols;
+      if (!f(q)) return false;
+    }
+  }
+  return true;
+}
+
+// The ring's position: stages handed over so far.
+struct Ring {
+  int n = 0;
+};
+
+struct Smem {
+  uint8_t* stages;
+  float* red;
+  Control* c;
+};
+
+// ------------------------------------------------------------ producer
+template <int WT, int RT>
+__device__ __forceinline__ uint8_t* stage_at(const Smem& sm, int s) {
+  return sm.stages + s * Unit<RT>::kBytes;
+}
+
+// The weight tile of unit `step` of a piece.
+template <int WT, bool SHARED>
+__device__ __forceinline__ void load_tile(const FewMaps& m, const FewParams& p, const Piece& q, int step, uint8_t* to,
+                                          uint64_t* bar, uint64_t policy) {
+  const CUtensorMap* map = SHARED ? &m.shared[q.mat] : &m.routed[q.mat];
+  if (WT == kFewBf16) {
+    ptx::tma_load_3d(to, map, bar, q.col0, step * 64, q.expert, policy);
+    ptx::tma_load_3d(to + 8192, map, bar, q.col0 + 64, step * 64, q.expert, policy);
+  } else if (WT == kFewE4m3) {
+    ptx::tma_load_3d(to, map, bar, q.col0, step * 128, q.expert, policy);
+  } else {
+    const int N = q.mat == 2 ? p.d : p.I;
+    ptx::tma_load_2d(to, map, bar, step * 128, q.expert * N + q.col0, policy);
+  }
+}
+
+// Streams a share.  early: as many tiles as the ring holds go ahead of the
+// activations' columns, which follow when `ready` completes.
+template <int WT, int RT, bool SHARED, bool DOWN>
+__device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring, bool early) {
+  constexpr int S = Unit<RT>::kStages;
+  constexpr int kSteps = Unit<WT>::kSteps;
+  constexpr int kPitch = Unit<WT>::kPitch;
+  const int lane = threadIdx.x & 31;
+  const uint64_t once = ptx::policy_evict_first(), more = ptx::policy_evict_normal();
+  const int K = DOWN ? (SHARED ? p.S : p.I) : p.d;
+  Control& c = *sm.c;
+  auto columns = [&](const Piece& q, int step, int slot) {
+    const int n = lane;
+    if (n >= q.rows * q.group) return;
+    const uint16_t* src = DOWN ? p.h + ((int64_t)q.first * 3 + n) * p.ld_h
+                               : p.x + (int64_t)(SHARED ? n : ls.ent[q.first + n] / p.k) * p.d;
+    bulk_load(ptx::smem_u32(stage_at<WT, RT>(sm, slot)) + kTileBytes + n * kPitch, src + step * kSteps,
+              2 * min(kSteps, K - step * kSteps), &c.full[slot]);
+  };
+  auto tile = [&](const Piece& q, int step, int slot) {
+    if (lane == 0) {
+      const uint32_t cols = q.rows * q.group * 2 * min(kSteps, K - step * kSteps);
+      ptx::mbar_arrive_expect_tx(&c.full[slot], kTileBytes + cols);
+      load_tile<WT, SHARED>(m, p, q, step, stage_at<WT, RT>(sm, slot), &c.full[slot], q.again ? more : once);
+    }
+    __syncwarp();
+  };
+  auto slot_free = [&](int n) {
+    if (ptx::wait_bounded(&c.empty[n % S], ((n / S) & 1) ^ 1, &c.abort)) return true;
+    if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
+    return false;
+  };
+  int ahead = 0;
+  if (early) {
+    int n = ring.n;
+    if (!for_pieces<WT, SHARED, DOWN>(p, ls, [&](const Piece& q) {
+          for (int step = q.step0; step < q.step1 && ahead < S; ++step, ++ahead, ++n) {
+            if (!slot_free(n)) return false;
+            tile(q, step, n % S);
+          }
+          return ahead < S;
+        }) &&
+        c.abort)
+      return false;
+    if (!ptx::wait_bounded(&c.ready, 0, &c.abort)) {
+      if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
+      return false;
+    }
+    ptx::fence_proxy_async_all();  // h was written by ordinary stores
+  }
+  return for_pieces<WT, SHARED, DOWN>(p, ls, [&](const Piece& q) {
+    for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
+      if (ahead > 0) {
+        --ahead;
+      } else {
+        if (!slot_free(ring.n)) return false;
+        tile(q, step, ring.n % S);
+      }
+      columns(q, step, ring.n % S);
+    }
+    return true;
+  });
+}
+
+// ------------------------------------------------------------ consumers
+template <int WT, int RT, int NT>
+__device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q, const uint8_t* scales, int K, int N,
+                                              const Smem& sm, Ring& ring) {
+  constexpr int S = Unit<RT>::kStages;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  constexpr int kParts = WT == kFewMxfp4 ? 2 : kWarps / 2;  // warps that share a column
-  if (WT == kFewMxfp4) {
-    float acc[NT][4] = {};
-    codes_piece<NT>(M.W, M.s, M.K, col0, step0, step1, B, acc);
-    float* to = red + (warp >> 3) * (8 * NT * kRedPitch) + (warp & 7) * 16 + g;
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) to[(8 * j + 2 * c + (i & 1)) * kRedPitch + (i >> 1) * 8] = acc[j][i];
-  } else {
-    float acc[4][NT][4] = {};
-    const float* s = WT == kFewE4m3 ? reinterpret_cast<const float*>(M.s) + col0 / 128 : nullptr;
-    rows_piece<WT, NT>(M.W, M.N, col0, step0, step1, s, M.N / 128, B, acc);
-    float* to = red + (warp >> 1) * (8 * NT * kRedPitch) + (warp & 1) * 64 + 8 * g;
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) to[(8 * j + 2 * c + (i & 1)) * kRedPitch + 2 * t + (i >> 1)] = acc[t][j][i];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * kFewCols; i += kThreads) {
-    const int r = i / kFewCols, col = i % kFewCols;
-    float a = 0.0f;
-    for (int q = 0; q < group; ++q)
-#pragma unroll
-      for (int p = 0; p < kParts; ++p) a += red[(p * 8 * NT + r * group + q) * kRedPitch + col];
-    out[(int64_t)r * kFewCols + col] = a;
-  }
-  __syncthreads();
-}
-
-template <int WT>
-__device__ __forceinline__ void piece_any(const Matrix& M, int col0, int step0, int step1, const Columns& B, int rows,
-                                          int group, float* out, float* red) {
-  const int nt = (rows * group + 7) / 8;
-  if (nt <= 1)
-    piece<WT, 1>(M, col0, step0, step1, B, rows, group, out, red);
-  else if (nt == 2)
-    piece<WT, 2>(M, col0, step0, step1, B, rows, group, out, red);
-  else
-    piece<WT, 3>(M, col0, step0, step1, B, rows, group, out, red);
-}
-
-// This CTA's share of the up projections: segments are (expert, W1 or W3,
-// column block).  Shared expert: every token, in order.
-template <int WT, bool SHARED>
-__device__ void up_share(const FewParams& p, const Lists& ls, float* buf, float* red) {
-  const int N = SHARED ? p.S : p.I;
-  const int blocks = N / kFewCols;
-  const Line L((SHARED ? 1 : ls.n) * 2 * blocks, p.d / kFewStep);
-  const int g = (threadIdx.x & 31) >> 2;
-  const uint32_t end = L.begin(blockIdx.x + 1);
-  for (uint32_t u = L.begin(blockIdx.x); u < end;) {
-    const uint32_t seg = u / L.steps;
-    const int step0 = (int)(u - seg * L.steps);
-    const int step1 = (int)min(L.steps, step0 + (end - u));
-    u += step1 - step0;
-    const int block = (int)(seg % blocks);
-    const int mat = (int)(seg / blocks) & 1;
-    const int ei = (int)(seg / (2 * blocks));
-    const int first = SHARED ? 0 : ls.start[ei];
-    const int rows = SHARED ? p.T : ls.start[ei + 1] - first;
-    Columns B;
-#pragma unroll
-    for (int j = 0; j < kMaxNT; ++j) {
-      const int n = 8 * j + g;
-      const int t = SHARED ? n : n < rows ? ls.ent[first + n] / p.k : 0;
-      B.p[j] = n < rows ? p.x + (int64_t)t * p.d : nullptr;
+  Control& ct = *sm.c;
+  float acc[NT][4] = {};
+  // scales of the next unit are fetched while this one is multiplied
+  const float* sf = nullptr;
+  const uint32_t* sw = nullptr;
+  float f = 0.0f;
+  uint32_t s[2] = {0u, 0u};
+  int64_t sld = 0;
+  const int half = warp >> 3;
+  if constexpr (WT == kFewE4m3) {
+    sld = N / 128;
+    sf = reinterpret_cast<const float*>(scales) + (int64_t)q.expert * (K / 128) * sld + q.col0 / 128;
+    f = __ldg(sf + q.step0 * sld);
+  } else if constexpr (WT == kFewMxfp4) {
+    sld = K / 128;  // words of four scales in a row
+    sw = reinterpret_cast<const uint32_t*>(scales) +
+         ((int64_t)q.expert * N + q.col0 + (warp & 7) * 16 + g) * sld + half;
+    if (2 * q.step0 + half < sld) {
+      s[0] = __ldg(sw + 2 * q.step0);
+      s[1] = __ldg(sw + 8 * sld + 2 * q.step0);
     }
-    Matrix M{SHARED ? (mat ? p.W3s : p.W1s) : (mat ? p.W3 : p.W1), mat ? p.s3 : p.s1, p.d, N};
-    if (!SHARED) {
-      const int64_t e = ls.expert[ei], n = (int64_t)p.d * p.I;
-      M.W += WT == kFewBf16 ? 2 * e * n : WT == kFewE4m3 ? e * n : e * n / 2;
-      M.s += WT == kFewE4m3 ? e * (n / 16384) * 4 : WT == kFewMxfp4 ? e * n / 32 : 0;
-    }
-    piece_any<WT>(M, block * kFewCols, step0, step1, B, rows, 1, buf + (int64_t)(seg + blockIdx.x) * p.T * kFewCols, red);
   }
-}
-
-// This CTA's share of the down projections: segments are (expert, column
-// block); the B columns are the three terms of each row's h, at most 8 rows a
-// pass (more read the weights again, from L2 mostly: only the shared expert
-// and crowded small layers have them).
-template <int WT, bool SHARED>
-__device__ void down_share(const FewParams& p, const Lists& ls, float* buf, float* red) {
-  const int K = SHARED ? p.S : p.I;
-  const int blocks = p.d / kFewCols;
-  const Line L((SHARED ? 1 : ls.n) * blocks, K / kFewStep);
-  const int g = (threadIdx.x & 31) >> 2;
-  const uint32_t end = L.begin(blockIdx.x + 1);
-  for (uint32_t u = L.begin(blockIdx.x); u < end;) {
-    const uint32_t seg = u / L.steps;
-    const int step0 = (int)(u - seg * L.steps);
-    const int step1 = (int)min(L.steps, step0 + (end - u));
-    u += step1 - step0;
-    const int block = (int)(seg % blocks);
-    const int ei = (int)(seg / blocks);
-    const int first = SHARED ? p.T * p.k : ls.start[ei];
-    const int all = SHARED ? p.T : ls.start[ei + 1] - first;
-    Matrix M{SHARED ? p.W2s : p.W2, p.s2, K, p.d};
-    if (!SHARED) {
-      const int64_t e = ls.expert[ei], n = (int64_t)p.d * p.I;
-      M.W += WT == kFewBf16 ? 2 * e * n : WT == kFewE4m3 ? e * n : e * n / 2;
-      M.s += WT == kFewE4m3 ? e * (n / 16384) * 4 : WT == kFewMxfp4 ? e * n / 32 : 0;
-    }
-    for (int r0 = 0; r0 < all; r0 += 8) {
-      const int rows = min(8, all - r0);
-      Columns B;
-#pragma unroll
-      for (int j = 0; j < kMaxNT; ++j) {
-        const int n = 8 * j + g;
-        B.p[j] = n < 3 * rows ? p.h + ((int64_t)(first + r0) * 3 + n) * p.ld_h : nullptr;
+  for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
+    float f1 = 0.0f;
+    uint32_t s1[2] = {0u, 0u};
+    if (step + 1 < q.step1) {
+      if constexpr (WT == kFewE4m3) f1 = __ldg(sf + (step + 1) * sld);
+      if constexpr (WT == kFewMxfp4) {
+        if (2 * (step + 1) + half < sld) {
+          s1[0] = __ldg(sw + 2 * (step + 1));
+          s1[1] = __ldg(sw + 8 * sld + 2 * (step + 1));
+        }
       }
-      piece_any<WT>(M, block * kFewCols, step0, step1, B, rows, 3,
-                    buf + ((int64_t)(seg + blockIdx.x) * p.T + r0) * kFewCols, red);
     }
+    const int slot = ring.n % S;
+    if (!ptx::wait_bounded(&ct.full[slot], (ring.n / S) & 1, &ct.abort)) {
+      raise_status(p.status, &ct.abort, kStatusTimeout);
+      return false;
+    }
+    const uint32_t tile = ptx::smem_u32(stage_at<WT, RT>(sm, slot)), cols = tile + kTileBytes;
+    if constexpr (WT == kFewBf16) stage_bf16<NT>(tile, cols, acc);
+    if constexpr (WT == kFewE4m3) stage_e4m3<NT>(tile, cols, f, acc);
+    if constexpr (WT == kFewMxfp4) {
+      if (2 * step + half < sld) stage_mxfp4<NT>(tile, cols, s, acc);  // the last unit may be half of one
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&ct.empty[slot]);
+    f = f1;
+    s[0] = s1[0];
+    s[1] = s1[1];
   }
+  // the two halves of the steps, and the terms of each row, are joined by the
+  // pair of warps that has these 16 columns
+  const int pair = warp & 7;
+  float* red = sm.red + pair * kRedFloats;
+  const int lo = WT == kFewE4m3 ? 2 * g : g, hi = WT == kFewE4m3 ? 2 * g + 1 : g + 8;
+  float* to = red + half * kMaxCols * kRedPitch;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    to[(8 * j + 2 * c) * kRedPitch + lo] = acc[j][0];
+    to[(8 * j + 2 * c + 1) * kRedPitch + lo] = acc[j][1];
+    to[(8 * j + 2 * c) * kRedPitch + hi] = acc[j][2];
+    to[(8 * j + 2 * c + 1) * kRedPitch + hi] = acc[j][3];
+  }
+  ptx::named_barrier(1 + pair, 64);
+  for (int i = half * 32 + lane; i < q.rows * 16; i += 64) {
+    const int r = i >> 4, col = i & 15;
+    float a = 0.0f;
+    for (int t = 0; t < q.group; ++t) {
+      const float* x = red + (r * q.group + t) * kRedPitch + col;
+      a += x[0] + x[kMaxCols * kRedPitch];
+    }
+    q.out[r * kFewCols + pair * 16 + col] = a;
+  }
+  ptx::named_barrier(1 + pair, 64);
+  return true;
+}
+
+template <int WT, int RT, bool SHARED, bool DOWN>
+__device__ bool consume(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
+  const int inner = SHARED ? p.S : p.I;
+  const int K = DOWN ? inner : p.d, N = DOWN ? p.d : inner;
+  return for_pieces<WT, SHARED, DOWN>(p, ls, [&](const Piece& q) {
+    const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
+    const int cols = q.rows * q.group;
+    if (cols <= 8) return consume_piece<WT, RT, 1>(p, q, scales, K, N, sm, ring);
+    if (cols <= 16) return consume_piece<WT, RT, 2>(p, q, scales, K, N, sm, ring);
+    return consume_piece<WT, RT, 3>(p, q, scales, K, N, sm, ring);
+  });
 }
 
 // ------------------------------------------------------------ router
@@ -502,14 +613,14 @@ __device__ void logits_share(const FewParams& p, double* red) {
         if (lane == 0) red[warp * kFewMaxTokens + t] = acc[t];
       }
     }
-    __syncthreads();
+    consumer_sync();
     if (tid < p.T) {
       double a = 0.0;
 #pragma unroll
       for (int w = 0; w < 8; ++w) a += red[(half * 8 + w) * kFewMaxTokens + tid];
       p.logits[(int64_t)tid * p.E + e] = (float)a;
     }
-    __syncthreads();
+    consumer_sync();
   }
 }
 
@@ -599,15 +710,19 @@ __device__ void choose(const FewParams& p, Lists& ls, int t, double* key) {
   }
 }
 
-// Routing of all tokens and the lists of chosen experts and their rows.
+// Routing of all tokens and the lists of chosen experts and their rows, by the
+// router's warps.
 __device__ void route(const FewParams& p, Lists& ls, double* keys) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < p.E; e += kThreads) ls.counts[e] = 0;
-  if (warp < p.T) choose(p, ls, warp, keys + (int64_t)warp * p.E);
-  __syncthreads();
+  constexpr int kThreads = 32 * kRouterWarps;
+  const int tid = threadIdx.x - kAllThreads + kThreads;
+  const int warp = tid >> 5, lane = tid & 31;
+  for (int e = tid; e < p.E; e += kThreads) ls.counts[e] = 0;
+  const int n_choose = choosers(p.E);
+  for (int t = warp; warp < n_choose && t < p.T; t += n_choose) choose(p, ls, t, keys + (int64_t)warp * p.E);
+  router_sync();
   const int n = p.T * p.k;
-  for (int i = threadIdx.x; i < n; i += kThreads) atomicAdd(&ls.counts[ls.idx[i]], 1);
-  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) atomicAdd(&ls.counts[ls.idx[i]], 1);
+  router_sync();
   if (warp == 0) {
     int chosen = 0, rows = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
@@ -634,8 +749,8 @@ __device__ void route(const FewParams& p, Lists& ls, double* keys) {
       ls.n = chosen;
     }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  router_sync();
+  for (int i = tid; i < n; i += kThreads) {
     const int e = ls.idx[i];
     int at = ls.start[ls.seg_of[e]];
     for (int q = 0; q < i; ++q) at += ls.idx[q] == e ? 1 : 0;
@@ -643,14 +758,14 @@ __device__ void route(const FewParams& p, Lists& ls, double* keys) {
     ls.row_of[i] = (int16_t)at;
   }
   if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < n; i += kThreads) {
+    for (int i = tid; i < n; i += kThreads) {
       if (p.idx_out) p.idx_out[i] = ls.idx[i];
       if (p.w_out) p.w_out[i] = ls.w[i];
     }
     if (p.counts_out)
-      for (int e = threadIdx.x; e < p.E; e += kThreads) p.counts_out[e] = ls.counts[e];
+      for (int e = tid; e < p.E; e += kThreads) p.counts_out[e] = ls.counts[e];
   }
-  __syncthreads();
+  router_sync();
 }
 
 // ------------------------------------------------------------ between the products
@@ -672,14 +787,15 @@ __device__ __forceinline__ void terms_of(float v, uint32_t (&t)[3]) {
 }
 
 // h of every row, four columns a lane.
+template <int WT>
 __device__ void activations(const FewParams& p, const Lists& ls) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * kWarps;
   const int rows = p.T * p.k;
   const int rb = p.I / kFewCols, sb = p.S / kFewCols;
   const int64_t jobs = (int64_t)rows * rb + (int64_t)p.T * sb;
-  const Line Lr(ls.n * 2 * rb, p.d / kFewStep);
-  const Line Ls(2 * sb, p.d / kFewStep);
+  const Line Lr(ls.n * 2 * rb, (p.d + Unit<WT>::kSteps - 1) / Unit<WT>::kSteps);
+  const Line Ls(2 * sb, p.d / Unit<kFewBf16>::kSteps);
   for (int64_t job = (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x; job < jobs; job += warps) {
     const bool shared = job >= (int64_t)rows * rb;
     const int64_t j = shared ? job - (int64_t)rows * rb : job;
@@ -708,12 +824,13 @@ __device__ void activations(const FewParams& p, const Lists& ls) {
 }
 
 // y: routed rows in slot order, then the shared expert's.
+template <int WT>
 __device__ void combine(const FewParams& p, const Lists& ls) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * kWarps;
   const int blocks = p.d / kFewCols;
-  const Line Lr(ls.n * blocks, p.I / kFewStep);
-  const Line Ls(blocks, p.S > 0 ? p.S / kFewStep : 1);
+  const Line Lr(ls.n * blocks, (p.I + Unit<WT>::kSteps - 1) / Unit<WT>::kSteps);
+  const Line Ls(blocks, p.S > 0 ? p.S / Unit<kFewBf16>::kSteps : 1);
   const int64_t jobs = (int64_t)p.T * blocks;
   for (int64_t job = (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x; job < jobs; job += warps) {
     const int t = (int)(job / blocks), block = (int)(job % blocks);
@@ -744,57 +861,105 @@ __device__ void combine(const FewParams& p, const Lists& ls) {
   }
 }
 
-template <int WT>
-__global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ FewParams p) {
-  extern __shared__ __align__(16) uint8_t dyn[];
+// ------------------------------------------------------------ the kernel
+template <int RT>
+__global__ void __launch_bounds__(kAllThreads, 1)
+    few_kernel(const __grid_constant__ FewParams p, const __grid_constant__ FewMaps maps) {
+  extern __shared__ uint8_t dyn[];
   __shared__ Lists ls;
-  float* red = reinterpret_cast<float*>(dyn);
-  double* keys = reinterpret_cast<double*>(dyn);
-  if (threadIdx.x == 0) ls.abort = 0;
+  __shared__ Control ct;
+  constexpr int S = Unit<RT>::kStages;
+  Smem sm;
+  sm.stages = align_1024(dyn);
+  sm.red = reinterpret_cast<float*>(sm.stages + S * Unit<RT>::kBytes);
+  sm.c = &ct;
+  double* keys = reinterpret_cast<double*>(sm.red + 8 * kRedFloats);  // the router's, or partial logits
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      ptx::mbar_init(&ct.full[s], 1);
+      ptx::mbar_init(&ct.empty[s], kWarps);
+    }
+    ptx::mbar_init(&ct.routed, 32 * kRouterWarps);
+    ptx::mbar_init(&ct.ready, 1);
+    ct.abort = 0u;
+    ct.never = 0u;
+    ptx::fence_barrier_init();
+    ptx::fence_proxy_async();
+  }
+  __syncthreads();
+  volatile uint32_t* abort = &ct.abort;
 
-  logits_share(p, keys);
-  grid_arrive(p.bar + 0);
-  if (p.S > 0) up_share<kFewBf16, true>(p, ls, p.up_s, red);
-  if (!grid_wait(p.bar + 0, p.status, &ls.abort)) return;
+  if (warp == kWarps) {
+    // ---------------------------------------------- producer
+    Ring ring;
+    bool ok = true;
+    if (p.S > 0) ok = produce<kFewBf16, RT, true, false>(maps, p, ls, sm, ring, false);
+    if (ok && !ptx::wait_bounded(&ct.routed, 0, abort)) {
+      raise_status(p.status, abort, kStatusTimeout);
+      ok = false;
+    }
+    ok = ok && *abort == 0;  // the router gave up: there are no lists
+    if (ok) ok = produce<RT, RT, false, false>(maps, p, ls, sm, ring, false);
+    // the routed share first: it is there in every call
+    if (ok) ok = produce<RT, RT, false, true>(maps, p, ls, sm, ring, true);
+    if (ok && p.S > 0) produce<kFewBf16, RT, true, true>(maps, p, ls, sm, ring, false);
+    // every issued copy must land before the CTA may exit (tiles that went
+    // ahead of a wait that failed have landed long before its limit)
+    if ((threadIdx.x & 31) == 0)
+      for (int j = ring.n > S ? ring.n - S : 0; j < ring.n; ++j)
+        if (!ptx::wait_bounded(&ct.full[j % S], (j / S) & 1, &ct.never)) raise_status(p.status, abort, kStatusTimeout);
+  } else if (warp > kWarps) {
+    // ---------------------------------------------- router
+    if (threadIdx.x == kThreads + 32) grid_poll(p.bar + 0, p.status, abort);
+    router_sync();
+    if (*abort == 0) route(p, ls, keys);
+    ptx::mbar_arrive(&ct.routed);
+  } else {
+    // ---------------------------------------------- consumers
+    Ring ring;
+    logits_share(p, reinterpret_cast<double*>(sm.red));
+    grid_arrive(p.bar + 0);
+    bool ok = true;
+    if (p.S > 0) ok = consume<kFewBf16, RT, true, false>(p, ls, sm, ring);
+    ok = ok && ptx::wait_bounded(&ct.routed, 0, abort) && *abort == 0;
+    if (ok) ok = consume<RT, RT, false, false>(p, ls, sm, ring);
+    grid_arrive(p.bar + 1);
+    if (grid_wait(p.bar + 1, p.status, abort)) {
+      activations<RT>(p, ls);
+      ptx::fence_proxy_async_all();  // h is read by bulk copies
+      grid_arrive(p.bar + 2);
+      if (grid_wait(p.bar + 2, p.status, abort)) {
+        if (threadIdx.x == 0) ptx::mbar_arrive(&ct.ready);
+        if (consume<RT, RT, false, true>(p, ls, sm, ring) && p.S > 0)
+          consume<kFewBf16, RT, true, true>(p, ls, sm, ring);
+        grid_arrive(p.bar + 3);
+        if (grid_wait(p.bar + 3, p.status, abort)) combine<RT>(p, ls);
+      }
+    }
+  }
+}
 
-  route(p, ls, keys);
-  up_share<WT, false>(p, ls, p.up_r, red);
-  grid_arrive(p.bar + 1);
-  if (!grid_wait(p.bar + 1, p.status, &ls.abort)) return;
-
-  activations(p, ls);
-  grid_arrive(p.bar + 2);
-  if (!grid_wait(p.bar + 2, p.status, &ls.abort)) return;
-
-  if (p.S > 0) down_share<kFewBf16, true>(p, ls, p.dn_s, red);
-  down_share<WT, false>(p, ls, p.dn_r, red);
-  grid_arrive(p.bar + 3);
-  if (!grid_wait(p.bar + 3, p.status, &ls.abort)) return;
-
-  combine(p, ls);
+template <int RT>
+cudaError_t launch(const FewParams& p, const FewMaps& maps, int sms, cudaStream_t stream) {
+  // stages, the pairs' joins, one routing key per expert and choosing warp
+  const size_t smem = 1024 + Unit<RT>::kStages * Unit<RT>::kBytes + 8 * kRedFloats * 4 + (size_t)choosers(p.E) * p.E * 8;
+  auto kernel = few_kernel<RT>;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
+  void* args[] = {const_cast<FewParams*>(&p), const_cast<FewMaps*>(&maps)};
+  return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(std::min(sms, kFewMaxSms)),
+                                     dim3(kAllThreads), args, smem, stream);
 }
 
 }  // namespace
 
-size_t few_smem_bytes(const FewParams& p, int weights) {
-  // the CTA's reduction buffer for the widest pass (the shared expert's is
-  // bf16 whatever the routed weights), or the tokens' routing keys
-  const size_t red = (size_t)(kWarps / 2) * 8 * kMaxNT * kRedPitch * 4;
-  (void)weights;
-  return std::max(red, (size_t)p.T * p.E * 8);
-}
-
-cudaError_t launch_few(const FewParams& p, int weights, int sms, cudaStream_t stream) {
-  const size_t smem = few_smem_bytes(p, weights);
-  auto kernel = weights == kFewBf16   ? few_kernel<kFewBf16>
-                : weights == kFewE4m3 ? few_kernel<kFewE4m3>
-                                      : few_kernel<kFewMxfp4>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (err != cudaSuccess) return err;
-  FewParams q = p;
-  void* args[] = {&q};
-  return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(std::min(sms, kFewMaxSms)),
-                                     dim3(kThreads), args, smem, stream);
+cudaError_t launch_few(const FewParams& p, const FewMaps& maps, int weights, int sms, cudaStream_t stream) {
+  switch (weights) {
+    case kFewBf16: return launch<kFewBf16>(p, maps, sms, stream);
+    case kFewE4m3: return launch<kFewE4m3>(p, maps, sms, stream);
+    default: return launch<kFewMxfp4>(p, maps, sms, stream);
+  }
 }
 
 }  // namespace moe

@@ -3,6 +3,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace moe {
@@ -10,10 +11,12 @@ namespace moe {
 constexpr int kFewMaxTokens = 16;
 constexpr int kFewMaxSms = 256;  // the workspace holds partial sums for this many CTAs
 constexpr int kFewCols = 128;    // output columns of a segment
-constexpr int kFewStep = 128;    // contraction length of a work unit
 
 // How a call's routed expert weights are held.
 enum FewWeights : int { kFewBf16 = 0, kFewE4m3 = 1, kFewMxfp4 = 2 };
+
+// Steps of the contraction in a work unit: 16 KB of 128 columns' weights.
+constexpr int few_unit_steps(int weights) { return weights == kFewBf16 ? 64 : weights == kFewE4m3 ? 128 : 256; }
 
 struct FewParams {
   int T, d, E, k, I, S;  // S = 0: no shared expert
@@ -23,9 +26,7 @@ struct FewParams {
   const uint16_t* x;
   const uint16_t* Wg;
   const float* bias;  // may be null
-  const uint8_t *W1, *W3, *W2;
   const uint8_t *s1, *s3, *s2;  // fp32 block scales or scale bytes
-  const uint8_t *W1s, *W3s, *W2s;
   void* y;
   int32_t* idx_out;    // may be null
   float* w_out;        // may be null
@@ -38,7 +39,13 @@ struct FewParams {
   int ld_h;
 };
 
-size_t few_smem_bytes(const FewParams& p, int weights);
-cudaError_t launch_few(const FewParams& p, int weights, int sms, cudaStream_t stream);
+// Tensor maps of W1, W3 and W2, all with the 128-byte swizzle.  bf16: [E, K, N]
+// in boxes of 64 steps by 64 columns; e4m3: [E, K, N] bytes in boxes of 128 by
+// 128; MXFP4: [E * N, K / 2] bytes in boxes of 128 columns by 256 steps.
+struct FewMaps {
+  CUtensorMap routed[3], shared[3];
+};
+
+cudaError_t launch_few(const FewParams& p, const FewMaps& maps, int weights, int sms, cudaStream_t stream);
 
 }  // namespace moe

@@ -45,7 +45,7 @@ moe_status check_few(const moe_shape* shape) {
   // the lines of work units times the CTAs have to fit 32 bits
   const int64_t experts = std::max<int64_t>(1, std::min<int64_t>(s.E, s.T * s.k));
   const int64_t wide = std::max(s.inter, s.shared_inter);
-  const int64_t units = experts * 2 * (wide / kFewCols) * (s.d / kFewStep);
+  const int64_t units = experts * 2 * (wide / kFewCols) * (s.d / few_unit_steps(kFewBf16));
   if (units * (kFewMaxSms + 1) >= (int64_t)1 << 32) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -191,15 +191,9 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.x = static_cast<const uint16_t*>(x);
   p.Wg = static_cast<const uint16_t*>(Wg);
   p.bias = s.route == MOE_ROUTE_SIGMOID_GROUP ? bias : nullptr;
-  p.W1 = bytes(W1);
-  p.W3 = bytes(W3);
-  p.W2 = bytes(W2);
   p.s1 = bytes(s1);
   p.s3 = bytes(s3);
   p.s2 = bytes(s2);
-  p.W1s = bytes(W1s);
-  p.W3s = bytes(W3s);
-  p.W2s = bytes(W2s);
   p.y = y;
   p.idx_out = topk_idx_out;
   p.w_out = topk_w_out;
@@ -214,9 +208,22 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.h = at<uint16_t>(ws, L.h);
   p.ld_h = L.ld_h;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int weights = s.w_dtype == MOE_BF16 ? kFewBf16 : s.w_dtype == MOE_E4M3 ? kFewE4m3 : kFewMxfp4;
+  FewMaps maps{};
+  const void* routed[] = {W1, W3, W2};
+  const void* shared[] = {W1s, W3s, W2s};
+  for (int i = 0; i < 3; ++i) {
+    const uint64_t K = i == 2 ? s.inter : s.d, N = i == 2 ? s.d : s.inter;
+    const bool made = weights == kFewBf16   ? map_bf16_tiles(&maps.routed[i], routed[i], N, K, s.E)
+                      : weights == kFewE4m3 ? map_byte_tiles(&maps.routed[i], routed[i], N, K, s.E)
+                                            : map_bytes(&maps.routed[i], routed[i], K / 2, N * s.E, 128);
+    if (!made) return MOE_ERR_CUDA;
+    if (s.shared_inter > 0 && !map_bf16_tiles(&maps.shared[i], shared[i], i == 2 ? s.d : s.shared_inter,
+                                              i == 2 ? s.shared_inter : s.d, 1))
+      return MOE_ERR_CUDA;
+  }
   MOE_CUDA(cudaMemsetAsync(ws, 0, kAlign, st));
-  MOE_CUDA(launch_few(p, s.w_dtype == MOE_BF16 ? kFewBf16 : s.w_dtype == MOE_E4M3 ? kFewE4m3 : kFewMxfp4,
-                      device_sms(), st));
+  MOE_CUDA(launch_few(p, maps, weights, device_sms(), st));
   return MOE_OK;
 }
 
