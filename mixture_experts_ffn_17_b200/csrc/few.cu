@@ -10,14 +10,13 @@
 // latency to be kept out of the stream's way.  One CTA per SM, three roles:
 //   consumers (16 warps)  logits of a share of the experts, then the products
 //                         and the two joins, with grid barriers between them;
-//   producer (1 warp)     fills a ring of stages with weight tiles (TMA) and the
-//                         matching columns of activations (bulk copies), ahead
+//   producer (1 warp)     fills a ring of stages with weight tiles by TMA, ahead
 //                         of the consumers and across the ends of pieces and
 //                         phases: the shared expert's up projections need no
 //                         routing and stream while it is found, and the first
 //                         tiles of the down projections are in the ring before
 //                         the barriers that the activations wait for;
-//   router (4 warps)      waits for all logits, finds the top-k (in every CTA)
+//   router (3 warps)      waits for all logits, finds the top-k (in every CTA)
 //                         and the list of chosen experts and their rows.
 //
 // Split of the work.  A segment is 128 output columns of one matrix of one
@@ -32,16 +31,23 @@
 //
 // Arithmetic: mma.sync m16n8k16 with the weights as the A operand (16 output
 // columns by 16 steps, ldmatrix from the stage) and the activations as B's
-// columns, 8 at a time.  (tcgen05 would pad the columns to 16 and could not take
-// these codes unconverted; the tensor pipe is idle either way.)  Consumer warp w
-// takes columns 16 (w % 8) of a tile and one half of its steps (w / 8).  e4m3
-// and MXFP4 codes become bf16 exactly: their exponent and mantissa bits are
-// moved to bf16's and the exponent's offset is made up by an exact
-// multiplication with a power of two.  x is bf16; h is fp32 and goes in as three
-// bf16 terms (8 bits each: 24 in all), so its rounding costs nothing against
-// fp32.
+// columns, 8 at a time, read from L2 one stage ahead (their small bulk copies
+// cost more than the weights': 710 instead of 455 us at T = 8, bf16, 28 experts
+// of 7168 x 2048).  (tcgen05 would pad the columns to 16 and could not take these
+// codes unconverted; the tensor pipe is idle either way.)  Consumer warp w takes
+// columns 16 (w % 8) of a tile and one half of its steps (w / 8).
+//   bf16 weights: x is bf16 as it comes; h is fp32 and goes in as three bf16
+//   terms (8 bits each: 24 in all).
+//   e4m3 and MXFP4 codes are converted to fp16, which holds them exactly; x and h
+//   are fp16 too, times a power of two that puts the largest of a token (of 128
+//   values of h) at 2^14: a bf16 x fits exactly down to 2^-29 of the largest
+//   and to 2^-40 of it below; h goes in as two terms (22 bits).  (Converting
+//   the codes to bf16 takes 5 instructions a pair instead of 1 to 1.5, which
+//   bound the kernel: 2.0 to 2.2 TB/s.)
+// Block scales multiply fp32 sums.
 #include <algorithm>
 #include <cstdint>
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "few.h"
@@ -51,7 +57,7 @@ namespace {
 
 constexpr int kWarps = 16;  // consumers
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRouterWarps = 4;
+constexpr int kRouterWarps = 3;  // 20 warps in all, which leaves a thread 96 registers
 constexpr int kAllThreads = kThreads + 32 + 32 * kRouterWarps;
 constexpr int kMaxNT = 3;       // 8-column B tiles of one pass
 constexpr int kMaxCols = 8 * kMaxNT;
@@ -59,19 +65,10 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxRows = kFewMaxTokens * 32;  // T * k
 constexpr uint32_t kTileBytes = 16384;
 
-// Steps of the contraction that a stage holds, the distance of its B columns in
-// bytes (2 steps + a pad that keeps their reads off each other's banks), and the
-// stages that fit beside the rest.
-template <int WT>
-struct Unit {
-  static constexpr int kSteps = few_unit_steps(WT);
-  static constexpr int kPitch = WT == kFewMxfp4 ? 2 * kSteps + 64 : 2 * kSteps + 16;
-  static constexpr uint32_t kBytes = (kTileBytes + kMaxCols * kPitch + 1023) / 1024 * 1024;
-  static constexpr int kStages = WT == kFewBf16 ? 8 : WT == kFewE4m3 ? 7 : 5;
-};
+constexpr int kStages = 10;
 
 // Router warps that choose experts at the same time (a key per expert each).
-__host__ __device__ constexpr int choosers(int E) { return E <= 512 ? kRouterWarps : kRouterWarps / 2; }
+__host__ __device__ constexpr int choosers(int E) { return E <= 512 ? kRouterWarps : 2; }
 
 constexpr int kRedPitch = 17;  // floats of one B column of a warp pair's 16 output columns
 constexpr int kRedFloats = 2 * kMaxCols * kRedPitch;  // of a pair of warps
@@ -89,9 +86,8 @@ struct Lists {  // what the routing leaves in shared memory
 };
 
 struct Control {
-  uint64_t full[9], empty[9];
+  uint64_t full[kStages], empty[kStages];
   uint64_t routed;  // the lists are there
-  uint64_t ready;   // h is there, in all CTAs
   uint32_t abort, never;
 };
 
@@ -161,12 +157,20 @@ __device__ __forceinline__ float4 sum_pieces(const float* buf, const Line& L, ui
 }
 
 // ------------------------------------------------------------ tiles and columns
+template <bool F16>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
@@ -183,152 +187,179 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-__device__ __forceinline__ void lds(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+// e4m3 codes in bytes (0, 1) and (2, 3) to two fp16 pairs.
+__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+// Eight MXFP4 codes to four fp16 pairs.
+__device__ __forceinline__ void mx_pairs(uint32_t w, uint32_t (&f)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+      : "r"(w));
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
-               : "memory");
+// Whether one of a word's four bytes is 0 or 255.
+__device__ __forceinline__ bool has_end_byte(uint32_t w) {
+  return ((((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w)) & 0x80808080u) != 0;
 }
 
-// Two e4m3 codes in bytes 1 and 3 to bf16x2: sign to bit 15, the seven other
-// bits to exponent and mantissa; 2^120 makes up the exponents' offsets (127 -
-// 7), exactly and for subnormal codes too.  The code 0x7f is NaN.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t v) {
-  const uint32_t m = (v >> 4) & 0x07f007f0u;
-  uint32_t r = mul_bf16x2((v & 0x80008000u) | m, 0x7b807b80u);
-  if (((m + 0x00100010u) & 0x08000800u) != 0) {  // a magnitude of 0x7f in either half
-    if ((m & 0xffffu) == 0x07f0u) r |= 0x00007fffu;
-    if ((m >> 16) == 0x07f0u) r |= 0x7fff0000u;
+// 2^(byte - 127); the ends, 2^-127 and NaN, only where `ends` says they may be.
+__device__ __forceinline__ float scale_of(uint32_t word, int byte, bool ends) {
+  const uint32_t v = (word >> (8 * byte)) & 255u;
+  uint32_t bits = v << 23;
+  if (ends) bits = v == 0 ? 0x00400000u : v == 255u ? 0x7fffffffu : bits;
+  return __uint_as_float(bits);
+}
+
+// How B's columns lie in memory.  A lane reads the steps that it feeds to the
+// MMAs: with ldmatrix.trans, 2c, 2c + 1 of each eight; of a 32-step block of
+// MXFP4, 8c to 8c + 7.  Columns that this kernel writes are ordered so that these
+// are 16 bytes in a row: step k of a 32-step block at place_of(k).
+template <int WT>
+__device__ __forceinline__ int place_of(int k) {
+  if (WT == kFewMxfp4) return k;
+  return (k & ~31) + 8 * ((k & 7) >> 1) + 2 * ((k & 31) >> 3) + (k & 1);
+}
+
+// The words of B that a lane uses of one stage, for one column tile.
+template <int WT>
+struct BWords {
+  static constexpr int kBlocks = WT == kFewBf16 ? 1 : WT == kFewE4m3 ? 2 : 4;  // of 32 steps
+  uint32_t w[kBlocks][4];
+};
+
+// raw: x as it comes (in step order), for bf16 weights.
+template <int WT>
+__device__ __forceinline__ void load_columns(BWords<WT>& b, const uint16_t* p, int step, bool raw) {
+  const int lane = threadIdx.x & 31, half = threadIdx.x >> 8, c = lane & 3;
+  constexpr int kBlocks = BWords<WT>::kBlocks;
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b.w[i][e] = 0u;
+  if (!p) return;
+  p += step * few_unit_steps(WT) + half * (32 * kBlocks);
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    if (raw) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b.w[i][e] = *reinterpret_cast<const uint32_t*>(p + 32 * i + 8 * e + 2 * c);
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 32 * i + 8 * c);
+      b.w[i][0] = v.x;
+      b.w[i][1] = v.y;
+      b.w[i][2] = v.z;
+      b.w[i][3] = v.w;
+    }
   }
-  return r;
-}
-
-// Codes j and j + 4 of eight MXFP4 codes to bf16x2, times `scale` (2^126 and
-// the block's scale in each half): the three low bits go to the ends of
-// exponent and mantissa, which reads 2^-126 times the code's value.
-template <int J>
-__device__ __forceinline__ uint32_t mx_pair(uint32_t w, uint32_t scale) {
-  const uint32_t s = J == 3 ? w : w << (12 - 4 * J);
-  const uint32_t m = J <= 1 ? w << (6 - 4 * J) : w >> (4 * J - 6);
-  return mul_bf16x2((s & 0x80008000u) | (m & 0x01c001c0u), scale);
 }
 
 // One stage of a piece: this warp's sums over its half of the steps.
 // bf16: two boxes of 64 columns, [steps][64 columns].
 template <int NT>
-__device__ __forceinline__ void stage_bf16(uint32_t tile, uint32_t cols, float (&acc)[NT][4]) {
-  constexpr int P = Unit<kFewBf16>::kPitch;
+__device__ __forceinline__ void stage_bf16(uint32_t tile, const BWords<kFewBf16> (&b)[NT], float (&acc)[NT][4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane >> 3, r = lane & 7;
-  const int k0 = (warp >> 3) * 32;
-  uint32_t b[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) ldsm(b[j], cols + (8 * j + r) * P + (k0 + 8 * i) * 2);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int k = k0 + 16 * q + (i >> 1) * 8 + r;
+    const int k = (warp >> 3) * 32 + 16 * q + (i >> 1) * 8 + r;
     const int chunk = (warp & 3) * 2 + (i & 1);
     uint32_t a[4];
     ldsm_t(a, tile + ((warp >> 2) & 1) * 8192 + k * 128 + ((chunk ^ (k & 7)) << 4));
 #pragma unroll
-    for (int j = 0; j < NT; ++j) mma(acc[j], a, b[j][2 * q], b[j][2 * q + 1]);
+    for (int j = 0; j < NT; ++j) mma<false>(acc[j], a, b[j].w[0][2 * q], b[j].w[0][2 * q + 1]);
   }
 }
 
 // e4m3: [steps][128 columns] codes; a 16-bit unit of ldmatrix is two columns of
 // one step, so a register holds columns 2g and 2g + 1 of steps 2c and 2c + 1.
+// f[j]: the block's scale times the columns'.
 template <int NT>
-__device__ __forceinline__ void stage_e4m3(uint32_t tile, uint32_t cols, float scale, float (&acc)[NT][4]) {
-  constexpr int P = Unit<kFewE4m3>::kPitch;
+__device__ __forceinline__ void stage_e4m3(uint32_t tile, const BWords<kFewE4m3> (&b)[NT], const float (&f)[NT],
+                                           float (&acc)[NT][4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane >> 3, r = lane & 7;
   float part[NT][4] = {};
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int k0 = (warp >> 3) * 64 + 32 * q;
-    const int k = k0 + 8 * i + r;
-    uint32_t w[4];
+    const int k = (warp >> 3) * 64 + 32 * q + 8 * i + r;
+    uint32_t w[4], a0[4], a1[4];
     ldsm_t(w, tile + k * 128 + (((warp & 7) ^ (k & 7)) << 4));
-    uint32_t a0[4] = {e4m3_pair(w[0] << 8), e4m3_pair(w[0]), e4m3_pair(w[1] << 8), e4m3_pair(w[1])};
-    uint32_t a1[4] = {e4m3_pair(w[2] << 8), e4m3_pair(w[2]), e4m3_pair(w[3] << 8), e4m3_pair(w[3])};
+    e4m3_pairs(__byte_perm(w[0], 0, 0x3120), a0[0], a0[1]);
+    e4m3_pairs(__byte_perm(w[1], 0, 0x3120), a0[2], a0[3]);
+    e4m3_pairs(__byte_perm(w[2], 0, 0x3120), a1[0], a1[1]);
+    e4m3_pairs(__byte_perm(w[3], 0, 0x3120), a1[2], a1[3]);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      uint32_t b[4];
-      ldsm(b, cols + (8 * j + r) * P + (k0 + 8 * i) * 2);
-      mma(part[j], a0, b[0], b[1]);
-      mma(part[j], a1, b[2], b[3]);
+      mma<true>(part[j], a0, b[j].w[q][0], b[j].w[q][1]);
+      mma<true>(part[j], a1, b[j].w[q][2], b[j].w[q][3]);
     }
   }
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(part[j][e], scale, acc[j][e]);
+    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(part[j][e], f[j], acc[j][e]);
 }
 
 // MXFP4: [128 columns][steps / 2] codes; lane (g, c) holds the eight codes 8c of
 // a scale block for columns g and g + 8, whose scale bytes are in s[0], s[1].
+// f[j]: the columns' factor.
 template <int NT>
-__device__ __forceinline__ void stage_mxfp4(uint32_t tile, uint32_t cols, const uint32_t (&s)[2], float (&acc)[NT][4]) {
-  constexpr int P = Unit<kFewMxfp4>::kPitch;
+__device__ __forceinline__ void stage_mxfp4(uint32_t tile, const BWords<kFewMxfp4> (&b)[NT], const uint32_t (&s)[2],
+                                            const float (&f)[NT], float (&acc)[NT][4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = lane >> 3, r = lane & 7, g = lane >> 2, c = lane & 3;
-  const int half = warp >> 3;
+  const int i = lane >> 3, r = lane & 7;
   const int n = (warp & 7) * 16 + (i & 1) * 8 + r;
+  const bool ends = __any_sync(0xffffffffu, has_end_byte(s[0]) || has_end_byte(s[1]));
+  float sum[NT][4] = {};
 #pragma unroll
   for (int p = 0; p < 2; ++p) {  // two scale blocks
     uint32_t w[4];
-    const int chunk = half * 4 + 2 * p + (i >> 1);
+    const int chunk = (warp >> 3) * 4 + 2 * p + (i >> 1);
     ldsm(w, tile + n * 128 + ((chunk ^ (n & 7)) << 4));
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int blk = 2 * p + q;
-      // 2^(byte - 127 + 126) as bf16x2; a scale of 4 or more would leave
-      // bf16's range there and takes a second multiplication by 2^(byte - 128)
-      const uint32_t v0 = (s[0] >> (8 * blk)) & 255u, v1 = (s[1] >> (8 * blk)) & 255u;
-      const uint32_t m0 = (min(v0, 128u) + 126u) * 0x00800080u, m1 = (min(v1, 128u) + 126u) * 0x00800080u;
-      const uint32_t x = w[2 * q], y = w[2 * q + 1];
-      uint32_t a0[4] = {mx_pair<0>(x, m0), mx_pair<0>(y, m1), mx_pair<1>(x, m0), mx_pair<1>(y, m1)};
-      uint32_t a1[4] = {mx_pair<2>(x, m0), mx_pair<2>(y, m1), mx_pair<3>(x, m0), mx_pair<3>(y, m1)};
-      if (__any_sync(0xffffffffu, max(v0, v1) > 128u)) {
-        const uint32_t n0 = v0 == 255u ? 0x7fff7fffu : ((v0 > 128u ? v0 - 128u : 0u) + 127u) * 0x00800080u;
-        const uint32_t n1 = v1 == 255u ? 0x7fff7fffu : ((v1 > 128u ? v1 - 128u : 0u) + 127u) * 0x00800080u;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a0[e] = mul_bf16x2(a0[e], (e & 1) ? n1 : n0);
-          a1[e] = mul_bf16x2(a1[e], (e & 1) ? n1 : n0);
-        }
-      }
+      uint32_t x[4], y[4];
+      mx_pairs(w[2 * q], x);
+      mx_pairs(w[2 * q + 1], y);
+      const uint32_t a0[4] = {x[0], y[0], x[1], y[1]}, a1[4] = {x[2], y[2], x[3], y[3]};
+      const float f0 = scale_of(s[0], blk, ends), f1 = scale_of(s[1], blk, ends);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        uint32_t b[4];
-        lds(b, cols + (8 * j + g) * P + (half * 128 + blk * 32 + 8 * c) * 2);
-        mma(acc[j], a0, __byte_perm(b[0], b[2], 0x5410), __byte_perm(b[0], b[2], 0x7632));
-        mma(acc[j], a1, __byte_perm(b[1], b[3], 0x5410), __byte_perm(b[1], b[3], 0x7632));
+        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        mma<true>(part, a0, b[j].w[blk][0], b[j].w[blk][1]);
+        mma<true>(part, a1, b[j].w[blk][2], b[j].w[blk][3]);
+        sum[j][0] = fmaf(part[0], f0, sum[j][0]);
+        sum[j][1] = fmaf(part[1], f0, sum[j][1]);
+        sum[j][2] = fmaf(part[2], f1, sum[j][2]);
+        sum[j][3] = fmaf(part[3], f1, sum[j][3]);
       }
     }
   }
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(sum[j][e], f[j], acc[j][e]);
 }
 
 // ------------------------------------------------------------ shares and pieces
+// B columns that a row of h takes.
+__host__ __device__ constexpr int terms(int weights) { return weights == kFewBf16 ? 3 : 2; }
+
 // One pass over a piece: units [step0, step1) of 128 output columns of one
 // matrix, for `rows` rows of `group` B columns each.
 struct Piece {
   int mat;     // 0: W1, 1: W3, 2: W2
   int expert;  // slice of the routed weights
   int col0, step0, step1;
-  int first;   // up: place of the first row in the list; down: row of h
+  int first;   // place of the first row in the list (shared expert: token)
   int rows, group;
   bool again;  // the weights are read by another pass too
   float* out;  // [rows][128]
@@ -337,7 +368,7 @@ struct Piece {
 // Calls f for every pass of this CTA's share, in order, until it returns false.
 // Up projections: segments are (expert, W1 or W3, column block), the shared
 // expert sees every token in order.  Down projections: segments are (expert,
-// column block) and B holds the three terms of each row's h, at most 8 rows a
+// column block) and B holds the terms of each row's h, at most 8 rows a
 // pass (more read the weights again, from L2 mostly: only the shared expert and
 // crowded small layers have them).
 template <int WT, bool SHARED, bool DOWN, typename F>
@@ -347,7 +378,7 @@ __device__ __forceinline__ bool for_pieces(const FewParams& p, const Lists& ls, 
   const int blocks = (DOWN ? p.d : inner) / kFewCols;
   const int per_expert = DOWN ? blocks : 2 * blocks;
   float* buf = SHARED ? (DOWN ? p.dn_s : p.up_s) : (DOWN ? p.dn_r : p.up_r);
-  const Line L((SHARED ? 1 : ls.n) * per_expert, (K + Unit<WT>::kSteps - 1) / Unit<WT>::kSteps);
+  const Line L((SHARED ? 1 : ls.n) * per_expert, (K + few_unit_steps(WT) - 1) / few_unit_steps(WT));
   const uint32_t end = L.begin(blockIdx.x + 1);
   for (uint32_t u = L.begin(blockIdx.x); u < end;) {
     const uint32_t seg = u / L.steps;
@@ -359,11 +390,11 @@ __device__ __forceinline__ bool for_pieces(const FewParams& p, const Lists& ls, 
     q.mat = DOWN ? 2 : in >= blocks ? 1 : 0;
     q.col0 = (in - (q.mat == 1 ? blocks : 0)) * kFewCols;
     q.expert = SHARED ? 0 : ls.expert[ei];
-    const int first = SHARED ? (DOWN ? p.T * p.k : 0) : ls.start[ei];
+    const int first = SHARED ? 0 : ls.start[ei];
     const int all = SHARED ? p.T : ls.start[ei + 1] - ls.start[ei];
     float* out = buf + (int64_t)(seg + blockIdx.x) * p.T * kFewCols;
-    constexpr int kPass = DOWN ? kMaxCols / 3 : kFewMaxTokens;
-    q.group = DOWN ? 3 : 1;
+    constexpr int kPass = DOWN ? 8 : kFewMaxTokens;
+    q.group = DOWN ? terms(WT) : 1;
     q.again = all > kPass;
     for (int r0 = 0; r0 < all; r0 += kPass) {
       q.first = first + r0;
@@ -387,11 +418,6 @@ struct Smem {
 };
 
 // ------------------------------------------------------------ producer
-template <int WT, int RT>
-__device__ __forceinline__ uint8_t* stage_at(const Smem& sm, int s) {
-  return sm.stages + s * Unit<RT>::kBytes;
-}
-
 // The weight tile of unit `step` of a piece.
 template <int WT, bool SHARED>
 __device__ __forceinline__ void load_tile(const FewMaps& m, const FewParams& p, const Piece& q, int step, uint8_t* to,
@@ -408,127 +434,122 @@ __device__ __forceinline__ void load_tile(const FewMaps& m, const FewParams& p, 
   }
 }
 
-// Streams a share.  early: as many tiles as the ring holds go ahead of the
-// activations' columns, which follow when `ready` completes.
-template <int WT, int RT, bool SHARED, bool DOWN>
-__device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring, bool early) {
-  constexpr int S = Unit<RT>::kStages;
-  constexpr int kSteps = Unit<WT>::kSteps;
-  constexpr int kPitch = Unit<WT>::kPitch;
+// Brings the scales of a unit into L2 (a row of MXFP4's is 32 bytes for four
+// units), where the consumers' loads, one stage ahead of their use, find them.
+template <int WT>
+__device__ __forceinline__ void prefetch_scales(const FewParams& p, const Piece& q, int step, int K, int N) {
+  const int lane = threadIdx.x & 31;
+  const uint8_t* s = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
+  if (WT == kFewE4m3) {
+    const int64_t at = ((int64_t)q.expert * (K / 128) + step) * (N / 128) + q.col0 / 128;
+    if (lane == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(s + 4 * at));
+  } else if (WT == kFewMxfp4) {
+    if (step != q.step0 && (step & 3) != 0) return;
+    const uint8_t* row = s + ((int64_t)q.expert * N + q.col0 + lane) * (K / 32) + 8 * step;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + (int64_t)i * 32 * (K / 32)));
+  }
+}
+
+template <int WT, bool SHARED, bool DOWN>
+__device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
   const int lane = threadIdx.x & 31;
   const uint64_t once = ptx::policy_evict_first(), more = ptx::policy_evict_normal();
-  const int K = DOWN ? (SHARED ? p.S : p.I) : p.d;
+  const int inner = SHARED ? p.S : p.I;
+  const int K = DOWN ? inner : p.d, N = DOWN ? p.d : inner;
   Control& c = *sm.c;
-  auto columns = [&](const Piece& q, int step, int slot) {
-    const int n = lane;
-    if (n >= q.rows * q.group) return;
-    const uint16_t* src = DOWN ? p.h + ((int64_t)q.first * 3 + n) * p.ld_h
-                               : p.x + (int64_t)(SHARED ? n : ls.ent[q.first + n] / p.k) * p.d;
-    bulk_load(ptx::smem_u32(stage_at<WT, RT>(sm, slot)) + kTileBytes + n * kPitch, src + step * kSteps,
-              2 * min(kSteps, K - step * kSteps), &c.full[slot]);
-  };
-  auto tile = [&](const Piece& q, int step, int slot) {
-    if (lane == 0) {
-      const uint32_t cols = q.rows * q.group * 2 * min(kSteps, K - step * kSteps);
-      ptx::mbar_arrive_expect_tx(&c.full[slot], kTileBytes + cols);
-      load_tile<WT, SHARED>(m, p, q, step, stage_at<WT, RT>(sm, slot), &c.full[slot], q.again ? more : once);
-    }
-    __syncwarp();
-  };
-  auto slot_free = [&](int n) {
-    if (ptx::wait_bounded(&c.empty[n % S], ((n / S) & 1) ^ 1, &c.abort)) return true;
-    if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
-    return false;
-  };
-  int ahead = 0;
-  if (early) {
-    int n = ring.n;
-    if (!for_pieces<WT, SHARED, DOWN>(p, ls, [&](const Piece& q) {
-          for (int step = q.step0; step < q.step1 && ahead < S; ++step, ++ahead, ++n) {
-            if (!slot_free(n)) return false;
-            tile(q, step, n % S);
-          }
-          return ahead < S;
-        }) &&
-        c.abort)
-      return false;
-    if (!ptx::wait_bounded(&c.ready, 0, &c.abort)) {
-      if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
-      return false;
-    }
-    ptx::fence_proxy_async_all();  // h was written by ordinary stores
-  }
   return for_pieces<WT, SHARED, DOWN>(p, ls, [&](const Piece& q) {
     for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
-      if (ahead > 0) {
-        --ahead;
-      } else {
-        if (!slot_free(ring.n)) return false;
-        tile(q, step, ring.n % S);
+      const int s = ring.n % kStages;
+      if (!ptx::wait_bounded(&c.empty[s], ((ring.n / kStages) & 1) ^ 1, &c.abort)) {
+        if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
+        return false;
       }
-      columns(q, step, ring.n % S);
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(&c.full[s], kTileBytes);
+        load_tile<WT, SHARED>(m, p, q, step, sm.stages + s * kTileBytes, &c.full[s], q.again ? more : once);
+      }
+      __syncwarp();
+      prefetch_scales<WT>(p, q, step, K, N);
     }
     return true;
   });
 }
 
 // ------------------------------------------------------------ consumers
-template <int WT, int RT, int NT>
-__device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q, const uint8_t* scales, int K, int N,
-                                              const Smem& sm, Ring& ring) {
-  constexpr int S = Unit<RT>::kStages;
+template <int WT, int NT, bool DOWN, typename F>
+__device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q, F column, const uint8_t* scales,
+                                              int K, int N, const Smem& sm, Ring& ring) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, c = lane & 3;
+  const int g = lane >> 2, c = lane & 3, half = warp >> 3;
   Control& ct = *sm.c;
   float acc[NT][4] = {};
-  // scales of the next unit are fetched while this one is multiplied
+  const uint16_t* bp[NT];
+  const float* hp[NT];  // factors of the row that columns 2c and 2c + 1 belong to
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    bp[j] = 8 * j + g < q.rows * q.group ? column(8 * j + g) : nullptr;
+    const bool in = DOWN && WT != kFewBf16 && 4 * j + c < q.rows;
+    hp[j] = in ? p.h_scale + (int64_t)(q.first + 4 * j + c) * (K / 128) : nullptr;
+  }
   const float* sf = nullptr;
   const uint32_t* sw = nullptr;
-  float f = 0.0f;
-  uint32_t s[2] = {0u, 0u};
   int64_t sld = 0;
-  const int half = warp >> 3;
   if constexpr (WT == kFewE4m3) {
     sld = N / 128;
     sf = reinterpret_cast<const float*>(scales) + (int64_t)q.expert * (K / 128) * sld + q.col0 / 128;
-    f = __ldg(sf + q.step0 * sld);
   } else if constexpr (WT == kFewMxfp4) {
     sld = K / 128;  // words of four scales in a row
     sw = reinterpret_cast<const uint32_t*>(scales) +
          ((int64_t)q.expert * N + q.col0 + (warp & 7) * 16 + g) * sld + half;
-    if (2 * q.step0 + half < sld) {
-      s[0] = __ldg(sw + 2 * q.step0);
-      s[1] = __ldg(sw + 8 * sld + 2 * q.step0);
-    }
   }
-  for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
-    float f1 = 0.0f;
-    uint32_t s1[2] = {0u, 0u};
-    if (step + 1 < q.step1) {
-      if constexpr (WT == kFewE4m3) f1 = __ldg(sf + (step + 1) * sld);
-      if constexpr (WT == kFewMxfp4) {
-        if (2 * (step + 1) + half < sld) {
-          s1[0] = __ldg(sw + 2 * (step + 1));
-          s1[1] = __ldg(sw + 8 * sld + 2 * (step + 1));
-        }
-      }
+  // what a unit needs beside its tile is fetched while the one before it is
+  // multiplied; of MXFP4's last unit there may be one half only
+  struct Beside {
+    BWords<WT> b[NT];
+    float f[NT];
+    uint32_t s[2];
+  } now, next;
+  auto there = [&](int step) { return WT != kFewMxfp4 || 2 * step + half < sld; };
+  auto fetch = [&](Beside& x, int step) {
+    if (!there(step)) return;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      load_columns<WT>(x.b[j], bp[j], step, WT == kFewBf16 && !DOWN);
+      x.f[j] = 1.0f;
+      if (DOWN && WT != kFewBf16 && hp[j]) x.f[j] = hp[j][WT == kFewMxfp4 ? 2 * step + half : step];
     }
-    const int slot = ring.n % S;
-    if (!ptx::wait_bounded(&ct.full[slot], (ring.n / S) & 1, &ct.abort)) {
+    if constexpr (WT == kFewE4m3) {
+      const float f = __ldg(sf + step * sld);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) x.f[j] *= f;
+    }
+    if constexpr (WT == kFewMxfp4) {
+      x.s[0] = __ldg(sw + 2 * step);
+      x.s[1] = __ldg(sw + 8 * sld + 2 * step);
+    }
+  };
+  // (two column tiles of MXFP4 leave no registers for that: theirs are fetched
+  // before the wait for the tile)
+  constexpr bool kAhead = WT != kFewMxfp4 || NT == 1;
+  if (kAhead) fetch(now, q.step0);
+  for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
+    if (!kAhead) fetch(now, step);
+    if (kAhead && step + 1 < q.step1) fetch(next, step + 1);
+    const int slot = ring.n % kStages;
+    if (!ptx::wait_bounded(&ct.full[slot], (ring.n / kStages) & 1, &ct.abort)) {
       raise_status(p.status, &ct.abort, kStatusTimeout);
       return false;
     }
-    const uint32_t tile = ptx::smem_u32(stage_at<WT, RT>(sm, slot)), cols = tile + kTileBytes;
-    if constexpr (WT == kFewBf16) stage_bf16<NT>(tile, cols, acc);
-    if constexpr (WT == kFewE4m3) stage_e4m3<NT>(tile, cols, f, acc);
+    const uint32_t tile = ptx::smem_u32(sm.stages) + slot * kTileBytes;
+    if constexpr (WT == kFewBf16) stage_bf16<NT>(tile, now.b, acc);
+    if constexpr (WT == kFewE4m3) stage_e4m3<NT>(tile, now.b, now.f, acc);
     if constexpr (WT == kFewMxfp4) {
-      if (2 * step + half < sld) stage_mxfp4<NT>(tile, cols, s, acc);  // the last unit may be half of one
+      if (there(step)) stage_mxfp4<NT>(tile, now.b, now.s, now.f, acc);
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&ct.empty[slot]);
-    f = f1;
-    s[0] = s1[0];
-    s[1] = s1[1];
+    if (kAhead) now = next;
   }
   // the two halves of the steps, and the terms of each row, are joined by the
   // pair of warps that has these 16 columns
@@ -557,16 +578,21 @@ __device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q
   return true;
 }
 
-template <int WT, int RT, bool SHARED, bool DOWN>
+template <int WT, bool SHARED, bool DOWN>
 __device__ bool consume(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
   const int inner = SHARED ? p.S : p.I;
   const int K = DOWN ? inner : p.d, N = DOWN ? p.d : inner;
   return for_pieces<WT, SHARED, DOWN>(p, ls, [&](const Piece& q) {
     const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
+    auto column = [&](int n) -> const uint16_t* {
+      if (DOWN) return (SHARED ? p.h_s : p.h_r) + ((int64_t)q.first * terms(WT) + n) * K;
+      const int64_t t = SHARED ? n : ls.ent[q.first + n] / p.k;
+      return (WT == kFewBf16 ? p.x : p.x16) + t * p.d;
+    };
     const int cols = q.rows * q.group;
-    if (cols <= 8) return consume_piece<WT, RT, 1>(p, q, scales, K, N, sm, ring);
-    if (cols <= 16) return consume_piece<WT, RT, 2>(p, q, scales, K, N, sm, ring);
-    return consume_piece<WT, RT, 3>(p, q, scales, K, N, sm, ring);
+    if (cols <= 8) return consume_piece<WT, 1, DOWN>(p, q, column, scales, K, N, sm, ring);
+    if (cols <= 16 || terms(WT) == 2) return consume_piece<WT, 2, DOWN>(p, q, column, scales, K, N, sm, ring);
+    return consume_piece<WT, terms(WT) == 2 ? 2 : 3, DOWN>(p, q, column, scales, K, N, sm, ring);
   });
 }
 
@@ -786,40 +812,137 @@ __device__ __forceinline__ void terms_of(float v, uint32_t (&t)[3]) {
   t[2] = __float_as_uint(q) >> 16;
 }
 
-// h of every row, four columns a lane.
+// The power of two 2^(14 - e) for a largest magnitude of exponent e, as the
+// factor and its inverse; both normal numbers.
+__device__ __forceinline__ void fp16_factor(uint32_t top, float& factor, float& inverse) {
+  const uint32_t field = max(top >> 23, 15u);
+  factor = __uint_as_float((268u - field) << 23);
+  inverse = __uint_as_float((field - 14u) << 23);
+}
+
+// Bits of |v| where v is finite, 0 otherwise.
+__device__ __forceinline__ uint32_t finite_bits(float v) {
+  const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+  return b < 0x7f800000u ? b : 0u;
+}
+
+__device__ __forceinline__ uint32_t fp16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float fp16_lo(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)v)); }
+__device__ __forceinline__ float fp16_hi(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)(v >> 16))); }
+
+// x of this CTA's tokens in fp16, each token times a power of two, for the
+// routed experts' codes.
+template <int WT>
+__device__ void fp16_tokens(const FewParams& p, uint32_t* red) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int t = gridDim.x - 1 - blockIdx.x; t < p.T; t += gridDim.x) {
+    const uint32_t* x = reinterpret_cast<const uint32_t*>(p.x + (int64_t)t * p.d);
+    uint32_t top = 0;
+    for (int i = threadIdx.x; i < p.d / 2; i += kThreads) {
+      const uint32_t v = __ldg(x + i);
+      top = max(top, max(finite_bits(ptx::bf16_lo(v)), finite_bits(ptx::bf16_hi(v))));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) red[warp] = top;
+    consumer_sync();
+    top = red[lane & (kWarps - 1)];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float factor, inverse;
+    fp16_factor(top, factor, inverse);
+    if (threadIdx.x == 0) p.x_scale[t] = inverse;
+    for (int i = threadIdx.x; i < p.d / 2; i += kThreads) {
+      const uint32_t v = __ldg(x + i);
+      *reinterpret_cast<uint32_t*>(p.x16 + (int64_t)t * p.d + place_of<WT>(2 * i)) =
+          fp16_pair(ptx::bf16_lo(v) * factor, ptx::bf16_hi(v) * factor);
+    }
+    consumer_sync();
+  }
+}
+
+// Four values of h, columns k to k + 3, to a row's terms [terms][K].
+template <int WT>
+__device__ __forceinline__ void store_terms(uint16_t* to, int K, int k, const float (&h)[4]) {
+  uint32_t w[3][2];
+  if (WT == kFewBf16) {
+    uint32_t t[4][3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) terms_of(h[i], t[i]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      w[q][0] = t[0][q] | (t[1][q] << 16);
+      w[q][1] = t[2][q] | (t[3][q] << 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float a = h[2 * i], b = h[2 * i + 1];
+      w[0][i] = fp16_pair(a, b);
+      // the second term of an infinity or NaN is none
+      const float ra = finite_bits(a) == (__float_as_uint(a) & 0x7fffffffu) ? a - fp16_lo(w[0][i]) : 0.0f;
+      const float rb = finite_bits(b) == (__float_as_uint(b) & 0x7fffffffu) ? b - fp16_hi(w[0][i]) : 0.0f;
+      w[1][i] = fp16_pair(ra, rb);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < terms(WT); ++q)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<uint32_t*>(to + (int64_t)q * K + place_of<WT>(k + 2 * i)) = w[q][i];
+}
+
+// h of every row, four columns a lane and 128 a warp.
 template <int WT>
 __device__ void activations(const FewParams& p, const Lists& ls) {
   const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * kWarps;
+  const int warps = gridDim.x * kWarps;
   const int rows = p.T * p.k;
   const int rb = p.I / kFewCols, sb = p.S / kFewCols;
-  const int64_t jobs = (int64_t)rows * rb + (int64_t)p.T * sb;
-  const Line Lr(ls.n * 2 * rb, (p.d + Unit<WT>::kSteps - 1) / Unit<WT>::kSteps);
-  const Line Ls(2 * sb, p.d / Unit<kFewBf16>::kSteps);
-  for (int64_t job = (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x; job < jobs; job += warps) {
-    const bool shared = job >= (int64_t)rows * rb;
-    const int64_t j = shared ? job - (int64_t)rows * rb : job;
+  const int jobs = rows * rb + p.T * sb;
+  const Line Lr(ls.n * 2 * rb, (p.d + few_unit_steps(WT) - 1) / few_unit_steps(WT));
+  const Line Ls(2 * sb, p.d / few_unit_steps(kFewBf16));
+  for (int job = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; job < jobs; job += warps) {
+    const bool shared = job >= rows * rb;
+    const int j = shared ? job - rows * rb : job;
     const int blocks = shared ? sb : rb;
-    const int row = (int)(j / blocks), block = (int)(j % blocks);
+    const int row = j / blocks, block = j % blocks;
     uint32_t seg = block;
     int at = row;
+    float f = 1.0f;
     if (!shared) {
-      const int ei = ls.seg_of[ls.idx[ls.ent[row]]];
+      const int i = ls.ent[row];
+      const int ei = ls.seg_of[ls.idx[i]];
       seg += (uint32_t)(ei * 2 * blocks);
       at = row - ls.start[ei];
+      if (WT != kFewBf16) f = __ldcg(p.x_scale + i / p.k);
     }
     const float* buf = shared ? p.up_s : p.up_r;
     const Line& L = shared ? Ls : Lr;
     const float4 g = sum_pieces(buf, L, seg, p.T, at, 4 * lane);
     const float4 u = sum_pieces(buf, L, seg + blocks, p.T, at, 4 * lane);
-    const float h[4] = {gated(g.x, u.x), gated(g.y, u.y), gated(g.z, u.z), gated(g.w, u.w)};
-    uint32_t t[4][3];
+    float h[4] = {gated(g.x * f, u.x * f), gated(g.y * f, u.y * f), gated(g.z * f, u.z * f), gated(g.w * f, u.w * f)};
+    const int k = block * kFewCols + 4 * lane;
+    if (shared) {
+      store_terms<kFewBf16>(p.h_s + (int64_t)row * 3 * p.S, p.S, k, h);
+    } else {
+      if (WT != kFewBf16) {
+        uint32_t top = max(max(finite_bits(h[0]), finite_bits(h[1])), max(finite_bits(h[2]), finite_bits(h[3])));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) terms_of(h[i], t[i]);
-    uint16_t* to = p.h + (int64_t)(shared ? rows + row : row) * 3 * p.ld_h + block * kFewCols + 4 * lane;
+        for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float factor, inverse;
+        fp16_factor(top, factor, inverse);
 #pragma unroll
-    for (int q = 0; q < 3; ++q)
-      *reinterpret_cast<uint2*>(to + (int64_t)q * p.ld_h) = make_uint2(t[0][q] | (t[1][q] << 16), t[2][q] | (t[3][q] << 16));
+        for (int i = 0; i < 4; ++i) h[i] *= factor;
+        if (lane == 0) p.h_scale[(int64_t)row * rb + block] = inverse;
+      }
+      store_terms<WT>(p.h_r + (int64_t)row * terms(WT) * p.I, p.I, k, h);
+    }
   }
 }
 
@@ -829,8 +952,8 @@ __device__ void combine(const FewParams& p, const Lists& ls) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * kWarps;
   const int blocks = p.d / kFewCols;
-  const Line Lr(ls.n * blocks, (p.I + Unit<WT>::kSteps - 1) / Unit<WT>::kSteps);
-  const Line Ls(blocks, p.S > 0 ? p.S / Unit<kFewBf16>::kSteps : 1);
+  const Line Lr(ls.n * blocks, (p.I + few_unit_steps(WT) - 1) / few_unit_steps(WT));
+  const Line Ls(blocks, p.S > 0 ? p.S / few_unit_steps(kFewBf16) : 1);
   const int64_t jobs = (int64_t)p.T * blocks;
   for (int64_t job = (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x; job < jobs; job += warps) {
     const int t = (int)(job / blocks), block = (int)(job % blocks);
@@ -868,20 +991,18 @@ __global__ void __launch_bounds__(kAllThreads, 1)
   extern __shared__ uint8_t dyn[];
   __shared__ Lists ls;
   __shared__ Control ct;
-  constexpr int S = Unit<RT>::kStages;
   Smem sm;
   sm.stages = align_1024(dyn);
-  sm.red = reinterpret_cast<float*>(sm.stages + S * Unit<RT>::kBytes);
+  sm.red = reinterpret_cast<float*>(sm.stages + kStages * kTileBytes);
   sm.c = &ct;
-  double* keys = reinterpret_cast<double*>(sm.red + 8 * kRedFloats);  // the router's, or partial logits
+  double* keys = reinterpret_cast<double*>(sm.red + 8 * kRedFloats);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&ct.full[s], 1);
       ptx::mbar_init(&ct.empty[s], kWarps);
     }
     ptx::mbar_init(&ct.routed, 32 * kRouterWarps);
-    ptx::mbar_init(&ct.ready, 1);
     ct.abort = 0u;
     ct.never = 0u;
     ptx::fence_barrier_init();
@@ -894,21 +1015,20 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     // ---------------------------------------------- producer
     Ring ring;
     bool ok = true;
-    if (p.S > 0) ok = produce<kFewBf16, RT, true, false>(maps, p, ls, sm, ring, false);
+    if (p.S > 0) ok = produce<kFewBf16, true, false>(maps, p, ls, sm, ring);
     if (ok && !ptx::wait_bounded(&ct.routed, 0, abort)) {
       raise_status(p.status, abort, kStatusTimeout);
       ok = false;
     }
     ok = ok && *abort == 0;  // the router gave up: there are no lists
-    if (ok) ok = produce<RT, RT, false, false>(maps, p, ls, sm, ring, false);
-    // the routed share first: it is there in every call
-    if (ok) ok = produce<RT, RT, false, true>(maps, p, ls, sm, ring, true);
-    if (ok && p.S > 0) produce<kFewBf16, RT, true, true>(maps, p, ls, sm, ring, false);
-    // every issued copy must land before the CTA may exit (tiles that went
-    // ahead of a wait that failed have landed long before its limit)
+    if (ok) ok = produce<RT, false, false>(maps, p, ls, sm, ring);
+    if (ok) ok = produce<RT, false, true>(maps, p, ls, sm, ring);
+    if (ok && p.S > 0) produce<kFewBf16, true, true>(maps, p, ls, sm, ring);
+    // every issued copy must land before the CTA may exit
     if ((threadIdx.x & 31) == 0)
-      for (int j = ring.n > S ? ring.n - S : 0; j < ring.n; ++j)
-        if (!ptx::wait_bounded(&ct.full[j % S], (j / S) & 1, &ct.never)) raise_status(p.status, abort, kStatusTimeout);
+      for (int j = ring.n > kStages ? ring.n - kStages : 0; j < ring.n; ++j)
+        if (!ptx::wait_bounded(&ct.full[j % kStages], (j / kStages) & 1, &ct.never))
+          raise_status(p.status, abort, kStatusTimeout);
   } else if (warp > kWarps) {
     // ---------------------------------------------- router
     if (threadIdx.x == kThreads + 32) grid_poll(p.bar + 0, p.status, abort);
@@ -919,20 +1039,18 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     // ---------------------------------------------- consumers
     Ring ring;
     logits_share(p, reinterpret_cast<double*>(sm.red));
+    if (RT != kFewBf16) fp16_tokens<RT>(p, reinterpret_cast<uint32_t*>(sm.red));
     grid_arrive(p.bar + 0);
     bool ok = true;
-    if (p.S > 0) ok = consume<kFewBf16, RT, true, false>(p, ls, sm, ring);
+    if (p.S > 0) ok = consume<kFewBf16, true, false>(p, ls, sm, ring);
     ok = ok && ptx::wait_bounded(&ct.routed, 0, abort) && *abort == 0;
-    if (ok) ok = consume<RT, RT, false, false>(p, ls, sm, ring);
+    if (ok) ok = consume<RT, false, false>(p, ls, sm, ring);
     grid_arrive(p.bar + 1);
     if (grid_wait(p.bar + 1, p.status, abort)) {
       activations<RT>(p, ls);
-      ptx::fence_proxy_async_all();  // h is read by bulk copies
       grid_arrive(p.bar + 2);
       if (grid_wait(p.bar + 2, p.status, abort)) {
-        if (threadIdx.x == 0) ptx::mbar_arrive(&ct.ready);
-        if (consume<RT, RT, false, true>(p, ls, sm, ring) && p.S > 0)
-          consume<kFewBf16, RT, true, true>(p, ls, sm, ring);
+        if (consume<RT, false, true>(p, ls, sm, ring) && p.S > 0) consume<kFewBf16, true, true>(p, ls, sm, ring);
         grid_arrive(p.bar + 3);
         if (grid_wait(p.bar + 3, p.status, abort)) combine<RT>(p, ls);
       }
@@ -943,7 +1061,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
 template <int RT>
 cudaError_t launch(const FewParams& p, const FewMaps& maps, int sms, cudaStream_t stream) {
   // stages, the pairs' joins, one routing key per expert and choosing warp
-  const size_t smem = 1024 + Unit<RT>::kStages * Unit<RT>::kBytes + 8 * kRedFloats * 4 + (size_t)choosers(p.E) * p.E * 8;
+  const size_t smem = 1024 + kStages * kTileBytes + 8 * kRedFloats * 4 + (size_t)choosers(p.E) * p.E * 8;
   auto kernel = few_kernel<RT>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;

@@ -35,8 +35,12 @@ struct FewParams {
   uint32_t* bar;       // arrivals at each of the grid's barriers, zero before the launch
   float* logits;       // [T, E]
   float *up_r, *up_s, *dn_r, *dn_s;  // partial sums, [segment + CTA][row][kFewCols]
-  uint16_t* h;         // [T * k + T][3][ld_h] bf16 terms of the activations
-  int ld_h;
+  uint16_t* h_r;       // [T * k][terms][I] terms of the routed rows' activations: 3 bf16 or 2 fp16
+  uint16_t* h_s;       // [T][3][S] bf16
+  // fp16 weights' codes: x in fp16, and the powers of two that undo its and h's scaling
+  uint16_t* x16;       // [T, d]
+  float* x_scale;      // [T]
+  float* h_scale;      // [T * k][I / 128]
 };
 
 // Tensor maps of W1, W3 and W2, all with the 128-byte swizzle.  bf16: [E, K, N]

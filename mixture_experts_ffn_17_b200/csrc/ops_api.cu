@@ -31,8 +31,7 @@ P* at(void* ws, size_t off) {
 
 // ------------------------------------------------------------ few tokens
 struct FewLayout {
-  size_t logits, up_r, up_s, dn_r, dn_s, h, total;
-  int ld_h;
+  size_t logits, up_r, up_s, dn_r, dn_s, h_r, h_s, x16, x_scale, h_scale, total;
 };
 
 moe_status check_few(const moe_shape* shape) {
@@ -60,13 +59,16 @@ FewLayout few_layout(const moe_shape& s) {
     return here;
   };
   auto slots = [&](int64_t segs) { return (size_t)(segs + kFewMaxSms) * T * kFewCols * 4; };
-  L.ld_h = std::max(s.inter, s.shared_inter);
   L.logits = take((size_t)T * s.E * 4);
   L.up_r = take(slots(experts * 2 * (s.inter / kFewCols)));
   L.up_s = take(s.shared_inter ? slots(2 * (s.shared_inter / kFewCols)) : 0);
   L.dn_r = take(slots(experts * (s.d / kFewCols)));
   L.dn_s = take(s.shared_inter ? slots(s.d / kFewCols) : 0);
-  L.h = take((size_t)(T * s.k + T) * 3 * L.ld_h * 2);
+  L.h_r = take((size_t)(T * s.k) * 3 * s.inter * 2);
+  L.h_s = take((size_t)T * 3 * s.shared_inter * 2);
+  L.x16 = take((size_t)T * s.d * 2);
+  L.x_scale = take((size_t)T * 4);
+  L.h_scale = take((size_t)(T * s.k) * (s.inter / 128) * 4);
   L.total = off;
   return L;
 }
@@ -205,8 +207,11 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.up_s = at<float>(ws, L.up_s);
   p.dn_r = at<float>(ws, L.dn_r);
   p.dn_s = at<float>(ws, L.dn_s);
-  p.h = at<uint16_t>(ws, L.h);
-  p.ld_h = L.ld_h;
+  p.h_r = at<uint16_t>(ws, L.h_r);
+  p.h_s = at<uint16_t>(ws, L.h_s);
+  p.x16 = at<uint16_t>(ws, L.x16);
+  p.x_scale = at<float>(ws, L.x_scale);
+  p.h_scale = at<float>(ws, L.h_scale);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int weights = s.w_dtype == MOE_BF16 ? kFewBf16 : s.w_dtype == MOE_E4M3 ? kFewE4m3 : kFewMxfp4;
   FewMaps maps{};
