@@ -392,9 +392,7 @@ moe_status moe_forward_profiled(const moe_shape* shape, const void* x, const voi
  *     status word, as for the other calls.
  * The kernel is launched cooperatively (its CTAs, one per SM, wait for one
  * another), which a stream capture records like any other launch.
- * Errors as moe_forward; MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_TOKENS, and
- * for layers whose up projections hold 2^23 and more 128 x 128 blocks that T
- * tokens may choose. */
+ * Errors as moe_forward; MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_TOKENS. */
 #define MOE_FEW_MAX_TOKENS 16
 size_t moe_few_workspace_size(const moe_shape* shape);
 moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg, const float* bias, const void* W1,

@@ -21,13 +21,12 @@
 //
 // Split of the work.  A segment is 128 output columns of one matrix of one
 // expert, a unit the part of its contraction that one stage holds (16 KB of
-// weights: 64 steps of bf16, 128 of e4m3, 256 of MXFP4).  The units of all
-// segments lie on one line that is cut into equal shares, one a CTA, so every
-// SM streams the same number of bytes whatever the number of experts; a share's
-// part of one segment is a piece, and its sums go to slot (segment + CTA) of a
-// buffer (unique: along the line each piece raises one of the two by one).  Who
-// consumes a segment adds its pieces in CTA order: no atomics, and equal inputs
-// give equal bits.
+// weights: 64 steps of bf16, 128 of e4m3, 256 of MXFP4), a chunk a run of at most
+// 32 units of one segment.  CTAs claim chunks from a counter: SMs do not see the
+// same bandwidth (with equal shares the slowest took 290 us for what others did
+// in 230), and a claim is made a chunk ahead, so it costs nothing.  A chunk's
+// sums go to a place of its own and who needs a segment adds its chunks in order:
+// no floating-point atomics, and equal inputs give equal bits.
 //
 // Arithmetic: mma.sync m16n8k16 with the weights as the A operand (16 output
 // columns by 16 steps, ldmatrix from the stage) and the activations as B's
@@ -80,13 +79,14 @@ struct Lists {  // what the routing leaves in shared memory
   int16_t row_of[kMaxRows];   // the inverse
   int16_t expert[kMaxRows];   // distinct experts, ascending
   int16_t start[kMaxRows + 1];
-  int16_t seg_of[kMaxExperts];  // place of an expert among the distinct ones
+  int16_t place[kMaxExperts];  // of an expert among the distinct ones
   int32_t counts[kMaxExperts];
   int n;                      // distinct experts
 };
 
 struct Control {
   uint64_t full[kStages], empty[kStages];
+  int chunk[kStages];  // which chunk a stage belongs to; -1: the share is done
   uint64_t routed;  // the lists are there
   uint32_t abort, never;
 };
@@ -129,29 +129,17 @@ __device__ bool grid_wait(const uint32_t* bar, uint32_t* status, volatile uint32
   return *abort == 0;
 }
 
-// ------------------------------------------------------------ the line of units
-// The host admits only calls whose units * CTAs fit 32 bits.
-struct Line {
-  uint32_t units;
-  uint32_t steps;  // units of a segment
-  __device__ Line(int segs, int s) : units((uint32_t)segs * (uint32_t)s), steps((uint32_t)s) {}
-  __device__ uint32_t begin(uint32_t cta) const { return units * cta / gridDim.x; }
-  // the CTA whose share holds unit u
-  __device__ uint32_t owner(uint32_t u) const { return ((u + 1) * gridDim.x - 1) / units; }
-};
-
-// Sum of a segment's pieces, four columns at `col` of row `row` of `rows`.
-__device__ __forceinline__ float4 sum_pieces(const float* buf, const Line& L, uint32_t seg, int rows, int row, int col) {
-  const uint32_t u0 = seg * L.steps, u1 = u0 + L.steps;
-  const uint32_t c1 = L.owner(u1 - 1);
-  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (uint32_t c = L.owner(u0); c <= c1; ++c) {
-    if (max(L.begin(c), u0) >= min(L.begin(c + 1), u1)) continue;  // an empty share
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(buf + ((int64_t)(seg + c) * rows + row) * kFewCols + col));
-    a.x += v.x;
-    a.y += v.y;
-    a.z += v.z;
-    a.w += v.w;
+// Sum of a segment's chunks, four columns a lane.
+__device__ __forceinline__ float4 sum_parts(const float* at, int parts) {
+  const float4* v = reinterpret_cast<const float4*>(at) + (threadIdx.x & 31);
+  float4 a = __ldcg(v);
+#pragma unroll 4
+  for (int i = 1; i < parts; ++i) {
+    const float4 b = __ldcg(v + i * (kFewCols / 4));
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
   }
   return a;
 }
@@ -353,8 +341,8 @@ __device__ __forceinline__ void stage_mxfp4(uint32_t tile, const BWords<kFewMxfp
 // B columns that a row of h takes.
 __host__ __device__ constexpr int terms(int weights) { return weights == kFewBf16 ? 3 : 2; }
 
-// One pass over a piece: units [step0, step1) of 128 output columns of one
-// matrix, for `rows` rows of `group` B columns each.
+// A chunk, or one pass over it: units [step0, step1) of 128 output columns of
+// one matrix, for `rows` rows of `group` B columns each.
 struct Piece {
   int mat;     // 0: W1, 1: W3, 2: W2
   int expert;  // slice of the routed weights
@@ -362,49 +350,62 @@ struct Piece {
   int first;   // place of the first row in the list (shared expert: token)
   int rows, group;
   bool again;  // the weights are read by another pass too
-  float* out;  // [rows][128]
+  float* out;  // sums of the first row, [128]
+  int64_t ld;  // to the next row's
 };
 
-// Calls f for every pass of this CTA's share, in order, until it returns false.
 // Up projections: segments are (expert, W1 or W3, column block), the shared
 // expert sees every token in order.  Down projections: segments are (expert,
-// column block) and B holds the terms of each row's h, at most 8 rows a
-// pass (more read the weights again, from L2 mostly: only the shared expert and
-// crowded small layers have them).
-template <int WT, bool SHARED, bool DOWN, typename F>
-__device__ __forceinline__ bool for_pieces(const FewParams& p, const Lists& ls, F f) {
-  const int inner = SHARED ? p.S : p.I;
-  const int K = DOWN ? inner : p.d;
-  const int blocks = (DOWN ? p.d : inner) / kFewCols;
-  const int per_expert = DOWN ? blocks : 2 * blocks;
-  float* buf = SHARED ? (DOWN ? p.dn_s : p.up_s) : (DOWN ? p.dn_r : p.up_r);
-  const Line L((SHARED ? 1 : ls.n) * per_expert, (K + few_unit_steps(WT) - 1) / few_unit_steps(WT));
-  const uint32_t end = L.begin(blockIdx.x + 1);
-  for (uint32_t u = L.begin(blockIdx.x); u < end;) {
-    const uint32_t seg = u / L.steps;
+// column block) and B holds the terms of each row's h.  Sums lie as [row][matrix]
+// [column block][chunk of the segment][128].
+template <int WT, bool SHARED, bool DOWN>
+struct Share {
+  int K, N, blocks, steps, per_expert, total;
+  FewSplit split;
+  float* buf;
+  __device__ __forceinline__ Share(const FewParams& p, const Lists& ls) {
+    const int inner = SHARED ? p.S : p.I;
+    K = DOWN ? inner : p.d;
+    N = DOWN ? p.d : inner;
+    blocks = N / kFewCols;
+    steps = (K + few_unit_steps(WT) - 1) / few_unit_steps(WT);
+    per_expert = DOWN ? blocks : 2 * blocks;
+    split = SHARED ? (DOWN ? p.split_dn_s : p.split_up_s) : (DOWN ? p.split_dn_r : p.split_up_r);
+    buf = SHARED ? (DOWN ? p.dn_s : p.up_s) : (DOWN ? p.dn_r : p.up_r);
+    total = (SHARED ? 1 : ls.n) * per_expert * split.parts;
+  }
+  __device__ __forceinline__ Piece chunk(const FewParams& p, const Lists& ls, int id) const {
     Piece q;
-    q.step0 = (int)(u - seg * L.steps);
-    q.step1 = (int)min(L.steps, q.step0 + (end - u));
-    u += q.step1 - q.step0;
-    const int ei = (int)(seg / per_expert), in = (int)seg - ei * per_expert;
+    const int seg = id / split.parts, part = id - seg * split.parts;
+    const int ei = seg / per_expert, in = seg - ei * per_expert;
     q.mat = DOWN ? 2 : in >= blocks ? 1 : 0;
     q.col0 = (in - (q.mat == 1 ? blocks : 0)) * kFewCols;
+    q.step0 = part * split.units;
+    q.step1 = min(steps, q.step0 + split.units);
     q.expert = SHARED ? 0 : ls.expert[ei];
-    const int first = SHARED ? 0 : ls.start[ei];
-    const int all = SHARED ? p.T : ls.start[ei + 1] - ls.start[ei];
-    float* out = buf + (int64_t)(seg + blockIdx.x) * p.T * kFewCols;
-    constexpr int kPass = DOWN ? 8 : kFewMaxTokens;
+    q.first = SHARED ? 0 : ls.start[ei];
+    q.rows = SHARED ? p.T : ls.start[ei + 1] - q.first;
     q.group = DOWN ? terms(WT) : 1;
-    q.again = all > kPass;
-    for (int r0 = 0; r0 < all; r0 += kPass) {
-      q.first = first + r0;
-      q.rows = min(kPass, all - r0);
-      q.out = out + r0 * kFewCols;
-      if (!f(q)) return false;
-    }
+    q.again = q.rows > kPass;
+    q.ld = (int64_t)per_expert * split.parts * kFewCols;
+    q.out = buf + q.first * q.ld + ((int64_t)in * split.parts + part) * kFewCols;
+    return q;
   }
-  return true;
-}
+  // At most 8 rows of the down projections a pass (more read the weights again,
+  // from L2 mostly: only the shared expert and crowded small layers have them).
+  static constexpr int kPass = DOWN ? 8 : kFewMaxTokens;
+  template <typename F>
+  __device__ __forceinline__ bool passes(Piece q, F f) const {
+    const int all = q.rows;
+    for (int r0 = 0; r0 < all; r0 += kPass) {
+      q.rows = min(kPass, all - r0);
+      if (!f(q)) return false;
+      q.first += kPass;
+      q.out += kPass * q.ld;
+    }
+    return true;
+  }
+};
 
 // The ring's position: stages handed over so far.
 struct Ring {
@@ -452,28 +453,47 @@ __device__ __forceinline__ void prefetch_scales(const FewParams& p, const Piece&
 }
 
 template <int WT, bool SHARED, bool DOWN>
-__device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
+__device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring,
+                        uint32_t* counter) {
   const int lane = threadIdx.x & 31;
   const uint64_t once = ptx::policy_evict_first(), more = ptx::policy_evict_normal();
   const int inner = SHARED ? p.S : p.I;
   const int K = DOWN ? inner : p.d, N = DOWN ? p.d : inner;
   Control& c = *sm.c;
-  return for_pieces<WT, SHARED, DOWN>(p, ls, [&](const Piece& q) {
-    for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
-      const int s = ring.n % kStages;
-      if (!ptx::wait_bounded(&c.empty[s], ((ring.n / kStages) & 1) ^ 1, &c.abort)) {
-        if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
-        return false;
+  const Share<WT, SHARED, DOWN> share(p, ls);
+  auto slot_free = [&] {
+    if (ptx::wait_bounded(&c.empty[ring.n % kStages], ((ring.n / kStages) & 1) ^ 1, &c.abort)) return true;
+    if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
+    return false;
+  };
+  int id = blockIdx.x;
+  while (id < share.total) {
+    int claimed = 0;
+    if (lane == 0) claimed = (int)atomicAdd(counter, 1u) + gridDim.x;  // used after this chunk
+    const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
+      for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
+        const int s = ring.n % kStages;
+        if (!slot_free()) return false;
+        if (lane == 0) {
+          c.chunk[s] = id;
+          ptx::mbar_arrive_expect_tx(&c.full[s], kTileBytes);
+          load_tile<WT, SHARED>(m, p, q, step, sm.stages + s * kTileBytes, &c.full[s], q.again ? more : once);
+        }
+        __syncwarp();
+        prefetch_scales<WT>(p, q, step, K, N);
       }
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(&c.full[s], kTileBytes);
-        load_tile<WT, SHARED>(m, p, q, step, sm.stages + s * kTileBytes, &c.full[s], q.again ? more : once);
-      }
-      __syncwarp();
-      prefetch_scales<WT>(p, q, step, K, N);
-    }
-    return true;
-  });
+      return true;
+    });
+    if (!ok) return false;
+    id = __shfl_sync(0xffffffffu, claimed, 0);
+  }
+  if (!slot_free()) return false;
+  if (lane == 0) {
+    c.chunk[ring.n % kStages] = -1;
+    ptx::mbar_arrive(&c.full[ring.n % kStages]);
+  }
+  ++ring.n;
+  return true;
 }
 
 // ------------------------------------------------------------ consumers
@@ -572,7 +592,7 @@ __device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q
       const float* x = red + (r * q.group + t) * kRedPitch + col;
       a += x[0] + x[kMaxCols * kRedPitch];
     }
-    q.out[r * kFewCols + pair * 16 + col] = a;
+    q.out[r * q.ld + pair * 16 + col] = a;
   }
   ptx::named_barrier(1 + pair, 64);
   return true;
@@ -580,37 +600,59 @@ __device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q
 
 template <int WT, bool SHARED, bool DOWN>
 __device__ bool consume(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
-  const int inner = SHARED ? p.S : p.I;
-  const int K = DOWN ? inner : p.d, N = DOWN ? p.d : inner;
-  return for_pieces<WT, SHARED, DOWN>(p, ls, [&](const Piece& q) {
-    const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
-    auto column = [&](int n) -> const uint16_t* {
-      if (DOWN) return (SHARED ? p.h_s : p.h_r) + ((int64_t)q.first * terms(WT) + n) * K;
-      const int64_t t = SHARED ? n : ls.ent[q.first + n] / p.k;
-      return (WT == kFewBf16 ? p.x : p.x16) + t * p.d;
-    };
-    const int cols = q.rows * q.group;
-    if (cols <= 8) return consume_piece<WT, 1, DOWN>(p, q, column, scales, K, N, sm, ring);
-    if (cols <= 16 || terms(WT) == 2) return consume_piece<WT, 2, DOWN>(p, q, column, scales, K, N, sm, ring);
-    return consume_piece<WT, terms(WT) == 2 ? 2 : 3, DOWN>(p, q, column, scales, K, N, sm, ring);
-  });
+  const Share<WT, SHARED, DOWN> share(p, ls);
+  const int K = share.K, N = share.N;
+  Control& ct = *sm.c;
+  while (true) {
+    const int slot = ring.n % kStages;
+    if (!ptx::wait_bounded(&ct.full[slot], (ring.n / kStages) & 1, &ct.abort)) {
+      raise_status(p.status, &ct.abort, kStatusTimeout);
+      return false;
+    }
+    const int id = ct.chunk[slot];
+    if (id < 0) {
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&ct.empty[slot]);
+      ++ring.n;
+      return true;
+    }
+    const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
+      const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
+      auto column = [&](int n) -> const uint16_t* {
+        if (DOWN) return (SHARED ? p.h_s : p.h_r) + ((int64_t)q.first * terms(WT) + n) * K;
+        const int64_t t = SHARED ? n : ls.ent[q.first + n] / p.k;
+        return (WT == kFewBf16 ? p.x : p.x16) + t * p.d;
+      };
+      const int cols = q.rows * q.group;
+      if (cols <= 8) return consume_piece<WT, 1, DOWN>(p, q, column, scales, K, N, sm, ring);
+      if (cols <= 16 || terms(WT) == 2) return consume_piece<WT, 2, DOWN>(p, q, column, scales, K, N, sm, ring);
+      return consume_piece<WT, terms(WT) == 2 ? 2 : 3, DOWN>(p, q, column, scales, K, N, sm, ring);
+    });
+    if (!ok) return false;
+  }
 }
 
 // ------------------------------------------------------------ router
-// Logits of this CTA's experts: 8 warps an expert, sums in fp64 (the products
+// Logits of this CTA's experts: 8 warps for an expert and a few tokens, sums in fp64 (the products
 // of two bf16 values are exact there and the sum is good to 2^-53 of its
 // terms), rounded once.
 __device__ void logits_share(const FewParams& p, double* red) {
+  constexpr int kG = 4;  // tokens of a job at most; fewer where there are CTAs for it
+  const int group = min(kG, (p.E * p.T + 2 * (int)gridDim.x - 1) / (2 * (int)gridDim.x));
+  const int groups = (p.T + group - 1) / group;
   const int half = threadIdx.x >> 8, tid = threadIdx.x & 255;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nv = p.d / 8;
-  for (int e0 = blockIdx.x * 2; e0 < p.E; e0 += gridDim.x * 2) {
-    const int e = e0 + half;  // E is even
-    double acc[kFewMaxTokens];
-#pragma unroll
-    for (int t = 0; t < kFewMaxTokens; ++t) acc[t] = 0.0;
+  for (int job0 = blockIdx.x * 2; job0 < p.E * groups; job0 += gridDim.x * 2) {
+    const int job = job0 + half;  // E is even, and so is their number
+    const int e = job % p.E, t0 = job / p.E * group, n = min(group, p.T - t0);
+    double acc[kG] = {};
     for (int v = tid; v < nv; v += 256) {
       const uint4 wv = __ldg(reinterpret_cast<const uint4*>(p.Wg + (int64_t)e * p.d) + v);
+      uint4 xv[kG];
+#pragma unroll
+      for (int t = 0; t < kG; ++t)
+        if (t < n) xv[t] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(t0 + t) * p.d) + v);
       const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
       double w[8];
 #pragma unroll
@@ -619,10 +661,9 @@ __device__ void logits_share(const FewParams& p, double* red) {
         w[2 * i + 1] = (double)ptx::bf16_hi(ww[i]);
       }
 #pragma unroll
-      for (int t = 0; t < kFewMaxTokens; ++t) {
-        if (t < p.T) {
-          const uint4 xv = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.d) + v);
-          const uint32_t xx[4] = {xv.x, xv.y, xv.z, xv.w};
+      for (int t = 0; t < kG; ++t) {
+        if (t < n) {
+          const uint32_t xx[4] = {xv[t].x, xv[t].y, xv[t].z, xv[t].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             acc[t] = fma(w[2 * i], (double)ptx::bf16_lo(xx[i]), acc[t]);
@@ -632,19 +673,19 @@ __device__ void logits_share(const FewParams& p, double* red) {
       }
     }
 #pragma unroll
-    for (int t = 0; t < kFewMaxTokens; ++t) {
-      if (t < p.T) {
+    for (int t = 0; t < kG; ++t) {
+      if (t < n) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-        if (lane == 0) red[warp * kFewMaxTokens + t] = acc[t];
+        if (lane == 0) red[warp * kG + t] = acc[t];
       }
     }
     consumer_sync();
-    if (tid < p.T) {
+    if (tid < n) {
       double a = 0.0;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) a += red[(half * 8 + w) * kFewMaxTokens + tid];
-      p.logits[(int64_t)tid * p.E + e] = (float)a;
+      for (int w = 0; w < 8; ++w) a += red[(half * 8 + w) * kG + tid];
+      p.logits[(int64_t)(t0 + tid) * p.E + e] = (float)a;
     }
     consumer_sync();
   }
@@ -765,7 +806,7 @@ __device__ void route(const FewParams& p, Lists& ls, double* keys) {
         const int at = chosen + __popc(any & ((1u << lane) - 1u));
         ls.expert[at] = (int16_t)(e0 + lane);
         ls.start[at] = (int16_t)(rows + before - cnt);
-        ls.seg_of[e0 + lane] = (int16_t)at;
+        ls.place[e0 + lane] = (int16_t)at;
       }
       chosen += __popc(any);
       rows += total;
@@ -778,7 +819,7 @@ __device__ void route(const FewParams& p, Lists& ls, double* keys) {
   router_sync();
   for (int i = tid; i < n; i += kThreads) {
     const int e = ls.idx[i];
-    int at = ls.start[ls.seg_of[e]];
+    int at = ls.start[ls.place[e]];
     for (int q = 0; q < i; ++q) at += ls.idx[q] == e ? 1 : 0;
     ls.ent[at] = (int16_t)i;
     ls.row_of[i] = (int16_t)at;
@@ -905,27 +946,17 @@ __device__ void activations(const FewParams& p, const Lists& ls) {
   const int rows = p.T * p.k;
   const int rb = p.I / kFewCols, sb = p.S / kFewCols;
   const int jobs = rows * rb + p.T * sb;
-  const Line Lr(ls.n * 2 * rb, (p.d + few_unit_steps(WT) - 1) / few_unit_steps(WT));
-  const Line Ls(2 * sb, p.d / few_unit_steps(kFewBf16));
   for (int job = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; job < jobs; job += warps) {
     const bool shared = job >= rows * rb;
     const int j = shared ? job - rows * rb : job;
     const int blocks = shared ? sb : rb;
     const int row = j / blocks, block = j % blocks;
-    uint32_t seg = block;
-    int at = row;
     float f = 1.0f;
-    if (!shared) {
-      const int i = ls.ent[row];
-      const int ei = ls.seg_of[ls.idx[i]];
-      seg += (uint32_t)(ei * 2 * blocks);
-      at = row - ls.start[ei];
-      if (WT != kFewBf16) f = __ldcg(p.x_scale + i / p.k);
-    }
+    if (!shared && WT != kFewBf16) f = __ldcg(p.x_scale + ls.ent[row] / p.k);
     const float* buf = shared ? p.up_s : p.up_r;
-    const Line& L = shared ? Ls : Lr;
-    const float4 g = sum_pieces(buf, L, seg, p.T, at, 4 * lane);
-    const float4 u = sum_pieces(buf, L, seg + blocks, p.T, at, 4 * lane);
+    const int parts = shared ? p.split_up_s.parts : p.split_up_r.parts;
+    const float4 g = sum_parts(buf + ((int64_t)(row * 2) * blocks + block) * parts * kFewCols, parts);
+    const float4 u = sum_parts(buf + ((int64_t)(row * 2 + 1) * blocks + block) * parts * kFewCols, parts);
     float h[4] = {gated(g.x * f, u.x * f), gated(g.y * f, u.y * f), gated(g.z * f, u.z * f), gated(g.w * f, u.w * f)};
     const int k = block * kFewCols + 4 * lane;
     if (shared) {
@@ -947,29 +978,28 @@ __device__ void activations(const FewParams& p, const Lists& ls) {
 }
 
 // y: routed rows in slot order, then the shared expert's.
-template <int WT>
 __device__ void combine(const FewParams& p, const Lists& ls) {
   const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * kWarps;
+  const int warps = gridDim.x * kWarps;
   const int blocks = p.d / kFewCols;
-  const Line Lr(ls.n * blocks, (p.I + few_unit_steps(WT) - 1) / few_unit_steps(WT));
-  const Line Ls(blocks, p.S > 0 ? p.S / few_unit_steps(kFewBf16) : 1);
-  const int64_t jobs = (int64_t)p.T * blocks;
-  for (int64_t job = (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x; job < jobs; job += warps) {
-    const int t = (int)(job / blocks), block = (int)(job % blocks);
+  const int jobs = p.T * blocks;
+  for (int job = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; job < jobs; job += warps) {
+    const int t = job / blocks, block = job % blocks;
     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
     for (int j = 0; j < p.k; ++j) {
       const int i = t * p.k + j;
-      const int ei = ls.seg_of[ls.idx[i]];
       const float w = ls.w[i];
-      const float4 o = sum_pieces(p.dn_r, Lr, (uint32_t)(ei * blocks + block), p.T, ls.row_of[i] - ls.start[ei], 4 * lane);
+      const int parts = p.split_dn_r.parts;
+      const float4 o = sum_parts(p.dn_r + ((int64_t)ls.row_of[i] * blocks + block) * parts * kFewCols, parts);
       y.x = fmaf(w, o.x, y.x);
       y.y = fmaf(w, o.y, y.y);
       y.z = fmaf(w, o.z, y.z);
       y.w = fmaf(w, o.w, y.w);
     }
     if (p.S > 0) {
-      const float4 o = sum_pieces(p.dn_s, Ls, block, p.T, t, 4 * lane);
+      const int parts = p.split_dn_s.parts;
+      const float4 o = sum_parts(p.dn_s + ((int64_t)t * blocks + block) * parts * kFewCols, parts);
       y.x += o.x;
       y.y += o.y;
       y.z += o.z;
@@ -1015,15 +1045,15 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     // ---------------------------------------------- producer
     Ring ring;
     bool ok = true;
-    if (p.S > 0) ok = produce<kFewBf16, true, false>(maps, p, ls, sm, ring);
+    if (p.S > 0) ok = produce<kFewBf16, true, false>(maps, p, ls, sm, ring, p.bar + 4);
     if (ok && !ptx::wait_bounded(&ct.routed, 0, abort)) {
       raise_status(p.status, abort, kStatusTimeout);
       ok = false;
     }
     ok = ok && *abort == 0;  // the router gave up: there are no lists
-    if (ok) ok = produce<RT, false, false>(maps, p, ls, sm, ring);
-    if (ok) ok = produce<RT, false, true>(maps, p, ls, sm, ring);
-    if (ok && p.S > 0) produce<kFewBf16, true, true>(maps, p, ls, sm, ring);
+    if (ok) ok = produce<RT, false, false>(maps, p, ls, sm, ring, p.bar + 5);
+    if (ok) ok = produce<RT, false, true>(maps, p, ls, sm, ring, p.bar + 6);
+    if (ok && p.S > 0) produce<kFewBf16, true, true>(maps, p, ls, sm, ring, p.bar + 7);
     // every issued copy must land before the CTA may exit
     if ((threadIdx.x & 31) == 0)
       for (int j = ring.n > kStages ? ring.n - kStages : 0; j < ring.n; ++j)
@@ -1052,7 +1082,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
       if (grid_wait(p.bar + 2, p.status, abort)) {
         if (consume<RT, false, true>(p, ls, sm, ring) && p.S > 0) consume<kFewBf16, true, true>(p, ls, sm, ring);
         grid_arrive(p.bar + 3);
-        if (grid_wait(p.bar + 3, p.status, abort)) combine<RT>(p, ls);
+        if (grid_wait(p.bar + 3, p.status, abort)) combine(p, ls);
       }
     }
   }
@@ -1066,7 +1096,7 @@ cudaError_t launch(const FewParams& p, const FewMaps& maps, int sms, cudaStream_
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   void* args[] = {const_cast<FewParams*>(&p), const_cast<FewMaps*>(&maps)};
-  return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(std::min(sms, kFewMaxSms)),
+  return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(sms),
                                      dim3(kAllThreads), args, smem, stream);
 }
 

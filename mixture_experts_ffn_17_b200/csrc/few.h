@@ -9,7 +9,6 @@
 namespace moe {
 
 constexpr int kFewMaxTokens = 16;
-constexpr int kFewMaxSms = 256;  // the workspace holds partial sums for this many CTAs
 constexpr int kFewCols = 128;    // output columns of a segment
 
 // How a call's routed expert weights are held.
@@ -17,6 +16,28 @@ enum FewWeights : int { kFewBf16 = 0, kFewE4m3 = 1, kFewMxfp4 = 2 };
 
 // Steps of the contraction in a work unit: 16 KB of 128 columns' weights.
 constexpr int few_unit_steps(int weights) { return weights == kFewBf16 ? 64 : weights == kFewE4m3 ? 128 : 256; }
+
+// How a segment's units are cut into chunks.
+struct FewSplit {
+  int parts, units;  // chunks of a segment, units of a chunk (the last may have fewer)
+};
+
+// The cut for `segs` segments of `steps` units at most: about 16 chunks a CTA,
+// so that CTAs that are ahead take more of them, of 8 to 32 units (a chunk's end
+// costs about one unit's time), and a chunk a CTA where there is less work.
+// Made for 148 CTAs whatever the device, so that results do not depend on it.
+inline FewSplit few_split(int64_t segs, int steps) {
+  constexpr int64_t kCtas = 148;
+  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  if (segs < 1 || steps < 1) return FewSplit{1, 1};  // nothing to cut
+  const int64_t total = segs * steps, least = up(total, kCtas);
+  int64_t units = up(total, 16 * kCtas);
+  if (units < 8) units = least < 8 ? least : 8;
+  if (units > 32) units = 32;
+  if (units > steps) units = steps;
+  const int64_t parts = up(steps, units);
+  return FewSplit{(int)parts, (int)up(steps, parts)};
+}
 
 struct FewParams {
   int T, d, E, k, I, S;  // S = 0: no shared expert
@@ -32,9 +53,10 @@ struct FewParams {
   float* w_out;        // may be null
   int32_t* counts_out; // may be null
   uint32_t* status;
-  uint32_t* bar;       // arrivals at each of the grid's barriers, zero before the launch
+  uint32_t* bar;       // arrivals at the grid's barriers, claimed chunks (4 each); zero before the launch
+  FewSplit split_up_r, split_up_s, split_dn_r, split_dn_s;
   float* logits;       // [T, E]
-  float *up_r, *up_s, *dn_r, *dn_s;  // partial sums, [segment + CTA][row][kFewCols]
+  float *up_r, *up_s, *dn_r, *dn_s;  // the chunks' sums, [row][segment][part][kFewCols]
   uint16_t* h_r;       // [T * k][terms][I] terms of the routed rows' activations: 3 bf16 or 2 fp16
   uint16_t* h_s;       // [T][3][S] bf16
   // fp16 weights' codes: x in fp16, and the powers of two that undo its and h's scaling

@@ -30,9 +30,44 @@ P* at(void* ws, size_t off) {
   } while (0)
 
 // ------------------------------------------------------------ few tokens
+int few_weights(const moe_shape& s) {
+  return s.w_dtype == MOE_BF16 ? kFewBf16 : s.w_dtype == MOE_E4M3 ? kFewE4m3 : kFewMxfp4;
+}
+
 struct FewLayout {
+  FewSplit split_up_r, split_up_s, split_dn_r, split_dn_s;
   size_t logits, up_r, up_s, dn_r, dn_s, h_r, h_s, x16, x_scale, h_scale, total;
 };
+
+FewLayout few_layout(const moe_shape& s) {
+  FewLayout L{};
+  const int64_t T = s.T, rows = T * s.k, experts = std::min<int64_t>(s.E, rows);
+  const int unit = few_unit_steps(few_weights(s)), unit_s = few_unit_steps(kFewBf16);
+  const int64_t bi = s.inter / kFewCols, bs = s.shared_inter / kFewCols, bd = s.d / kFewCols;
+  L.split_up_r = few_split(experts * 2 * bi, (s.d + unit - 1) / unit);
+  L.split_up_s = few_split(2 * bs, s.d / unit_s);
+  L.split_dn_r = few_split(experts * bd, (s.inter + unit - 1) / unit);
+  L.split_dn_s = few_split(bd, s.shared_inter / unit_s);
+  size_t off = kAlign;  // the status word and the counters
+  auto take = [&](size_t bytes) {
+    const size_t here = off;
+    off += (bytes + kAlign - 1) / kAlign * kAlign;
+    return here;
+  };
+  auto sums = [&](int64_t segs, const FewSplit& sp) { return (size_t)(segs * sp.parts) * kFewCols * 4; };
+  L.logits = take((size_t)T * s.E * 4);
+  L.up_r = take(sums(rows * 2 * bi, L.split_up_r));
+  L.up_s = take(sums(T * 2 * bs, L.split_up_s));
+  L.dn_r = take(sums(rows * bd, L.split_dn_r));
+  L.dn_s = take(s.shared_inter > 0 ? sums(T * bd, L.split_dn_s) : 0);
+  L.h_r = take((size_t)rows * 3 * s.inter * 2);
+  L.h_s = take((size_t)T * 3 * s.shared_inter * 2);
+  L.x16 = take((size_t)T * s.d * 2);
+  L.x_scale = take((size_t)T * 4);
+  L.h_scale = take((size_t)rows * bi * 4);
+  L.total = off;
+  return L;
+}
 
 moe_status check_few(const moe_shape* shape) {
   if (!shape) return MOE_ERR_INVALID_ARG;
@@ -41,36 +76,15 @@ moe_status check_few(const moe_shape* shape) {
   const moe_status v = check_shape(&s);
   if (v != MOE_OK) return v;
   if (s.T > kFewMaxTokens) return MOE_ERR_UNSUPPORTED;
-  // the lines of work units times the CTAs have to fit 32 bits
-  const int64_t experts = std::max<int64_t>(1, std::min<int64_t>(s.E, s.T * s.k));
-  const int64_t wide = std::max(s.inter, s.shared_inter);
-  const int64_t units = experts * 2 * (wide / kFewCols) * (s.d / few_unit_steps(kFewBf16));
-  if (units * (kFewMaxSms + 1) >= (int64_t)1 << 32) return MOE_ERR_UNSUPPORTED;
+  // chunk numbers are 32 bits, with room for one claim more from every CTA
+  const FewLayout L = few_layout(*shape);
+  const int64_t experts = std::min<int64_t>(s.E, s.T * s.k), limit = (int64_t)1 << 30;
+  if (experts * 2 * (s.inter / kFewCols) * L.split_up_r.parts >= limit ||
+      experts * (s.d / kFewCols) * L.split_dn_r.parts >= limit)
+    return MOE_ERR_UNSUPPORTED;
+  // and so are the rows of the tensor maps
+  if ((int64_t)s.E * std::max(s.d, s.inter) >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
-}
-
-FewLayout few_layout(const moe_shape& s) {
-  FewLayout L{};
-  const int64_t T = s.T, experts = std::min<int64_t>(s.E, T * s.k);
-  size_t off = kAlign;  // the status word and the barriers' counters
-  auto take = [&](size_t bytes) {
-    const size_t here = off;
-    off += (bytes + kAlign - 1) / kAlign * kAlign;
-    return here;
-  };
-  auto slots = [&](int64_t segs) { return (size_t)(segs + kFewMaxSms) * T * kFewCols * 4; };
-  L.logits = take((size_t)T * s.E * 4);
-  L.up_r = take(slots(experts * 2 * (s.inter / kFewCols)));
-  L.up_s = take(s.shared_inter ? slots(2 * (s.shared_inter / kFewCols)) : 0);
-  L.dn_r = take(slots(experts * (s.d / kFewCols)));
-  L.dn_s = take(s.shared_inter ? slots(s.d / kFewCols) : 0);
-  L.h_r = take((size_t)(T * s.k) * 3 * s.inter * 2);
-  L.h_s = take((size_t)T * 3 * s.shared_inter * 2);
-  L.x16 = take((size_t)T * s.d * 2);
-  L.x_scale = take((size_t)T * 4);
-  L.h_scale = take((size_t)(T * s.k) * (s.inter / 128) * 4);
-  L.total = off;
-  return L;
 }
 
 // ------------------------------------------------------------ gradients
@@ -202,6 +216,10 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.counts_out = counts_out;
   p.status = at<uint32_t>(ws, 0);
   p.bar = at<uint32_t>(ws, 64);
+  p.split_up_r = L.split_up_r;
+  p.split_up_s = L.split_up_s;
+  p.split_dn_r = L.split_dn_r;
+  p.split_dn_s = L.split_dn_s;
   p.logits = at<float>(ws, L.logits);
   p.up_r = at<float>(ws, L.up_r);
   p.up_s = at<float>(ws, L.up_s);
@@ -213,7 +231,7 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.x_scale = at<float>(ws, L.x_scale);
   p.h_scale = at<float>(ws, L.h_scale);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int weights = s.w_dtype == MOE_BF16 ? kFewBf16 : s.w_dtype == MOE_E4M3 ? kFewE4m3 : kFewMxfp4;
+  const int weights = few_weights(s);
   FewMaps maps{};
   const void* routed[] = {W1, W3, W2};
   const void* shared[] = {W1s, W3s, W2s};

@@ -65,7 +65,8 @@ def test_few_workspace(p):
     (dict(T=17), UNSUPPORTED), (dict(T=-1), INVALID), (dict(d=200), UNSUPPORTED), (dict(E=48), UNSUPPORTED),
     (dict(k=33), INVALID), (dict(inter=0), INVALID), (dict(w_dtype=4), INVALID), (dict(w_dtype=2), INVALID),
     (dict(y_dtype=3), INVALID), (dict(route=1, n_group=3), INVALID),
-    (dict(T=16, k=16, E=256, d=1 << 16, inter=1 << 16), UNSUPPORTED),
+    (dict(T=16, k=16, E=1024, d=1 << 20, inter=1 << 20), UNSUPPORTED),
+    (dict(T=1, E=1024, inter=1 << 21), UNSUPPORTED),
 ])
 def test_few_refuses_shapes(p, bad, status):
     assert few(p, bad, bytes=1 << 40) == status
