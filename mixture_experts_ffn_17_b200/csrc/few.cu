@@ -37,12 +37,13 @@
 // columns 16 (w % 8) of a tile and one half of its steps (w / 8).
 //   bf16 weights: x is bf16 as it comes; h is fp32 and goes in as three bf16
 //   terms (8 bits each: 24 in all).
-//   e4m3 and MXFP4 codes are converted to fp16, which holds them exactly; x and h
-//   are fp16 too, times a power of two that puts the largest of a token (of 128
-//   values of h) at 2^14: a bf16 x fits exactly down to 2^-29 of the largest
-//   and to 2^-40 of it below; h goes in as two terms (22 bits).  (Converting
-//   the codes to bf16 takes 5 instructions a pair instead of 1 to 1.5, which
-//   bound the kernel: 2.0 to 2.2 TB/s.)
+//   e4m3 and MXFP4 codes become fp16, which holds them exactly, by moving their
+//   bits: exponent and mantissa read 2^-8 and 2^-14 times the code's value there,
+//   made up in the sums' factors.  (The conversion instructions run at a
+//   sixteenth of the rate: 2700 cycles a stage of MXFP4 where HBM needs 730.)
+//   x and h are fp16 too, times a power of two that puts the largest of a token
+//   (of 128 values of h) at 2^14: a bf16 x fits exactly down to 2^-29 of the
+//   largest and to 2^-40 of it below; h goes in as two terms (22 bits).
 // Block scales multiply fp32 sums.
 #include <algorithm>
 #include <cstdint>
@@ -66,7 +67,7 @@ constexpr uint32_t kTileBytes = 16384;
 
 constexpr int kStages = 10;
 
-// Router warps that choose experts at the same time (a key per expert each).
+// Router warps that choose experts at the same time (12 bytes per expert each).
 __host__ __device__ constexpr int choosers(int E) { return E <= 512 ? kRouterWarps : 2; }
 
 constexpr int kRedPitch = 17;  // floats of one B column of a warp pair's 16 output columns
@@ -175,21 +176,27 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-// e4m3 codes in bytes (0, 1) and (2, 3) to two fp16 pairs.
-__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
+// Four e4m3 codes to two fp16 pairs, bytes (0, 2) and (1, 3), times 2^-8.  The
+// code 0x7f, NaN, is not looked at (it reads 480).
+__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t& even, uint32_t& odd) {
+  even = ((w << 8) & 0x80008000u) | ((w << 7) & 0x3f803f80u);
+  odd = (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
 }
 
-// Eight MXFP4 codes to four fp16 pairs.
+// The same by the conversion instruction, NaN included.
+__device__ __forceinline__ void e4m3_pairs_nan(uint32_t w, uint32_t& even, uint32_t& odd) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(even), "=r"(odd)
+      : "r"(__byte_perm(w, 0, 0x3120)));
+}
+
+// Eight MXFP4 codes to four fp16 pairs, codes j and j + 4, times 2^-14.
 __device__ __forceinline__ void mx_pairs(uint32_t w, uint32_t (&f)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
-      : "r"(w));
+  f[0] = ((w << 12) & 0x80008000u) | ((w << 9) & 0x0e000e00u);
+  f[1] = ((w << 8) & 0x80008000u) | ((w << 5) & 0x0e000e00u);
+  f[2] = ((w << 4) & 0x80008000u) | ((w << 1) & 0x0e000e00u);
+  f[3] = (w & 0x80008000u) | ((w >> 3) & 0x0e000e00u);
 }
 
 // Whether one of a word's four bytes is 0 or 255.
@@ -207,12 +214,23 @@ __device__ __forceinline__ float scale_of(uint32_t word, int byte, bool ends) {
 
 // How B's columns lie in memory.  A lane reads the steps that it feeds to the
 // MMAs: with ldmatrix.trans, 2c, 2c + 1 of each eight; of a 32-step block of
-// MXFP4, 8c to 8c + 7.  Columns that this kernel writes are ordered so that these
-// are 16 bytes in a row: step k of a 32-step block at place_of(k).
+// MXFP4, 8c + j and 8c + j + 4 for j = 0 to 3.  Columns that this kernel writes are
+// ordered so that these are 16 bytes in a row: step k at place_of(k).
 template <int WT>
 __device__ __forceinline__ int place_of(int k) {
-  if (WT == kFewMxfp4) return k;
+  if (WT == kFewMxfp4) return (k & ~7) + 2 * (k & 3) + ((k >> 2) & 1);
   return (k & ~31) + 8 * ((k & 7) >> 1) + 2 * ((k & 31) >> 3) + (k & 1);
+}
+
+// Values k and k + 1 (k even) in a column.
+template <int WT>
+__device__ __forceinline__ void store_pair(uint16_t* column, int k, uint32_t v) {
+  if (WT == kFewMxfp4) {
+    column[place_of<WT>(k)] = (uint16_t)v;
+    column[place_of<WT>(k + 1)] = (uint16_t)(v >> 16);
+  } else {
+    *reinterpret_cast<uint32_t*>(column + place_of<WT>(k)) = v;
+  }
 }
 
 // The words of B that a lane uses of one stage, for one column tile.
@@ -268,31 +286,52 @@ __device__ __forceinline__ void stage_bf16(uint32_t tile, const BWords<kFewBf16>
 // e4m3: [steps][128 columns] codes; a 16-bit unit of ldmatrix is two columns of
 // one step, so a register holds columns 2g and 2g + 1 of steps 2c and 2c + 1.
 // f[j]: the block's scale times the columns'.
-template <int NT>
-__device__ __forceinline__ void stage_e4m3(uint32_t tile, const BWords<kFewE4m3> (&b)[NT], const float (&f)[NT],
-                                           float (&acc)[NT][4]) {
+template <int NT, bool NANS>
+__device__ __forceinline__ bool e4m3_sums(uint32_t tile, const BWords<kFewE4m3> (&b)[NT], float (&part)[NT][4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane >> 3, r = lane & 7;
-  float part[NT][4] = {};
+  uint32_t seen = 0;  // the top bit of a byte: the code 0x7f
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[j][e] = 0.0f;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int k = (warp >> 3) * 64 + 32 * q + 8 * i + r;
-    uint32_t w[4], a0[4], a1[4];
+    uint32_t w[4], a[4][2];
     ldsm_t(w, tile + k * 128 + (((warp & 7) ^ (k & 7)) << 4));
-    e4m3_pairs(__byte_perm(w[0], 0, 0x3120), a0[0], a0[1]);
-    e4m3_pairs(__byte_perm(w[1], 0, 0x3120), a0[2], a0[3]);
-    e4m3_pairs(__byte_perm(w[2], 0, 0x3120), a1[0], a1[1]);
-    e4m3_pairs(__byte_perm(w[3], 0, 0x3120), a1[2], a1[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (NANS) {
+        e4m3_pairs_nan(w[e], a[e][0], a[e][1]);
+      } else {
+        e4m3_pairs(w[e], a[e][0], a[e][1]);
+        seen |= (w[e] & 0x7f7f7f7fu) + 0x01010101u;
+      }
+    }
+    const uint32_t a0[4] = {a[0][0], a[0][1], a[1][0], a[1][1]}, a1[4] = {a[2][0], a[2][1], a[3][0], a[3][1]};
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       mma<true>(part[j], a0, b[j].w[q][0], b[j].w[q][1]);
       mma<true>(part[j], a1, b[j].w[q][2], b[j].w[q][3]);
     }
   }
+  return (seen & 0x80808080u) != 0;
+}
+
+template <int NT>
+__device__ __forceinline__ void stage_e4m3(uint32_t tile, const BWords<kFewE4m3> (&b)[NT], const float (&f)[NT],
+                                           float (&acc)[NT][4]) {
+  float part[NT][4];
+  float up = 256.0f;
+  if (__any_sync(0xffffffffu, e4m3_sums<NT, false>(tile, b, part))) {
+    e4m3_sums<NT, true>(tile, b, part);
+    up = 1.0f;
+  }
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(part[j][e], f[j], acc[j][e]);
+    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(part[j][e], f[j] * up, acc[j][e]);
 }
 
 // MXFP4: [128 columns][steps / 2] codes; lane (g, c) holds the eight codes 8c of
@@ -334,7 +373,7 @@ __device__ __forceinline__ void stage_mxfp4(uint32_t tile, const BWords<kFewMxfp
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(sum[j][e], f[j], acc[j][e]);
+    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(sum[j][e], f[j] * 16384.0f, acc[j][e]);
 }
 
 // ------------------------------------------------------------ shares and pieces
@@ -529,7 +568,7 @@ __device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q
     BWords<WT> b[NT];
     float f[NT];
     uint32_t s[2];
-  } now, next;
+  };
   auto there = [&](int step) { return WT != kFewMxfp4 || 2 * step + half < sld; };
   auto fetch = [&](Beside& x, int step) {
     if (!there(step)) return;
@@ -549,27 +588,42 @@ __device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q
       x.s[1] = __ldg(sw + 8 * sld + 2 * step);
     }
   };
-  // (two column tiles of MXFP4 leave no registers for that: theirs are fetched
-  // before the wait for the tile)
-  constexpr bool kAhead = WT != kFewMxfp4 || NT == 1;
-  if (kAhead) fetch(now, q.step0);
-  for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
-    if (!kAhead) fetch(now, step);
-    if (kAhead && step + 1 < q.step1) fetch(next, step + 1);
+  auto use = [&](const Beside& x, int step) {
     const int slot = ring.n % kStages;
     if (!ptx::wait_bounded(&ct.full[slot], (ring.n / kStages) & 1, &ct.abort)) {
       raise_status(p.status, &ct.abort, kStatusTimeout);
       return false;
     }
     const uint32_t tile = ptx::smem_u32(sm.stages) + slot * kTileBytes;
-    if constexpr (WT == kFewBf16) stage_bf16<NT>(tile, now.b, acc);
-    if constexpr (WT == kFewE4m3) stage_e4m3<NT>(tile, now.b, now.f, acc);
+    if constexpr (WT == kFewBf16) stage_bf16<NT>(tile, x.b, acc);
+    if constexpr (WT == kFewE4m3) stage_e4m3<NT>(tile, x.b, x.f, acc);
     if constexpr (WT == kFewMxfp4) {
-      if (there(step)) stage_mxfp4<NT>(tile, now.b, now.s, now.f, acc);
+      if (there(step)) stage_mxfp4<NT>(tile, x.b, x.s, x.f, acc);
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&ct.empty[slot]);
-    if (kAhead) now = next;
+    ++ring.n;
+    return true;
+  };
+  if constexpr (WT != kFewMxfp4 || NT == 1) {
+    // two buffers by name: a copy from one to the other would wait for its loads
+    Beside even, odd;
+    fetch(even, q.step0);
+    for (int step = q.step0; step < q.step1; step += 2) {
+      if (step + 1 < q.step1) fetch(odd, step + 1);
+      if (!use(even, step)) return false;
+      if (step + 1 < q.step1) {
+        if (step + 2 < q.step1) fetch(even, step + 2);
+        if (!use(odd, step + 1)) return false;
+      }
+    }
+  } else {
+    // two column tiles of MXFP4 leave no registers for that
+    for (int step = q.step0; step < q.step1; ++step) {
+      Beside x;
+      fetch(x, step);
+      if (!use(x, step)) return false;
+    }
   }
   // the two halves of the steps, and the terms of each row, are joined by the
   // pair of warps that has these 16 columns
@@ -691,81 +745,99 @@ __device__ void logits_share(const FewParams& p, double* red) {
   }
 }
 
-struct Best {
-  double key;
-  int idx;
-};
+// Doubles in the order of unsigned numbers, -0 as 0 and NaN as the lowest.
+__device__ __forceinline__ uint64_t ordered(double v) {
+  if (v != v) return 0;
+  const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+  return (b >> 63) ? ~b : b | 0x8000000000000000ull;
+}
 
-__device__ __forceinline__ Best warp_best(Best b) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double k = __shfl_xor_sync(0xffffffffu, b.key, o);
-    const int i = __shfl_xor_sync(0xffffffffu, b.idx, o);
-    if (k > b.key || (k == b.key && i < b.idx)) b = Best{k, i};
-  }
-  return b;
+__device__ __forceinline__ double of_ordered(uint64_t b) {
+  return __longlong_as_double((long long)((b >> 63) ? b & 0x7fffffffffffffffull : ~b));
+}
+
+// Lowest index among the lanes' largest keys (index 0x7fffffff: no candidate).
+__device__ __forceinline__ int warp_best(uint64_t key, int idx) {
+  const bool in = idx != 0x7fffffff;
+  const uint32_t hi = in ? (uint32_t)(key >> 32) : 0u, top = __reduce_max_sync(0xffffffffu, hi);
+  const uint32_t lo = in && hi == top ? (uint32_t)key : 0u, low = __reduce_max_sync(0xffffffffu, lo);
+  return (int)__reduce_min_sync(0xffffffffu, in && hi == top && (uint32_t)key == low ? (uint32_t)idx : 0x7fffffffu);
 }
 
 // The k experts of token t and their weights, by one warp.  Scores that decide
 // the selection are fp64 (of the fp32 logits); a NaN score ranks last.
-__device__ void choose(const FewParams& p, Lists& ls, int t, double* key) {
+__device__ void choose(const FewParams& p, Lists& ls, int t, uint64_t* key, float* logit) {
   const int lane = threadIdx.x & 31;
-  const double kLow = -__longlong_as_double(0x7ff0000000000000ll);
   const float* l = p.logits + (int64_t)t * p.E;
+#pragma unroll 8
+  for (int e = lane; e < p.E; e += 32) logit[e] = __ldcg(l + e);
   for (int e = lane; e < p.E; e += 32) {
-    const double v = (double)__ldcg(l + e);
-    double s = p.route == 0 ? v : 1.0 / (1.0 + exp(-v)) + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
-    key[e] = s != s ? kLow : s;
+    const double v = (double)logit[e];
+    key[e] = ordered(p.route == 0 ? v : 1.0 / (1.0 + exp(-v)) + (p.bias ? (double)__ldg(p.bias + e) : 0.0));
   }
   __syncwarp();
   uint32_t taken = 0;  // bit v: expert 32 v + lane is out
   if (p.route == 1) {
     const int size = p.E / p.n_group;
-    Best mine{kLow, 0x7fffffff};
+    uint64_t mine = 0;
+    int group = 0x7fffffff;
     if (lane < p.n_group) {
       uint64_t used = 0;
       double sum = 0.0;
       for (int r = 0; r < p.group_topn; ++r) {
         int bi = -1;
-        double bv = kLow;
+        uint64_t bv = 0;
         for (int i = 0; i < size; ++i)
           if (!((used >> i) & 1) && (bi < 0 || key[lane * size + i] > bv)) {
             bi = i;
             bv = key[lane * size + i];
           }
         used |= 1ull << bi;
-        sum += bv;
+        sum += bv == 0 ? -__longlong_as_double(0x7ff0000000000000ll) : of_ordered(bv);
       }
-      mine = Best{sum, lane};
+      mine = ordered(sum);
+      group = lane;
     }
     uint32_t kept = 0;
     for (int r = 0; r < p.topk_group; ++r) {
-      const Best b = warp_best(mine);
-      kept |= 1u << b.idx;
-      if (lane == b.idx) mine = Best{kLow, 0x7fffffff};
+      const int b = warp_best(mine, group);
+      kept |= 1u << b;
+      if (lane == b) group = 0x7fffffff;
     }
     for (int e = lane, v = 0; e < p.E; e += 32, ++v)
       if (!((kept >> (e / size)) & 1)) taken |= 1u << v;
   }
+  // each lane holds its best; only the lane that gave one away looks again
+  uint64_t best = 0;
+  int at = 0x7fffffff;
+  auto look = [&] {
+    at = 0x7fffffff;
+    for (int e = lane, v = 0; e < p.E; e += 32, ++v)
+      if (!((taken >> v) & 1) && (at == 0x7fffffff || key[e] > best)) {
+        best = key[e];
+        at = e;
+      }
+  };
+  look();
   int my_idx = 0;
   for (int j = 0; j < p.k; ++j) {
-    Best b{kLow, 0x7fffffff};
-    for (int e = lane, v = 0; e < p.E; e += 32, ++v)
-      if (!((taken >> v) & 1) && (key[e] > b.key || (key[e] == b.key && e < b.idx))) b = Best{key[e], e};
-    b = warp_best(b);
-    if ((b.idx & 31) == lane) taken |= 1u << (b.idx >> 5);
-    if (lane == j) my_idx = b.idx;
+    const int b = warp_best(best, at);
+    if (at == b) {
+      taken |= 1u << (b >> 5);
+      look();
+    }
+    if (lane == j) my_idx = b;
   }
   const int top = __shfl_sync(0xffffffffu, my_idx, 0);
   float w;
   if (p.route == 0) {
-    const float e = lane < p.k ? expf(__ldcg(l + my_idx) - __ldcg(l + top)) : 0.0f;
+    const float e = lane < p.k ? expf(logit[my_idx] - logit[top]) : 0.0f;
     float den = e;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
     w = e / den;
   } else {
-    const double s = lane < p.k ? 1.0 / (1.0 + exp(-(double)__ldcg(l + my_idx))) : 0.0;
+    const double s = lane < p.k ? 1.0 / (1.0 + exp(-(double)logit[my_idx])) : 0.0;
     double den = s;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
@@ -775,17 +847,18 @@ __device__ void choose(const FewParams& p, Lists& ls, int t, double* key) {
     ls.idx[t * p.k + lane] = my_idx;
     ls.w[t * p.k + lane] = w;
   }
+  __syncwarp();
 }
 
 // Routing of all tokens and the lists of chosen experts and their rows, by the
 // router's warps.
-__device__ void route(const FewParams& p, Lists& ls, double* keys) {
+__device__ void route(const FewParams& p, Lists& ls, uint64_t* keys) {
   constexpr int kThreads = 32 * kRouterWarps;
   const int tid = threadIdx.x - kAllThreads + kThreads;
   const int warp = tid >> 5, lane = tid & 31;
   for (int e = tid; e < p.E; e += kThreads) ls.counts[e] = 0;
   const int n_choose = choosers(p.E);
-  for (int t = warp; warp < n_choose && t < p.T; t += n_choose) choose(p, ls, t, keys + (int64_t)warp * p.E);
+  for (int t = warp; warp < n_choose && t < p.T; t += n_choose) choose(p, ls, t, keys + warp * p.E, reinterpret_cast<float*>(keys + n_choose * p.E) + warp * p.E);
   router_sync();
   const int n = p.T * p.k;
   for (int i = tid; i < n; i += kThreads) atomicAdd(&ls.counts[ls.idx[i]], 1);
@@ -900,8 +973,7 @@ __device__ void fp16_tokens(const FewParams& p, uint32_t* red) {
     if (threadIdx.x == 0) p.x_scale[t] = inverse;
     for (int i = threadIdx.x; i < p.d / 2; i += kThreads) {
       const uint32_t v = __ldg(x + i);
-      *reinterpret_cast<uint32_t*>(p.x16 + (int64_t)t * p.d + place_of<WT>(2 * i)) =
-          fp16_pair(ptx::bf16_lo(v) * factor, ptx::bf16_hi(v) * factor);
+      store_pair<WT>(p.x16 + (int64_t)t * p.d, 2 * i, fp16_pair(ptx::bf16_lo(v) * factor, ptx::bf16_hi(v) * factor));
     }
     consumer_sync();
   }
@@ -934,8 +1006,7 @@ __device__ __forceinline__ void store_terms(uint16_t* to, int K, int k, const fl
 #pragma unroll
   for (int q = 0; q < terms(WT); ++q)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<uint32_t*>(to + (int64_t)q * K + place_of<WT>(k + 2 * i)) = w[q][i];
+    for (int i = 0; i < 2; ++i) store_pair<WT>(to + (int64_t)q * K, k + 2 * i, w[q][i]);
 }
 
 // h of every row, four columns a lane and 128 a warp.
@@ -1025,7 +1096,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
   sm.stages = align_1024(dyn);
   sm.red = reinterpret_cast<float*>(sm.stages + kStages * kTileBytes);
   sm.c = &ct;
-  double* keys = reinterpret_cast<double*>(sm.red + 8 * kRedFloats);
+  uint64_t* keys = reinterpret_cast<uint64_t*>(sm.red + 8 * kRedFloats);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -1090,8 +1161,8 @@ __global__ void __launch_bounds__(kAllThreads, 1)
 
 template <int RT>
 cudaError_t launch(const FewParams& p, const FewMaps& maps, int sms, cudaStream_t stream) {
-  // stages, the pairs' joins, one routing key per expert and choosing warp
-  const size_t smem = 1024 + kStages * kTileBytes + 8 * kRedFloats * 4 + (size_t)choosers(p.E) * p.E * 8;
+  // stages, the pairs' joins, a routing key and a logit per expert and choosing warp
+  const size_t smem = 1024 + kStages * kTileBytes + 8 * kRedFloats * 4 + (size_t)choosers(p.E) * p.E * 12;
   auto kernel = few_kernel<RT>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
