@@ -7,7 +7,7 @@
 // With at most 16 tokens an expert sees one or two rows, so the layer is a
 // stream of the chosen experts' weights through the SMs (bound by HBM: 3 d I
 // weights an expert against 2 T operations a weight) and everything else is
-// latency to be kept out of the stream's way.  One CTA per SM, three roles:
+// latency to be kept out of the stream's way.  One CTA per SM, four roles:
 //   consumers (16 warps)  logits of a share of the experts, then the products
 //                         and the two joins, with grid barriers between them;
 //   producer (1 warp)     fills a ring of stages with weight tiles by TMA, ahead
@@ -16,7 +16,12 @@
 //                         routing and stream while it is found, and the first
 //                         tiles of the down projections are in the ring before
 //                         the barriers that the activations wait for;
-//   router (3 warps)      waits for all logits, finds the top-k (in every CTA)
+//   columns (1 warp)      follows the tiles and brings the activations that go with
+//                         them, several stages' at a time (bulk copies; copies of
+//                         single stages, 128 bytes each, cost more than the
+//                         weights: 710 instead of 455 us at T = 8 with 28 experts
+//                         of 7168 x 2048 in bf16);
+//   router (2 warps)      waits for all logits, finds the top-k (in every CTA)
 //                         and the list of chosen experts and their rows.
 //
 // Split of the work.  A segment is 128 output columns of one matrix of one
@@ -30,11 +35,9 @@
 //
 // Arithmetic: mma.sync m16n8k16 with the weights as the A operand (16 output
 // columns by 16 steps, ldmatrix from the stage) and the activations as B's
-// columns, 8 at a time, read from L2 one stage ahead (their small bulk copies
-// cost more than the weights': 710 instead of 455 us at T = 8, bf16, 28 experts
-// of 7168 x 2048).  (tcgen05 would pad the columns to 16 and could not take these
-// codes unconverted; the tensor pipe is idle either way.)  Consumer warp w takes
-// columns 16 (w % 8) of a tile and one half of its steps (w / 8).
+// columns, 8 at a time.  (tcgen05 would pad the columns to 16 and could not take
+// these codes unconverted; the tensor pipe is idle either way.)  Consumer warp w
+// takes columns 16 (w % 8) of a tile and one half of its steps (w / 8).
 //   bf16 weights: x is bf16 as it comes; h is fp32 and goes in as three bf16
 //   terms (8 bits each: 24 in all).
 //   e4m3 and MXFP4 codes become fp16, which holds them exactly, by moving their
@@ -57,18 +60,16 @@ namespace {
 
 constexpr int kWarps = 16;  // consumers
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRouterWarps = 3;  // 20 warps in all, which leaves a thread 96 registers
-constexpr int kAllThreads = kThreads + 32 + 32 * kRouterWarps;
+constexpr int kRouterWarps = 2;  // 20 warps in all, which leaves a thread 96 registers
+constexpr int kAllThreads = kThreads + 64 + 32 * kRouterWarps;
 constexpr int kMaxNT = 3;       // 8-column B tiles of one pass
 constexpr int kMaxCols = 8 * kMaxNT;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxRows = kFewMaxTokens * 32;  // T * k
 constexpr uint32_t kTileBytes = 16384;
 
-constexpr int kStages = 10;
-
-// Router warps that choose experts at the same time (12 bytes per expert each).
-__host__ __device__ constexpr int choosers(int E) { return E <= 512 ? kRouterWarps : 2; }
+constexpr int kStages = 8;
+constexpr uint32_t kColBytes = 16384;  // of a buffer of B columns; there are two
 
 constexpr int kRedPitch = 17;  // floats of one B column of a warp pair's 16 output columns
 constexpr int kRedFloats = 2 * kMaxCols * kRedPitch;  // of a pair of warps
@@ -87,6 +88,8 @@ struct Lists {  // what the routing leaves in shared memory
 
 struct Control {
   uint64_t full[kStages], empty[kStages];
+  uint64_t col_full[2], col_empty[2];
+  uint64_t ready;   // h is there, in all CTAs
   int chunk[kStages];  // which chunk a stage belongs to; -1: the share is done
   uint64_t routed;  // the lists are there
   uint32_t abort, never;
@@ -199,27 +202,39 @@ __device__ __forceinline__ void mx_pairs(uint32_t w, uint32_t (&f)[4]) {
   f[3] = (w & 0x80008000u) | ((w >> 3) & 0x0e000e00u);
 }
 
+__device__ __forceinline__ void lds(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+               : "memory");
+}
+
 // Whether one of a word's four bytes is 0 or 255.
 __device__ __forceinline__ bool has_end_byte(uint32_t w) {
   return ((((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w)) & 0x80808080u) != 0;
 }
 
-// 2^(byte - 127); the ends, 2^-127 and NaN, only where `ends` says they may be.
-__device__ __forceinline__ float scale_of(uint32_t word, int byte, bool ends) {
+// 2^(byte - 127); ENDS: 2^-127 and NaN, too.
+template <bool ENDS>
+__device__ __forceinline__ float scale_of(uint32_t word, int byte) {
   const uint32_t v = (word >> (8 * byte)) & 255u;
-  uint32_t bits = v << 23;
-  if (ends) bits = v == 0 ? 0x00400000u : v == 255u ? 0x7fffffffu : bits;
-  return __uint_as_float(bits);
+  if (ENDS && v == 0) return __uint_as_float(0x00400000u);
+  if (ENDS && v == 255u) return __uint_as_float(0x7fffffffu);
+  return __uint_as_float(v << 23);
 }
 
-// How B's columns lie in memory.  A lane reads the steps that it feeds to the
-// MMAs: with ldmatrix.trans, 2c, 2c + 1 of each eight; of a 32-step block of
-// MXFP4, 8c + j and 8c + j + 4 for j = 0 to 3.  Columns that this kernel writes are
-// ordered so that these are 16 bytes in a row: step k at place_of(k).
+// Place of step k in a column of B that this kernel writes: in order, but for
+// MXFP4 with 8c + j and 8c + j + 4 side by side, as the codes come apart.
 template <int WT>
 __device__ __forceinline__ int place_of(int k) {
   if (WT == kFewMxfp4) return (k & ~7) + 2 * (k & 3) + ((k >> 2) & 1);
-  return (k & ~31) + 8 * ((k & 7) >> 1) + 2 * ((k & 31) >> 3) + (k & 1);
+  return k;
 }
 
 // Values k and k + 1 (k even) in a column.
@@ -233,61 +248,34 @@ __device__ __forceinline__ void store_pair(uint16_t* column, int k, uint32_t v) 
   }
 }
 
-// The words of B that a lane uses of one stage, for one column tile.
-template <int WT>
-struct BWords {
-  static constexpr int kBlocks = WT == kFewBf16 ? 1 : WT == kFewE4m3 ? 2 : 4;  // of 32 steps
-  uint32_t w[kBlocks][4];
-};
-
-// raw: x as it comes (in step order), for bf16 weights.
-template <int WT>
-__device__ __forceinline__ void load_columns(BWords<WT>& b, const uint16_t* p, int step, bool raw) {
-  const int lane = threadIdx.x & 31, half = threadIdx.x >> 8, c = lane & 3;
-  constexpr int kBlocks = BWords<WT>::kBlocks;
-#pragma unroll
-  for (int i = 0; i < kBlocks; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) b.w[i][e] = 0u;
-  if (!p) return;
-  p += step * few_unit_steps(WT) + half * (32 * kBlocks);
-#pragma unroll
-  for (int i = 0; i < kBlocks; ++i) {
-    if (raw) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) b.w[i][e] = *reinterpret_cast<const uint32_t*>(p + 32 * i + 8 * e + 2 * c);
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(p + 32 * i + 8 * c);
-      b.w[i][0] = v.x;
-      b.w[i][1] = v.y;
-      b.w[i][2] = v.z;
-      b.w[i][3] = v.w;
-    }
-  }
-}
-
-// One stage of a piece: this warp's sums over its half of the steps.
+// One stage of a piece: this warp's sums over its half of the steps.  cols: the
+// stage's part of the first B column, the others `pitch` bytes apart, up to column
+// `last` (which stands in for those that do not exist: an MMA's columns do not mix).
 // bf16: two boxes of 64 columns, [steps][64 columns].
 template <int NT>
-__device__ __forceinline__ void stage_bf16(uint32_t tile, const BWords<kFewBf16> (&b)[NT], float (&acc)[NT][4]) {
+__device__ __forceinline__ void stage_bf16(uint32_t tile, uint32_t cols, int pitch, int last, float (&acc)[NT][4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane >> 3, r = lane & 7;
+  const int k0 = (warp >> 3) * 32;
+  uint32_t b[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) ldsm(b[j], cols + min(8 * j + r, last) * pitch + (k0 + 8 * i) * 2);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int k = (warp >> 3) * 32 + 16 * q + (i >> 1) * 8 + r;
+    const int k = k0 + 16 * q + (i >> 1) * 8 + r;
     const int chunk = (warp & 3) * 2 + (i & 1);
     uint32_t a[4];
     ldsm_t(a, tile + ((warp >> 2) & 1) * 8192 + k * 128 + ((chunk ^ (k & 7)) << 4));
 #pragma unroll
-    for (int j = 0; j < NT; ++j) mma<false>(acc[j], a, b[j].w[0][2 * q], b[j].w[0][2 * q + 1]);
+    for (int j = 0; j < NT; ++j) mma<false>(acc[j], a, b[j][2 * q], b[j][2 * q + 1]);
   }
 }
 
 // e4m3: [steps][128 columns] codes; a 16-bit unit of ldmatrix is two columns of
 // one step, so a register holds columns 2g and 2g + 1 of steps 2c and 2c + 1.
-// f[j]: the block's scale times the columns'.
+// True where the tile has a code 0x7f, whose sums are to be done again with NANS.
 template <int NT, bool NANS>
-__device__ __forceinline__ bool e4m3_sums(uint32_t tile, const BWords<kFewE4m3> (&b)[NT], float (&part)[NT][4]) {
+__device__ __forceinline__ bool e4m3_sums(uint32_t tile, uint32_t cols, int pitch, int last, float (&part)[NT][4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane >> 3, r = lane & 7;
   uint32_t seen = 0;  // the top bit of a byte: the code 0x7f
@@ -297,7 +285,7 @@ __device__ __forceinline__ bool e4m3_sums(uint32_t tile, const BWords<kFewE4m3> 
     for (int e = 0; e < 4; ++e) part[j][e] = 0.0f;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int k = (warp >> 3) * 64 + 32 * q + 8 * i + r;
+    const int k0 = (warp >> 3) * 64 + 32 * q, k = k0 + 8 * i + r;
     uint32_t w[4], a[4][2];
     ldsm_t(w, tile + k * 128 + (((warp & 7) ^ (k & 7)) << 4));
 #pragma unroll
@@ -312,21 +300,24 @@ __device__ __forceinline__ bool e4m3_sums(uint32_t tile, const BWords<kFewE4m3> 
     const uint32_t a0[4] = {a[0][0], a[0][1], a[1][0], a[1][1]}, a1[4] = {a[2][0], a[2][1], a[3][0], a[3][1]};
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      mma<true>(part[j], a0, b[j].w[q][0], b[j].w[q][1]);
-      mma<true>(part[j], a1, b[j].w[q][2], b[j].w[q][3]);
+      uint32_t b[4];
+      ldsm(b, cols + min(8 * j + r, last) * pitch + (k0 + 8 * i) * 2);
+      mma<true>(part[j], a0, b[0], b[1]);
+      mma<true>(part[j], a1, b[2], b[3]);
     }
   }
   return (seen & 0x80808080u) != 0;
 }
 
+// scale: the block's; f[j]: the columns' factor.
 template <int NT>
-__device__ __forceinline__ void stage_e4m3(uint32_t tile, const BWords<kFewE4m3> (&b)[NT], const float (&f)[NT],
-                                           float (&acc)[NT][4]) {
+__device__ __forceinline__ void stage_e4m3(uint32_t tile, uint32_t cols, int pitch, int last, float scale,
+                                           const float (&f)[NT], float (&acc)[NT][4]) {
   float part[NT][4];
-  float up = 256.0f;
-  if (__any_sync(0xffffffffu, e4m3_sums<NT, false>(tile, b, part))) {
-    e4m3_sums<NT, true>(tile, b, part);
-    up = 1.0f;
+  float up = 256.0f * scale;
+  if (__any_sync(0xffffffffu, e4m3_sums<NT, false>(tile, cols, pitch, last, part))) {
+    e4m3_sums<NT, true>(tile, cols, pitch, last, part);
+    up = scale;
   }
 #pragma unroll
   for (int j = 0; j < NT; ++j)
@@ -336,15 +327,12 @@ __device__ __forceinline__ void stage_e4m3(uint32_t tile, const BWords<kFewE4m3>
 
 // MXFP4: [128 columns][steps / 2] codes; lane (g, c) holds the eight codes 8c of
 // a scale block for columns g and g + 8, whose scale bytes are in s[0], s[1].
-// f[j]: the columns' factor.
-template <int NT>
-__device__ __forceinline__ void stage_mxfp4(uint32_t tile, const BWords<kFewMxfp4> (&b)[NT], const uint32_t (&s)[2],
-                                            const float (&f)[NT], float (&acc)[NT][4]) {
+template <int NT, bool ENDS>
+__device__ __forceinline__ void mxfp4_sums(uint32_t tile, uint32_t cols, int pitch, int last, const uint32_t (&s)[2],
+                                           float (&sum)[NT][4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = lane >> 3, r = lane & 7;
+  const int i = lane >> 3, r = lane & 7, g = lane >> 2, c = lane & 3;
   const int n = (warp & 7) * 16 + (i & 1) * 8 + r;
-  const bool ends = __any_sync(0xffffffffu, has_end_byte(s[0]) || has_end_byte(s[1]));
-  float sum[NT][4] = {};
 #pragma unroll
   for (int p = 0; p < 2; ++p) {  // two scale blocks
     uint32_t w[4];
@@ -357,12 +345,14 @@ __device__ __forceinline__ void stage_mxfp4(uint32_t tile, const BWords<kFewMxfp
       mx_pairs(w[2 * q], x);
       mx_pairs(w[2 * q + 1], y);
       const uint32_t a0[4] = {x[0], y[0], x[1], y[1]}, a1[4] = {x[2], y[2], x[3], y[3]};
-      const float f0 = scale_of(s[0], blk, ends), f1 = scale_of(s[1], blk, ends);
+      const float f0 = scale_of<ENDS>(s[0], blk), f1 = scale_of<ENDS>(s[1], blk);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
+        uint32_t b[4];
+        lds(b, cols + min(8 * j + g, last) * pitch + ((warp >> 3) * 128 + blk * 32 + 8 * c) * 2);
         float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        mma<true>(part, a0, b[j].w[blk][0], b[j].w[blk][1]);
-        mma<true>(part, a1, b[j].w[blk][2], b[j].w[blk][3]);
+        mma<true>(part, a0, b[0], b[1]);
+        mma<true>(part, a1, b[2], b[3]);
         sum[j][0] = fmaf(part[0], f0, sum[j][0]);
         sum[j][1] = fmaf(part[1], f0, sum[j][1]);
         sum[j][2] = fmaf(part[2], f1, sum[j][2]);
@@ -370,6 +360,16 @@ __device__ __forceinline__ void stage_mxfp4(uint32_t tile, const BWords<kFewMxfp
       }
     }
   }
+}
+
+template <int NT>
+__device__ __forceinline__ void stage_mxfp4(uint32_t tile, uint32_t cols, int pitch, int last, const uint32_t (&s)[2],
+                                            const float (&f)[NT], float (&acc)[NT][4]) {
+  float sum[NT][4] = {};
+  if (__any_sync(0xffffffffu, has_end_byte(s[0]) || has_end_byte(s[1])))
+    mxfp4_sums<NT, true>(tile, cols, pitch, last, s, sum);
+  else
+    mxfp4_sums<NT, false>(tile, cols, pitch, last, s, sum);
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -446,13 +446,30 @@ struct Share {
   }
 };
 
-// The ring's position: stages handed over so far.
+// How many units' columns a buffer takes for a piece, and the columns' distance
+// in bytes: a pad keeps the reads of 8 columns off each other's banks.
+template <int WT>
+struct ColumnPlan {
+  static constexpr int kUnitBytes = 2 * few_unit_steps(WT);
+  static constexpr int kPad = WT == kFewMxfp4 ? 64 : 16;
+  int units, pitch;
+  __device__ __forceinline__ explicit ColumnPlan(const Piece& q) {
+    const int cols = q.rows * q.group;
+    units = min(q.step1 - q.step0, ((int)kColBytes / cols - kPad) / kUnitBytes);
+    pitch = units * kUnitBytes + kPad;
+  }
+};
+// every piece has room for one unit's columns
+static_assert((int)kColBytes / kMaxCols >= 2 * 64 + 16 && (int)kColBytes / 16 >= 2 * 256 + 64, "B columns");
+
+// The rings' positions: stages and column buffers handed over so far.
 struct Ring {
-  int n = 0;
+  int n = 0, cols = 0;
 };
 
 struct Smem {
   uint8_t* stages;
+  uint8_t* cols;
   float* red;
   Control* c;
 };
@@ -535,19 +552,74 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
   return true;
 }
 
+// ------------------------------------------------------------ columns
+template <int WT, bool SHARED, bool DOWN>
+__device__ bool bring_columns(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
+  constexpr int kSteps = few_unit_steps(WT);
+  const int lane = threadIdx.x & 31;
+  const Share<WT, SHARED, DOWN> share(p, ls);
+  Control& c = *sm.c;
+  auto wait = [&](uint64_t* bar, int n) {
+    if (ptx::wait_bounded(bar, n & 1, &c.abort)) return true;
+    if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
+    return false;
+  };
+  // a stage is also released by this warp, so that its chunk is still to be read
+  auto next_stage = [&] {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&c.empty[ring.n % kStages]);
+    ++ring.n;
+  };
+  while (true) {
+    if (!wait(&c.full[ring.n % kStages], ring.n / kStages)) return false;
+    const int id = c.chunk[ring.n % kStages];
+    if (id < 0) {
+      next_stage();
+      return true;
+    }
+    const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
+      const ColumnPlan<WT> plan(q);
+      const int cols = q.rows * q.group;
+      const uint16_t* src = nullptr;
+      if (lane < cols) {
+        if (DOWN)
+          src = (SHARED ? p.h_s : p.h_r) + ((int64_t)q.first * terms(WT) + lane) * share.K;
+        else
+          src = (WT == kFewBf16 ? p.x : p.x16) + (int64_t)(SHARED ? lane : ls.ent[q.first + lane] / p.k) * p.d;
+      }
+      for (int step = q.step0; step < q.step1; ++step) {
+        if ((step - q.step0) % plan.units == 0) {
+          const int buf = ring.cols & 1;
+          if (!wait(&c.col_empty[buf], (ring.cols >> 1) + 1)) return false;
+          const int last = min(q.step1, step + plan.units);
+          const uint32_t bytes = 2 * (min(share.K, last * kSteps) - step * kSteps);
+          if (lane == 0) ptx::mbar_arrive_expect_tx(&c.col_full[buf], bytes * cols);
+          __syncwarp();
+          if (lane < cols)
+            bulk_load(ptx::smem_u32(sm.cols) + buf * kColBytes + lane * plan.pitch, src + step * kSteps, bytes,
+                      &c.col_full[buf]);
+          ++ring.cols;
+        }
+        if (!wait(&c.full[ring.n % kStages], ring.n / kStages)) return false;
+        next_stage();
+      }
+      return true;
+    });
+    if (!ok) return false;
+  }
+}
+
 // ------------------------------------------------------------ consumers
-template <int WT, int NT, bool DOWN, typename F>
-__device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q, F column, const uint8_t* scales,
-                                              int K, int N, const Smem& sm, Ring& ring) {
+template <int WT, int NT, bool DOWN>
+__device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q, const uint8_t* scales, int K, int N,
+                                              const Smem& sm, Ring& ring) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3, half = warp >> 3;
   Control& ct = *sm.c;
   float acc[NT][4] = {};
-  const uint16_t* bp[NT];
   const float* hp[NT];  // factors of the row that columns 2c and 2c + 1 belong to
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    bp[j] = 8 * j + g < q.rows * q.group ? column(8 * j + g) : nullptr;
     const bool in = DOWN && WT != kFewBf16 && 4 * j + c < q.rows;
     hp[j] = in ? p.h_scale + (int64_t)(q.first + 4 * j + c) * (K / 128) : nullptr;
   }
@@ -562,67 +634,71 @@ __device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q
     sw = reinterpret_cast<const uint32_t*>(scales) +
          ((int64_t)q.expert * N + q.col0 + (warp & 7) * 16 + g) * sld + half;
   }
-  // what a unit needs beside its tile is fetched while the one before it is
-  // multiplied; of MXFP4's last unit there may be one half only
+  // scales and factors are fetched while the unit before is multiplied; of
+  // MXFP4's last unit there may be one half only
   struct Beside {
-    BWords<WT> b[NT];
     float f[NT];
+    float scale;
     uint32_t s[2];
   };
   auto there = [&](int step) { return WT != kFewMxfp4 || 2 * step + half < sld; };
   auto fetch = [&](Beside& x, int step) {
     if (!there(step)) return;
+    if constexpr (WT != kFewBf16) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      load_columns<WT>(x.b[j], bp[j], step, WT == kFewBf16 && !DOWN);
-      x.f[j] = 1.0f;
-      if (DOWN && WT != kFewBf16 && hp[j]) x.f[j] = hp[j][WT == kFewMxfp4 ? 2 * step + half : step];
+      for (int j = 0; j < NT; ++j) {
+        x.f[j] = 1.0f;
+        if (DOWN && hp[j]) x.f[j] = hp[j][WT == kFewMxfp4 ? 2 * step + half : step];
+      }
     }
-    if constexpr (WT == kFewE4m3) {
-      const float f = __ldg(sf + step * sld);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) x.f[j] *= f;
-    }
+    if constexpr (WT == kFewE4m3) x.scale = __ldg(sf + step * sld);
     if constexpr (WT == kFewMxfp4) {
       x.s[0] = __ldg(sw + 2 * step);
       x.s[1] = __ldg(sw + 8 * sld + 2 * step);
     }
   };
+  const ColumnPlan<WT> plan(q);
+  const int last = q.rows * q.group - 1;
+  int left = 0;  // units whose columns are in the buffer
+  uint32_t cols = 0;
+  auto fail = [&] {
+    raise_status(p.status, &ct.abort, kStatusTimeout);
+    return false;
+  };
   auto use = [&](const Beside& x, int step) {
+    if (left == 0) {
+      const int buf = ring.cols & 1;
+      if (!ptx::wait_bounded(&ct.col_full[buf], (ring.cols >> 1) & 1, &ct.abort)) return fail();
+      cols = ptx::smem_u32(sm.cols) + buf * kColBytes;
+      left = min(plan.units, q.step1 - step);
+    }
     const int slot = ring.n % kStages;
-    if (!ptx::wait_bounded(&ct.full[slot], (ring.n / kStages) & 1, &ct.abort)) {
-      raise_status(p.status, &ct.abort, kStatusTimeout);
-      return false;
-    }
+    if (!ptx::wait_bounded(&ct.full[slot], (ring.n / kStages) & 1, &ct.abort)) return fail();
     const uint32_t tile = ptx::smem_u32(sm.stages) + slot * kTileBytes;
-    if constexpr (WT == kFewBf16) stage_bf16<NT>(tile, x.b, acc);
-    if constexpr (WT == kFewE4m3) stage_e4m3<NT>(tile, x.b, x.f, acc);
+    if constexpr (WT == kFewBf16) stage_bf16<NT>(tile, cols, plan.pitch, last, acc);
+    if constexpr (WT == kFewE4m3) stage_e4m3<NT>(tile, cols, plan.pitch, last, x.scale, x.f, acc);
     if constexpr (WT == kFewMxfp4) {
-      if (there(step)) stage_mxfp4<NT>(tile, x.b, x.s, x.f, acc);
+      if (there(step)) stage_mxfp4<NT>(tile, cols, plan.pitch, last, x.s, x.f, acc);
     }
+    cols += ColumnPlan<WT>::kUnitBytes;
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&ct.empty[slot]);
     ++ring.n;
+    if (--left == 0) {
+      if (lane == 0) ptx::mbar_arrive(&ct.col_empty[ring.cols & 1]);
+      ++ring.cols;
+    }
     return true;
   };
-  if constexpr (WT != kFewMxfp4 || NT == 1) {
-    // two buffers by name: a copy from one to the other would wait for its loads
-    Beside even, odd;
-    fetch(even, q.step0);
-    for (int step = q.step0; step < q.step1; step += 2) {
-      if (step + 1 < q.step1) fetch(odd, step + 1);
-      if (!use(even, step)) return false;
-      if (step + 1 < q.step1) {
-        if (step + 2 < q.step1) fetch(even, step + 2);
-        if (!use(odd, step + 1)) return false;
-      }
-    }
-  } else {
-    // two column tiles of MXFP4 leave no registers for that
-    for (int step = q.step0; step < q.step1; ++step) {
-      Beside x;
-      fetch(x, step);
-      if (!use(x, step)) return false;
+  // two buffers by name: a copy from one to the other would wait for its loads
+  Beside even, odd;
+  fetch(even, q.step0);
+  for (int step = q.step0; step < q.step1; step += 2) {
+    if (step + 1 < q.step1) fetch(odd, step + 1);
+    if (!use(even, step)) return false;
+    if (step + 1 < q.step1) {
+      if (step + 2 < q.step1) fetch(even, step + 2);
+      if (!use(odd, step + 1)) return false;
     }
   }
   // the two halves of the steps, and the terms of each row, are joined by the
@@ -672,15 +748,10 @@ __device__ bool consume(const FewParams& p, const Lists& ls, const Smem& sm, Rin
     }
     const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
       const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
-      auto column = [&](int n) -> const uint16_t* {
-        if (DOWN) return (SHARED ? p.h_s : p.h_r) + ((int64_t)q.first * terms(WT) + n) * K;
-        const int64_t t = SHARED ? n : ls.ent[q.first + n] / p.k;
-        return (WT == kFewBf16 ? p.x : p.x16) + t * p.d;
-      };
       const int cols = q.rows * q.group;
-      if (cols <= 8) return consume_piece<WT, 1, DOWN>(p, q, column, scales, K, N, sm, ring);
-      if (cols <= 16 || terms(WT) == 2) return consume_piece<WT, 2, DOWN>(p, q, column, scales, K, N, sm, ring);
-      return consume_piece<WT, terms(WT) == 2 ? 2 : 3, DOWN>(p, q, column, scales, K, N, sm, ring);
+      if (cols <= 8) return consume_piece<WT, 1, DOWN>(p, q, scales, K, N, sm, ring);
+      if (cols <= 16 || terms(WT) == 2) return consume_piece<WT, 2, DOWN>(p, q, scales, K, N, sm, ring);
+      return consume_piece<WT, terms(WT) == 2 ? 2 : 3, DOWN>(p, q, scales, K, N, sm, ring);
     });
     if (!ok) return false;
   }
@@ -857,8 +928,8 @@ __device__ void route(const FewParams& p, Lists& ls, uint64_t* keys) {
   const int tid = threadIdx.x - kAllThreads + kThreads;
   const int warp = tid >> 5, lane = tid & 31;
   for (int e = tid; e < p.E; e += kThreads) ls.counts[e] = 0;
-  const int n_choose = choosers(p.E);
-  for (int t = warp; warp < n_choose && t < p.T; t += n_choose) choose(p, ls, t, keys + warp * p.E, reinterpret_cast<float*>(keys + n_choose * p.E) + warp * p.E);
+  for (int t = warp; t < p.T; t += kRouterWarps)
+    choose(p, ls, t, keys + warp * p.E, reinterpret_cast<float*>(keys + kRouterWarps * p.E) + warp * p.E);
   router_sync();
   const int n = p.T * p.k;
   for (int i = tid; i < n; i += kThreads) atomicAdd(&ls.counts[ls.idx[i]], 1);
@@ -1094,15 +1165,21 @@ __global__ void __launch_bounds__(kAllThreads, 1)
   __shared__ Control ct;
   Smem sm;
   sm.stages = align_1024(dyn);
-  sm.red = reinterpret_cast<float*>(sm.stages + kStages * kTileBytes);
+  sm.cols = sm.stages + kStages * kTileBytes;
+  sm.red = reinterpret_cast<float*>(sm.cols + 2 * kColBytes);
   sm.c = &ct;
   uint64_t* keys = reinterpret_cast<uint64_t*>(sm.red + 8 * kRedFloats);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&ct.full[s], 1);
-      ptx::mbar_init(&ct.empty[s], kWarps);
+      ptx::mbar_init(&ct.empty[s], kWarps + 1);
     }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&ct.col_full[b], 1);
+      ptx::mbar_init(&ct.col_empty[b], kWarps);
+    }
+    ptx::mbar_init(&ct.ready, 1);
     ptx::mbar_init(&ct.routed, 32 * kRouterWarps);
     ct.abort = 0u;
     ct.never = 0u;
@@ -1130,9 +1207,29 @@ __global__ void __launch_bounds__(kAllThreads, 1)
       for (int j = ring.n > kStages ? ring.n - kStages : 0; j < ring.n; ++j)
         if (!ptx::wait_bounded(&ct.full[j % kStages], (j / kStages) & 1, &ct.never))
           raise_status(p.status, abort, kStatusTimeout);
+  } else if (warp == kWarps + 1) {
+    // ---------------------------------------------- columns
+    Ring ring;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar) {
+      if (ptx::wait_bounded(bar, 0, abort) && *abort == 0) {
+        ptx::fence_proxy_async_all();  // x in fp16, and h, were written by ordinary stores
+        return true;
+      }
+      raise_status(p.status, abort, kStatusTimeout);
+      return false;
+    };
+    if (p.S > 0) ok = bring_columns<kFewBf16, true, false>(p, ls, sm, ring);
+    ok = ok && wait(&ct.routed) && bring_columns<RT, false, false>(p, ls, sm, ring);
+    ok = ok && wait(&ct.ready) && bring_columns<RT, false, true>(p, ls, sm, ring);
+    if (ok && p.S > 0) bring_columns<kFewBf16, true, true>(p, ls, sm, ring);
+    // every issued copy must land before the CTA may exit
+    for (int j = ring.cols > 2 ? ring.cols - 2 : 0; j < ring.cols; ++j)
+      if (!ptx::wait_bounded(&ct.col_full[j & 1], (j >> 1) & 1, &ct.never))
+        raise_status(p.status, abort, kStatusTimeout);
   } else if (warp > kWarps) {
     // ---------------------------------------------- router
-    if (threadIdx.x == kThreads + 32) grid_poll(p.bar + 0, p.status, abort);
+    if (threadIdx.x == kThreads + 64) grid_poll(p.bar + 0, p.status, abort);
     router_sync();
     if (*abort == 0) route(p, ls, keys);
     ptx::mbar_arrive(&ct.routed);
@@ -1140,7 +1237,10 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     // ---------------------------------------------- consumers
     Ring ring;
     logits_share(p, reinterpret_cast<double*>(sm.red));
-    if (RT != kFewBf16) fp16_tokens<RT>(p, reinterpret_cast<uint32_t*>(sm.red));
+    if (RT != kFewBf16) {
+      fp16_tokens<RT>(p, reinterpret_cast<uint32_t*>(sm.red));
+      ptx::fence_proxy_async_all();  // bulk copies will read them
+    }
     grid_arrive(p.bar + 0);
     bool ok = true;
     if (p.S > 0) ok = consume<kFewBf16, true, false>(p, ls, sm, ring);
@@ -1149,8 +1249,10 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     grid_arrive(p.bar + 1);
     if (grid_wait(p.bar + 1, p.status, abort)) {
       activations<RT>(p, ls);
+      ptx::fence_proxy_async_all();  // bulk copies will read h
       grid_arrive(p.bar + 2);
       if (grid_wait(p.bar + 2, p.status, abort)) {
+        if (threadIdx.x == 0) ptx::mbar_arrive(&ct.ready);
         if (consume<RT, false, true>(p, ls, sm, ring) && p.S > 0) consume<kFewBf16, true, true>(p, ls, sm, ring);
         grid_arrive(p.bar + 3);
         if (grid_wait(p.bar + 3, p.status, abort)) combine(p, ls);
@@ -1161,8 +1263,8 @@ __global__ void __launch_bounds__(kAllThreads, 1)
 
 template <int RT>
 cudaError_t launch(const FewParams& p, const FewMaps& maps, int sms, cudaStream_t stream) {
-  // stages, the pairs' joins, a routing key and a logit per expert and choosing warp
-  const size_t smem = 1024 + kStages * kTileBytes + 8 * kRedFloats * 4 + (size_t)choosers(p.E) * p.E * 12;
+  // stages, the pairs' joins, the columns, a routing key and a logit per expert and router warp
+  const size_t smem = 1024 + kStages * kTileBytes + 2 * kColBytes + 8 * kRedFloats * 4 + (size_t)kRouterWarps * p.E * 12;
   auto kernel = few_kernel<RT>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
