@@ -133,17 +133,24 @@ __device__ bool grid_wait(const uint32_t* bar, uint32_t* status, volatile uint32
   return *abort == 0;
 }
 
-// Sum of a segment's chunks, four columns a lane.
+// Sum of a segment's chunks in order, four columns a lane, eight loads at a time.
 __device__ __forceinline__ float4 sum_parts(const float* at, int parts) {
   const float4* v = reinterpret_cast<const float4*>(at) + (threadIdx.x & 31);
-  float4 a = __ldcg(v);
-#pragma unroll 4
-  for (int i = 1; i < parts; ++i) {
-    const float4 b = __ldcg(v + i * (kFewCols / 4));
-    a.x += b.x;
-    a.y += b.y;
-    a.z += b.z;
-    a.w += b.w;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i = 0; i < parts; i += 8) {
+    float4 b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < parts) b[j] = __ldcg(v + (i + j) * (kFewCols / 4));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (i + j < parts) {
+        a.x += b[j].x;
+        a.y += b[j].y;
+        a.z += b[j].z;
+        a.w += b[j].w;
+      }
+    }
   }
   return a;
 }
@@ -215,18 +222,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-// Whether one of a word's four bytes is 0 or 255.
-__device__ __forceinline__ bool has_end_byte(uint32_t w) {
-  return ((((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w)) & 0x80808080u) != 0;
-}
-
-// 2^(byte - 127); ENDS: 2^-127 and NaN, too.
-template <bool ENDS>
-__device__ __forceinline__ float scale_of(uint32_t word, int byte) {
-  const uint32_t v = (word >> (8 * byte)) & 255u;
-  if (ENDS && v == 0) return __uint_as_float(0x00400000u);
-  if (ENDS && v == 255u) return __uint_as_float(0x7fffffffu);
-  return __uint_as_float(v << 23);
+// Four scale bytes as 2^(byte - 127), 255 as NaN: through bf16, which holds them all.
+__device__ __forceinline__ void scales_of(uint32_t w, float (&f)[4]) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %0, l;\n\tcvt.rn.bf16x2.ue8m0x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+  f[0] = ptx::bf16_lo(lo);
+  f[1] = ptx::bf16_hi(lo);
+  f[2] = ptx::bf16_lo(hi);
+  f[3] = ptx::bf16_hi(hi);
 }
 
 // Place of step k in a column of B that this kernel writes: in order, but for
@@ -278,7 +284,7 @@ template <int NT, bool NANS>
 __device__ __forceinline__ bool e4m3_sums(uint32_t tile, uint32_t cols, int pitch, int last, float (&part)[NT][4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane >> 3, r = lane & 7;
-  uint32_t seen = 0;  // the top bit of a byte: the code 0x7f
+  uint32_t seen = 0;  // a byte's top bit, which adding 1 flips where the seven others are set
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -294,7 +300,7 @@ __device__ __forceinline__ bool e4m3_sums(uint32_t tile, uint32_t cols, int pitc
         e4m3_pairs_nan(w[e], a[e][0], a[e][1]);
       } else {
         e4m3_pairs(w[e], a[e][0], a[e][1]);
-        seen |= (w[e] & 0x7f7f7f7fu) + 0x01010101u;
+        seen |= (w[e] + 0x01010101u) ^ w[e];
       }
     }
     const uint32_t a0[4] = {a[0][0], a[0][1], a[1][0], a[1][1]}, a1[4] = {a[2][0], a[2][1], a[3][0], a[3][1]};
@@ -327,12 +333,17 @@ __device__ __forceinline__ void stage_e4m3(uint32_t tile, uint32_t cols, int pit
 
 // MXFP4: [128 columns][steps / 2] codes; lane (g, c) holds the eight codes 8c of
 // a scale block for columns g and g + 8, whose scale bytes are in s[0], s[1].
-template <int NT, bool ENDS>
-__device__ __forceinline__ void mxfp4_sums(uint32_t tile, uint32_t cols, int pitch, int last, const uint32_t (&s)[2],
-                                           float (&sum)[NT][4]) {
+// f[j]: the columns' factor.
+template <int NT>
+__device__ __forceinline__ void stage_mxfp4(uint32_t tile, uint32_t cols, int pitch, int last, const uint32_t (&s)[2],
+                                            const float (&f)[NT], float (&acc)[NT][4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane >> 3, r = lane & 7, g = lane >> 2, c = lane & 3;
   const int n = (warp & 7) * 16 + (i & 1) * 8 + r;
+  float sum[NT][4] = {};
+  float s0[4], s1[4];
+  scales_of(s[0], s0);
+  scales_of(s[1], s1);
 #pragma unroll
   for (int p = 0; p < 2; ++p) {  // two scale blocks
     uint32_t w[4];
@@ -345,7 +356,6 @@ __device__ __forceinline__ void mxfp4_sums(uint32_t tile, uint32_t cols, int pit
       mx_pairs(w[2 * q], x);
       mx_pairs(w[2 * q + 1], y);
       const uint32_t a0[4] = {x[0], y[0], x[1], y[1]}, a1[4] = {x[2], y[2], x[3], y[3]};
-      const float f0 = scale_of<ENDS>(s[0], blk), f1 = scale_of<ENDS>(s[1], blk);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         uint32_t b[4];
@@ -353,23 +363,13 @@ __device__ __forceinline__ void mxfp4_sums(uint32_t tile, uint32_t cols, int pit
         float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         mma<true>(part, a0, b[0], b[1]);
         mma<true>(part, a1, b[2], b[3]);
-        sum[j][0] = fmaf(part[0], f0, sum[j][0]);
-        sum[j][1] = fmaf(part[1], f0, sum[j][1]);
-        sum[j][2] = fmaf(part[2], f1, sum[j][2]);
-        sum[j][3] = fmaf(part[3], f1, sum[j][3]);
+        sum[j][0] = fmaf(part[0], s0[blk], sum[j][0]);
+        sum[j][1] = fmaf(part[1], s0[blk], sum[j][1]);
+        sum[j][2] = fmaf(part[2], s1[blk], sum[j][2]);
+        sum[j][3] = fmaf(part[3], s1[blk], sum[j][3]);
       }
     }
   }
-}
-
-template <int NT>
-__device__ __forceinline__ void stage_mxfp4(uint32_t tile, uint32_t cols, int pitch, int last, const uint32_t (&s)[2],
-                                            const float (&f)[NT], float (&acc)[NT][4]) {
-  float sum[NT][4] = {};
-  if (__any_sync(0xffffffffu, has_end_byte(s[0]) || has_end_byte(s[1])))
-    mxfp4_sums<NT, true>(tile, cols, pitch, last, s, sum);
-  else
-    mxfp4_sums<NT, false>(tile, cols, pitch, last, s, sum);
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -570,10 +570,10 @@ __device__ bool bring_columns(const FewParams& p, const Lists& ls, const Smem& s
     if (lane == 0) ptx::mbar_arrive(&c.empty[ring.n % kStages]);
     ++ring.n;
   };
+  int id = blockIdx.x < share.total ? (int)blockIdx.x : -1;  // the first chunk needs no tile to be known by
   while (true) {
-    if (!wait(&c.full[ring.n % kStages], ring.n / kStages)) return false;
-    const int id = c.chunk[ring.n % kStages];
     if (id < 0) {
+      if (!wait(&c.full[ring.n % kStages], ring.n / kStages)) return false;
       next_stage();
       return true;
     }
@@ -605,7 +605,8 @@ __device__ bool bring_columns(const FewParams& p, const Lists& ls, const Smem& s
       }
       return true;
     });
-    if (!ok) return false;
+    if (!ok || !wait(&c.full[ring.n % kStages], ring.n / kStages)) return false;
+    id = c.chunk[ring.n % kStages];
   }
 }
 
@@ -1192,6 +1193,10 @@ __global__ void __launch_bounds__(kAllThreads, 1)
   if (warp == kWarps) {
     // ---------------------------------------------- producer
     Ring ring;
+    if ((threadIdx.x & 31) < 3) {
+      ptx::prefetch_tmap(&maps.routed[threadIdx.x & 31]);
+      if (p.S > 0) ptx::prefetch_tmap(&maps.shared[threadIdx.x & 31]);
+    }
     bool ok = true;
     if (p.S > 0) ok = produce<kFewBf16, true, false>(maps, p, ls, sm, ring, p.bar + 4);
     if (ok && !ptx::wait_bounded(&ct.routed, 0, abort)) {
