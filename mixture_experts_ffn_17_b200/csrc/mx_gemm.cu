@@ -94,23 +94,32 @@ __device__ __forceinline__ int64_t segment(const MxProduct& p, int e, int64_t* s
   return a < 0 || b > p.rows || b < a ? 0 : b - a;
 }
 
-__device__ bool tile_at(const MxProduct& p, const Shared& sh, int t, Tile& out) {
-  const int nb = p.N / kM;
-  const int tt = t / nb;
-  int lo = 0, hi = p.E - 1;  // the expert whose tiles hold tt
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (sh.first[mid] <= tt) lo = mid; else hi = mid - 1;
+// The CTA's tiles: every gridDim.x-th, by steps instead of divisions and searches
+// (each role walks them in its own single thread or warps).
+struct Walk {
+  int t, tt, nb, e;  // tile, token tile, column block, expert
+  __device__ __forceinline__ Walk(const MxProduct& p) : t(blockIdx.x), e(0) {
+    tt = t / (p.N / kM);
+    nb = t - tt * (p.N / kM);
   }
-  int64_t start;
-  const int64_t rows = segment(p, lo, &start);
-  const int64_t skip = (int64_t)(tt - sh.first[lo]) * kTok;
-  out.e = lo;
-  out.nb = t - tt * nb;
-  out.row0 = start + skip;
-  out.rows = (int)min((int64_t)kTok, rows - skip);
-  return out.rows > 0;
-}
+  __device__ __forceinline__ void next(int dt, int dn, int blocks) {
+    t += gridDim.x;
+    tt += dt;
+    nb += dn;
+    if (nb >= blocks) {
+      nb -= blocks;
+      ++tt;
+    }
+  }
+  // the expert whose token tiles hold tt (t < total: there is one)
+  __device__ __forceinline__ Tile tile(const MxProduct& p, const Shared& sh) {
+    while (sh.first[e + 1] <= tt) ++e;
+    int64_t start;
+    const int64_t rows = segment(p, e, &start);
+    const int64_t skip = (int64_t)(tt - sh.first[e]) * kTok;
+    return Tile{start + skip, e, nb, (int)min((int64_t)kTok, rows - skip)};
+  }
+};
 
 __device__ __forceinline__ int padded(int rows) { return (rows + 15) & ~15; }
 
@@ -166,7 +175,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (e0 + lane < p.E) sh.first[e0 + lane] = base + sum - n;
       base += __shfl_sync(0xffffffffu, sum, 31);
     }
-    if (lane == 0) sh.tiles = base;
+    if (lane == 0) {
+      sh.tiles = base;
+      sh.first[p.E] = base;
+    }
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -175,6 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* abort = &sh.abort;
   const int total = sh.tiles * (p.N / kM);
   const int nk = (p.K + kK - 1) / kK;
+  const int blocks = p.N / kM, dt = (int)gridDim.x / blocks, dn = (int)gridDim.x - dt * blocks;
+  Walk walk(p);
 
   if (warp == 8) {
     // ------------------------------------------------ producer
@@ -182,9 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t pol_w = ptx::policy_evict_first(), pol_t = ptx::policy_evict_normal();
       int kg = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-        Tile ti;
-        if (!tile_at(p, sh, t, ti)) continue;
+      for (; ok && walk.t < total; walk.next(dt, dn, blocks)) {
+        const Tile ti = walk.tile(p, sh);
         const int wrow = ti.e * p.N + ti.nb * kM;
         const bool small = ti.rows <= 48;  // boxes of 16 rows, else of 64
         const int boxes = small ? (ti.rows + 15) / 16 : (ti.rows + 63) / 64;
@@ -214,9 +227,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       int kg = 0, use = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-        Tile ti;
-        if (!tile_at(p, sh, t, ti)) continue;
+      const uint32_t base = ptx::smem_u32(stage0);
+      const uint64_t w_desc = ptx::sdesc_sw128(base, 16, 1024), x_desc = ptx::sdesc_sw128(base + kWBytes, 16, 1024);
+      const uint64_t sw_desc = ptx::sdesc(base + kWBytes + kTBytes, 16, 128, 0);
+      const uint64_t sx_desc = ptx::sdesc(base + kWBytes + kTBytes + kSfW, 16, 128, 0);
+      for (; ok && walk.t < total; walk.next(dt, dn, blocks)) {
+        const Tile ti = walk.tile(p, sh);
         const int b = use & 1;
         if (!ptx::wait_bounded(&sh.tempty[b], ((use >> 1) & 1) ^ 1, abort)) {
           raise_status(p.status, abort, kStatusTimeout);
@@ -225,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         const int N = padded(ti.rows);
         const uint32_t d = tmem + b * kTok;
+        const uint32_t id0 = idesc_mxf4(N, 0), id1 = idesc_mxf4(N, 1);
         for (int kb = 0; kb < nk; ++kb, ++kg) {
           const int s = kg % kStages;
           if (!ptx::wait_bounded(&sh.full[s], (kg / kStages) & 1, abort)) {
@@ -233,18 +250,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t w0 = ptx::smem_u32(stage0 + s * kStageBytes);
-          const uint32_t t0 = w0 + kWBytes, sw0 = t0 + kTBytes, st0 = sw0 + kSfW;
+          // descriptors differ from the first stage's in their address field alone
+          const uint32_t off = s * (kStageBytes >> 4);
+          const uint64_t w = w_desc + off, x = x_desc + off, sw = sw_desc + off, sx = sx_desc + off;
           const uint32_t sf = tmem + 2 * kTok + s * kSfCols;
-          const int halves = p.K - kb * kK > kK / 2 ? 2 : 1;  // 128-step halves that hold data
-          for (int h = 0; h < halves; ++h) {
-            copy_scales(sf + 4 * h, ptx::sdesc(sw0 + 512 * h, 16, 128, 0));
-            copy_scales(sf + 8 + 8 * h, ptx::sdesc(st0 + 1024 * h, 16, 128, 0));
-            if (N > 128) copy_scales(sf + 12 + 8 * h, ptx::sdesc(st0 + 1024 * h + 512, 16, 128, 0));
+          const bool whole = p.K - kb * kK > kK / 2;  // else one 128-step half holds data
+          copy_scales(sf, sw);
+          copy_scales(sf + 8, sx);
+          if (N > 128) copy_scales(sf + 12, sx + (512 >> 4));
+          if (whole) {
+            copy_scales(sf + 4, sw + (512 >> 4));
+            copy_scales(sf + 16, sx + (1024 >> 4));
+            if (N > 128) copy_scales(sf + 20, sx + (1536 >> 4));
           }
-          for (int kk = 0; kk < 2 * halves; ++kk)
-            mma_mxf4(d, ptx::sdesc_sw128(w0 + 32 * kk, 16, 1024), ptx::sdesc_sw128(t0 + 32 * kk, 16, 1024),
-                     idesc_mxf4(N, kk & 1), sf + 4 * (kk >> 1), sf + 8 + 8 * (kk >> 1), (kb | kk) != 0 ? 1u : 0u);
+          mma_mxf4(d, w, x, id0, sf, sf + 8, kb != 0 ? 1u : 0u);
+          mma_mxf4(d, w + 2, x + 2, id1, sf, sf + 8, 1u);
+          if (whole) {
+            mma_mxf4(d, w + 4, x + 4, id0, sf + 4, sf + 16, 1u);
+            mma_mxf4(d, w + 6, x + 6, id1, sf + 4, sf + 16, 1u);
+          }
           ptx::mma_commit(&sh.empty[s]);
         }
         if (!ok) break;
@@ -265,9 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int words = p.K / 128;  // of a row
     int kg = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-      Tile ti;
-      if (!tile_at(p, sh, t, ti)) continue;
+    for (; ok && walk.t < total; walk.next(dt, dn, blocks)) {
+      const Tile ti = walk.tile(p, sh);
       const uint32_t* w = reinterpret_cast<const uint32_t*>(p.w_scales) +
                           ((int64_t)ti.e * p.N + ti.nb * kM + r) * words;
       const uint32_t* a = reinterpret_cast<const uint32_t*>(p.a_scales) + (ti.row0 + r) * words;
@@ -323,9 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------ epilogue
     int use = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      Tile ti;
-      if (!tile_at(p, sh, t, ti)) continue;
+    for (; walk.t < total; walk.next(dt, dn, blocks)) {
+      const Tile ti = walk.tile(p, sh);
       const int b = use & 1;
       if (!ptx::wait_bounded(&sh.tfull[b], (use >> 1) & 1, abort)) {
         raise_status(p.status, abort, kStatusTimeout);
