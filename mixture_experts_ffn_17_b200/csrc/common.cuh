@@ -21,6 +21,11 @@ __device__ __forceinline__ uint8_t* align_1024(uint8_t* p) {
   return p + pad;
 }
 
+// wait_bounded by a whole warp, whose lanes all get the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort) {
+  return __all_sync(0xffffffffu, ptx::wait_bounded(bar, parity, abort));
+}
+
 // (value, index) ordering of every top-k here: larger value first, on equal
 // values the lower index first.
 __device__ __forceinline__ bool key_before(float va, int ia, float vb, int ib) {

@@ -518,7 +518,7 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
   Control& c = *sm.c;
   const Share<WT, SHARED, DOWN> share(p, ls);
   auto slot_free = [&] {
-    if (ptx::wait_bounded(&c.empty[ring.n % kStages], ((ring.n / kStages) & 1) ^ 1, &c.abort)) return true;
+    if (warp_wait(&c.empty[ring.n % kStages], ((ring.n / kStages) & 1) ^ 1, &c.abort)) return true;
     if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
     return false;
   };
@@ -560,7 +560,7 @@ __device__ bool bring_columns(const FewParams& p, const Lists& ls, const Smem& s
   const Share<WT, SHARED, DOWN> share(p, ls);
   Control& c = *sm.c;
   auto wait = [&](uint64_t* bar, int n) {
-    if (ptx::wait_bounded(bar, n & 1, &c.abort)) return true;
+    if (warp_wait(bar, n & 1, &c.abort)) return true;
     if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
     return false;
   };
@@ -662,19 +662,24 @@ __device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q
   const int last = q.rows * q.group - 1;
   int left = 0;  // units whose columns are in the buffer
   uint32_t cols = 0;
-  auto fail = [&] {
-    raise_status(p.status, &ct.abort, kStatusTimeout);
-    return false;
+  // A warp whose wait failed goes on to the end of the piece without waiting:
+  // its partner needs it at their barrier, where both learn of it.
+  bool ok = true;
+  auto arrived = [&](uint64_t* bar, uint32_t parity) {
+    if (ok && !warp_wait(bar, parity, &ct.abort)) {
+      raise_status(p.status, &ct.abort, kStatusTimeout);
+      ok = false;
+    }
   };
   auto use = [&](const Beside& x, int step) {
     if (left == 0) {
       const int buf = ring.cols & 1;
-      if (!ptx::wait_bounded(&ct.col_full[buf], (ring.cols >> 1) & 1, &ct.abort)) return fail();
+      arrived(&ct.col_full[buf], (ring.cols >> 1) & 1);
       cols = ptx::smem_u32(sm.cols) + buf * kColBytes;
       left = min(plan.units, q.step1 - step);
     }
     const int slot = ring.n % kStages;
-    if (!ptx::wait_bounded(&ct.full[slot], (ring.n / kStages) & 1, &ct.abort)) return fail();
+    arrived(&ct.full[slot], (ring.n / kStages) & 1);
     const uint32_t tile = ptx::smem_u32(sm.stages) + slot * kTileBytes;
     if constexpr (WT == kFewBf16) stage_bf16<NT>(tile, cols, plan.pitch, last, acc);
     if constexpr (WT == kFewE4m3) stage_e4m3<NT>(tile, cols, plan.pitch, last, x.scale, x.f, acc);
@@ -689,17 +694,16 @@ __device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q
       if (lane == 0) ptx::mbar_arrive(&ct.col_empty[ring.cols & 1]);
       ++ring.cols;
     }
-    return true;
   };
   // two buffers by name: a copy from one to the other would wait for its loads
   Beside even, odd;
   fetch(even, q.step0);
   for (int step = q.step0; step < q.step1; step += 2) {
     if (step + 1 < q.step1) fetch(odd, step + 1);
-    if (!use(even, step)) return false;
+    use(even, step);
     if (step + 1 < q.step1) {
       if (step + 2 < q.step1) fetch(even, step + 2);
-      if (!use(odd, step + 1)) return false;
+      use(odd, step + 1);
     }
   }
   // the two halves of the steps, and the terms of each row, are joined by the
@@ -715,7 +719,7 @@ __device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q
     to[(8 * j + 2 * c) * kRedPitch + hi] = acc[j][2];
     to[(8 * j + 2 * c + 1) * kRedPitch + hi] = acc[j][3];
   }
-  ptx::named_barrier(1 + pair, 64);
+  ok = ptx::named_barrier_and(1 + pair, 64, ok);
   for (int i = half * 32 + lane; i < q.rows * 16; i += 64) {
     const int r = i >> 4, col = i & 15;
     float a = 0.0f;
@@ -726,7 +730,7 @@ __device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q
     q.out[r * q.ld + pair * 16 + col] = a;
   }
   ptx::named_barrier(1 + pair, 64);
-  return true;
+  return ok;
 }
 
 template <int WT, bool SHARED, bool DOWN>
@@ -736,10 +740,10 @@ __device__ bool consume(const FewParams& p, const Lists& ls, const Smem& sm, Rin
   Control& ct = *sm.c;
   while (true) {
     const int slot = ring.n % kStages;
-    if (!ptx::wait_bounded(&ct.full[slot], (ring.n / kStages) & 1, &ct.abort)) {
-      raise_status(p.status, &ct.abort, kStatusTimeout);
-      return false;
-    }
+    const bool there = warp_wait(&ct.full[slot], (ring.n / kStages) & 1, &ct.abort);
+    if (!there) raise_status(p.status, &ct.abort, kStatusTimeout);
+    // both warps of a pair take the chunk or neither
+    if (!ptx::named_barrier_and(1 + ((threadIdx.x >> 5) & 7), 64, there)) return false;
     const int id = ct.chunk[slot];
     if (id < 0) {
       __syncwarp();
@@ -1199,11 +1203,11 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     }
     bool ok = true;
     if (p.S > 0) ok = produce<kFewBf16, true, false>(maps, p, ls, sm, ring, p.bar + 4);
-    if (ok && !ptx::wait_bounded(&ct.routed, 0, abort)) {
+    if (ok && !warp_wait(&ct.routed, 0, abort)) {
       raise_status(p.status, abort, kStatusTimeout);
       ok = false;
     }
-    ok = ok && *abort == 0;  // the router gave up: there are no lists
+    ok = ok && __all_sync(0xffffffffu, *abort == 0);  // the router gave up: there are no lists
     if (ok) ok = produce<RT, false, false>(maps, p, ls, sm, ring, p.bar + 5);
     if (ok) ok = produce<RT, false, true>(maps, p, ls, sm, ring, p.bar + 6);
     if (ok && p.S > 0) produce<kFewBf16, true, true>(maps, p, ls, sm, ring, p.bar + 7);
@@ -1217,7 +1221,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     Ring ring;
     bool ok = true;
     auto wait = [&](uint64_t* bar) {
-      if (ptx::wait_bounded(bar, 0, abort) && *abort == 0) {
+      if (warp_wait(bar, 0, abort) && __all_sync(0xffffffffu, *abort == 0)) {
         ptx::fence_proxy_async_all();  // x in fp16, and h, were written by ordinary stores
         return true;
       }
@@ -1249,7 +1253,8 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     grid_arrive(p.bar + 0);
     bool ok = true;
     if (p.S > 0) ok = consume<kFewBf16, true, false>(p, ls, sm, ring);
-    ok = ok && ptx::wait_bounded(&ct.routed, 0, abort) && *abort == 0;
+    // all consumers agree on whether there are lists
+    ok = ptx::named_barrier_and(9, kThreads, ok && ptx::wait_bounded(&ct.routed, 0, abort) && *abort == 0);
     if (ok) ok = consume<RT, false, false>(p, ls, sm, ring);
     grid_arrive(p.bar + 1);
     if (grid_wait(p.bar + 1, p.status, abort)) {

@@ -17,10 +17,16 @@
 // columns), the column blocks of one token tile next to each other: the tokens
 // stay in L2 and the weights stream.  Roles: a producer thread (TMA, 256 steps
 // of k = 128 bytes a row and stage, 128-byte swizzle), four warps that bring the
-// scale bytes from their row-major arrays into the 512-byte blocks which
-// tcgen05.cp spreads over TMEM (row r of 128 at byte (r % 32) * 16 + (r / 32) * 4,
-// four blocks of 32 steps next to each other), an MMA thread, and four warps
-// that drain the accumulators (two, so that draining overlaps the next tile).
+// scale bytes, an MMA thread, and four warps that drain the accumulators (two, so
+// that draining overlaps the next tile).
+//
+// Scales.  The tensor core takes them from TMEM: row r of 128 in lane r % 32 (the
+// same in all four lane quarters) of column r / 32, the four bytes of a word being
+// four blocks of 32 steps.  The scale warps read their row-major arrays, four
+// stages' worth of a row (32 bytes) at a time and a group ahead, exchange rows
+// through shared memory and store each quarter with tcgen05.st.  (tcgen05.cp from
+// shared memory spreads them too, but runs in the MMAs' own queue: 404 instead of
+// 295 us for a decode batch of 512 rows, 226 experts of 7168 x 2048.)
 // TMEM: 2 x 192 accumulator columns and 24 columns of scales a stage.
 //
 // Bound: HBM by the weights (17/32 byte a value) up to several hundred rows an
@@ -40,14 +46,15 @@ constexpr int kM = 128;              // output columns of a tile
 constexpr int kK = 256;              // steps of k of a stage
 constexpr uint32_t kWBytes = kM * kK / 2;
 constexpr uint32_t kTBytes = kTok * kK / 2;
-constexpr uint32_t kSfW = 2 * 512;      // two 128-step halves of 128 rows
-constexpr uint32_t kSfT = 2 * 2 * 512;  // two halves of 2 x 128 rows
-constexpr uint32_t kStageBytes = kWBytes + kTBytes + kSfW + kSfT;
+constexpr uint32_t kStageBytes = kWBytes + kTBytes;
 static_assert(kStageBytes % 1024 == 0, "stages stay aligned for the 128-byte swizzle");
-constexpr int kSfCols = 8 + 16;  // TMEM columns of a stage's scales
+constexpr int kSfCols = 8 + 16;  // TMEM columns of a stage's scales: 2 x 4 of the weights, 2 x 8 of the tokens
+constexpr int kGroup = 4;        // stages whose scales are read together
+constexpr int kSfRows = kM + kTok;
 constexpr int kTmemCols = 512;
 static_assert(2 * kTok + kStages * kSfCols <= kTmemCols, "TMEM columns");
-constexpr size_t kSmem = kStages * kStageBytes + 1024 + 256;
+constexpr size_t kSmem = kStages * kStageBytes + 1024 + 2 * 2 * kGroup * kSfRows * 4;
+static_assert(kSmem + sizeof(int) * (kMxMaxExperts + 40) <= 232448, "shared memory");
 constexpr int kThreads = 320;  // 4 epilogue warps, 4 scale warps, producer, MMA
 constexpr uint32_t kOne4 = 0x7f7f7f7fu;  // four scales of 1
 
@@ -74,10 +81,11 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
-// 512 bytes of scales to four TMEM columns, the 32 lanes' words in all four
-// lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+// Eight columns of this warp's lane quarter.
+__device__ __forceinline__ void store_scales(uint32_t tmem, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(tmem), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 struct Shared {
@@ -229,8 +237,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const uint32_t base = ptx::smem_u32(stage0);
       const uint64_t w_desc = ptx::sdesc_sw128(base, 16, 1024), x_desc = ptx::sdesc_sw128(base + kWBytes, 16, 1024);
-      const uint64_t sw_desc = ptx::sdesc(base + kWBytes + kTBytes, 16, 128, 0);
-      const uint64_t sx_desc = ptx::sdesc(base + kWBytes + kTBytes + kSfW, 16, 128, 0);
       for (; ok && walk.t < total; walk.next(dt, dn, blocks)) {
         const Tile ti = walk.tile(p, sh);
         const int b = use & 1;
@@ -252,17 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tc_fence_after();
           // descriptors differ from the first stage's in their address field alone
           const uint32_t off = s * (kStageBytes >> 4);
-          const uint64_t w = w_desc + off, x = x_desc + off, sw = sw_desc + off, sx = sx_desc + off;
+          const uint64_t w = w_desc + off, x = x_desc + off;
           const uint32_t sf = tmem + 2 * kTok + s * kSfCols;
           const bool whole = p.K - kb * kK > kK / 2;  // else one 128-step half holds data
-          copy_scales(sf, sw);
-          copy_scales(sf + 8, sx);
-          if (N > 128) copy_scales(sf + 12, sx + (512 >> 4));
-          if (whole) {
-            copy_scales(sf + 4, sw + (512 >> 4));
-            copy_scales(sf + 16, sx + (1024 >> 4));
-            if (N > 128) copy_scales(sf + 20, sx + (1536 >> 4));
-          }
           mma_mxf4(d, w, x, id0, sf, sf + 8, kb != 0 ? 1u : 0u);
           mma_mxf4(d, w + 2, x + 2, id1, sf, sf + 8, 1u);
           if (whole) {
@@ -280,67 +278,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------------------------ scales
-    // Thread r takes row r of the weights and rows r and r + 128 of the
-    // tokens.  Words of four scales; a group of four stages is read while the
-    // one before it is handed over, so a load has a group's time to arrive.
-    constexpr int kG = 4;
+    // Thread r reads row r of the weights and rows r and r + 128 of the tokens.
     const int r = threadIdx.x - 128;
-    const uint32_t at = (uint32_t)(r & 31) * 16 + (uint32_t)(r >> 5) * 4;
-    const int words = p.K / 128;  // of a row
-    int kg = 0;
+    const int words = p.K / 128;  // of four scales in a row
+    const bool wide = words % 4 == 0;
+    uint32_t* exchange = reinterpret_cast<uint32_t*>(stage0 + kStages * kStageBytes);  // [2][8 words][rows]
+    uint32_t q[3][2 * kGroup];
+    auto row_words = [&](uint32_t (&v)[2 * kGroup], const uint8_t* base, int64_t row, int k0, bool have) {
+      const uint32_t* a = reinterpret_cast<const uint32_t*>(base) + row * words + k0;
+#pragma unroll
+      for (int i = 0; i < 2 * kGroup; i += 4) {
+        if (wide) {
+          const uint4 x = have && k0 + i < words ? __ldg(reinterpret_cast<const uint4*>(a + i))
+                                                 : make_uint4(kOne4, kOne4, kOne4, kOne4);
+          v[i] = x.x;
+          v[i + 1] = x.y;
+          v[i + 2] = x.z;
+          v[i + 3] = x.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[i + j] = have && k0 + i + j < words ? __ldg(a + i + j) : kOne4;
+        }
+      }
+    };
+    auto fetch = [&](const Tile& ti, int kb0) {
+      row_words(q[0], p.w_scales, (int64_t)ti.e * p.N + ti.nb * kM + r, 2 * kb0, true);
+      row_words(q[1], p.a_scales, ti.row0 + r, 2 * kb0, r < ti.rows);
+      row_words(q[2], p.a_scales, ti.row0 + r + 128, 2 * kb0, r + 128 < ti.rows);
+    };
+    int kg = 0, buf = 0;
     bool ok = true;
-    for (; ok && walk.t < total; walk.next(dt, dn, blocks)) {
-      const Tile ti = walk.tile(p, sh);
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(p.w_scales) +
-                          ((int64_t)ti.e * p.N + ti.nb * kM + r) * words;
-      const uint32_t* a = reinterpret_cast<const uint32_t*>(p.a_scales) + (ti.row0 + r) * words;
-      const uint32_t* a2 = a + 128 * (int64_t)words;
-      const bool in = r < ti.rows, in2 = r + 128 < ti.rows;
-      uint32_t q[kG][2][3];
-      auto fetch = [&](int kb0) {
+    Tile ti{}, next{};
+    if (walk.t < total) {
+      next = walk.tile(p, sh);
+      fetch(next, 0);
+    }
+    // a warp whose wait failed goes on without waiting: the others need it at the
+    // barrier
+    while (walk.t < total) {
+      ti = next;
+      for (int kb0 = 0; kb0 < nk; kb0 += kGroup) {
+        uint32_t* ex = exchange + buf * (2 * kGroup * kSfRows);
 #pragma unroll
-        for (int i = 0; i < kG; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int k = (kb0 + i) * 2 + h;
-            const bool have = k < words;
-            q[i][h][0] = have ? __ldg(w + k) : kOne4;
-            q[i][h][1] = have && in ? __ldg(a + k) : kOne4;
-            q[i][h][2] = have && in2 ? __ldg(a2 + k) : kOne4;
-          }
-      };
-      fetch(0);
-      for (int kb0 = 0; ok && kb0 < nk; kb0 += kG) {
-        uint32_t now[kG][2][3];
-#pragma unroll
-        for (int i = 0; i < kG; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 3; ++j) now[i][h][j] = q[i][h][j];
-        if (kb0 + kG < nk) fetch(kb0 + kG);
-#pragma unroll
-        for (int i = 0; i < kG; ++i) {
-          if (ok && kb0 + i < nk) {
-            const int s = kg % kStages;
-            if (!ptx::wait_bounded(&sh.empty[s], ((kg / kStages) & 1) ^ 1, abort)) {
-              raise_status(p.status, abort, kStatusTimeout);
-              ok = false;
-            } else {
-              uint8_t* sw = stage0 + s * kStageBytes + kWBytes + kTBytes;
-              uint8_t* st = sw + kSfW;
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                *reinterpret_cast<uint32_t*>(sw + 512 * h + at) = now[i][h][0];
-                *reinterpret_cast<uint32_t*>(st + 1024 * h + at) = now[i][h][1];
-                *reinterpret_cast<uint32_t*>(st + 1024 * h + 512 + at) = now[i][h][2];
-              }
-              ptx::fence_proxy_async();
-              ptx::mbar_arrive(&sh.full[s]);
-              ++kg;
-            }
+        for (int i = 0; i < 2 * kGroup; ++i) {
+          ex[i * kSfRows + r] = q[0][i];
+          ex[i * kSfRows + kM + r] = q[1][i];
+          if (r + 128 < kTok) ex[i * kSfRows + kM + 128 + r] = q[2][i];
+        }
+        // the next group, of this tile or the next one
+        if (kb0 + kGroup < nk) {
+          fetch(ti, kb0 + kGroup);
+        } else {
+          walk.next(dt, dn, blocks);
+          if (walk.t < total) {
+            next = walk.tile(p, sh);
+            fetch(next, 0);
           }
         }
+        ptx::named_barrier(1, 128);
+        for (int i = 0; i < kGroup && kb0 + i < nk; ++i, ++kg) {
+          const int s = kg % kStages;
+          uint32_t w[8], a[2][8];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t* line = ex + (2 * i + h) * kSfRows + lane;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[4 * h + j] = line[32 * j];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[h][j] = 32 * j < kTok ? line[kM + 32 * j] : kOne4;
+          }
+          if (ok && !warp_wait(&sh.empty[s], ((kg / kStages) & 1) ^ 1, abort)) {
+            raise_status(p.status, abort, kStatusTimeout);
+            ok = false;
+          }
+          if (!ok) continue;
+          ptx::tc_fence_after();
+          const uint32_t sf = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 2 * kTok + s * kSfCols;
+          store_scales(sf, w);
+          store_scales(sf + 8, a[0]);
+          store_scales(sf + 16, a[1]);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&sh.full[s]);
+        }
+        buf ^= 1;
       }
     }
   } else {
@@ -349,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; walk.t < total; walk.next(dt, dn, blocks)) {
       const Tile ti = walk.tile(p, sh);
       const int b = use & 1;
-      if (!ptx::wait_bounded(&sh.tfull[b], (use >> 1) & 1, abort)) {
+      if (!warp_wait(&sh.tfull[b], (use >> 1) & 1, abort)) {
         raise_status(p.status, abort, kStatusTimeout);
         break;
       }
