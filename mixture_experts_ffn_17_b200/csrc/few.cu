@@ -612,7 +612,7 @@ __device__ bool bring_columns(const FewParams& p, const Lists& ls, const Smem& s
 
 // ------------------------------------------------------------ consumers
 template <int WT, int NT, bool DOWN>
-__device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q, const uint8_t* scales, int K, int N,
+__device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q, const uint8_t* scales, int K, int N,
                                               const Smem& sm, Ring& ring) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3, half = warp >> 3;
@@ -662,14 +662,11 @@ __device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q
   const int last = q.rows * q.group - 1;
   int left = 0;  // units whose columns are in the buffer
   uint32_t cols = 0;
-  // A warp whose wait failed goes on to the end of the piece without waiting:
-  // its partner needs it at their barrier, where both learn of it.
-  bool ok = true;
+  // A wait that fails raises the abort flag, which ends all later ones at once, and
+  // the piece goes on with whatever the buffers hold: its barriers need every
+  // warp, and the share ends at the next chunk.
   auto arrived = [&](uint64_t* bar, uint32_t parity) {
-    if (ok && !warp_wait(bar, parity, &ct.abort)) {
-      raise_status(p.status, &ct.abort, kStatusTimeout);
-      ok = false;
-    }
+    if (!ptx::wait_bounded(bar, parity, &ct.abort)) raise_status(p.status, &ct.abort, kStatusTimeout);
   };
   auto use = [&](const Beside& x, int step) {
     if (left == 0) {
@@ -719,7 +716,7 @@ __device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q
     to[(8 * j + 2 * c) * kRedPitch + hi] = acc[j][2];
     to[(8 * j + 2 * c + 1) * kRedPitch + hi] = acc[j][3];
   }
-  ok = ptx::named_barrier_and(1 + pair, 64, ok);
+  ptx::named_barrier(1 + pair, 64);
   for (int i = half * 32 + lane; i < q.rows * 16; i += 64) {
     const int r = i >> 4, col = i & 15;
     float a = 0.0f;
@@ -730,7 +727,6 @@ __device__ __forceinline__ bool consume_piece(const FewParams& p, const Piece& q
     q.out[r * q.ld + pair * 16 + col] = a;
   }
   ptx::named_barrier(1 + pair, 64);
-  return ok;
 }
 
 template <int WT, bool SHARED, bool DOWN>
@@ -738,12 +734,13 @@ __device__ bool consume(const FewParams& p, const Lists& ls, const Smem& sm, Rin
   const Share<WT, SHARED, DOWN> share(p, ls);
   const int K = share.K, N = share.N;
   Control& ct = *sm.c;
+  volatile uint32_t* abort = &ct.abort;
   while (true) {
     const int slot = ring.n % kStages;
     const bool there = warp_wait(&ct.full[slot], (ring.n / kStages) & 1, &ct.abort);
     if (!there) raise_status(p.status, &ct.abort, kStatusTimeout);
     // both warps of a pair take the chunk or neither
-    if (!ptx::named_barrier_and(1 + ((threadIdx.x >> 5) & 7), 64, there)) return false;
+    if (!ptx::named_barrier_and(1 + ((threadIdx.x >> 5) & 7), 64, there && *abort == 0)) return false;
     const int id = ct.chunk[slot];
     if (id < 0) {
       __syncwarp();
@@ -751,14 +748,17 @@ __device__ bool consume(const FewParams& p, const Lists& ls, const Smem& sm, Rin
       ++ring.n;
       return true;
     }
-    const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
+    share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
       const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
       const int cols = q.rows * q.group;
-      if (cols <= 8) return consume_piece<WT, 1, DOWN>(p, q, scales, K, N, sm, ring);
-      if (cols <= 16 || terms(WT) == 2) return consume_piece<WT, 2, DOWN>(p, q, scales, K, N, sm, ring);
-      return consume_piece<WT, terms(WT) == 2 ? 2 : 3, DOWN>(p, q, scales, K, N, sm, ring);
+      if (cols <= 8)
+        consume_piece<WT, 1, DOWN>(p, q, scales, K, N, sm, ring);
+      else if (cols <= 16 || terms(WT) == 2)
+        consume_piece<WT, 2, DOWN>(p, q, scales, K, N, sm, ring);
+      else
+        consume_piece<WT, terms(WT) == 2 ? 2 : 3, DOWN>(p, q, scales, K, N, sm, ring);
+      return true;
     });
-    if (!ok) return false;
   }
 }
 
