@@ -22,7 +22,11 @@
 //                         weights: 710 instead of 455 us at T = 8 with 28 experts
 //                         of 7168 x 2048 in bf16);
 //   router (2 warps)      waits for all logits, finds the top-k (in every CTA)
-//                         and the list of chosen experts and their rows.
+//                         and the list of chosen experts and their rows; then
+//                         brings the block scales of coded weights, and h's
+//                         factors, beside the tiles (a consumer's own load one
+//                         stage ahead comes too late: 0.6 us a stage of e4m3
+//                         where HBM needs 0.37).
 //
 // Split of the work.  A segment is 128 output columns of one matrix of one
 // expert, a unit the part of its contraction that one stage holds (16 KB of
@@ -40,13 +44,16 @@
 // takes columns 16 (w % 8) of a tile and one half of its steps (w / 8).
 //   bf16 weights: x is bf16 as it comes; h is fp32 and goes in as three bf16
 //   terms (8 bits each: 24 in all).
-//   e4m3 and MXFP4 codes become fp16, which holds them exactly, by moving their
-//   bits: exponent and mantissa read 2^-8 and 2^-14 times the code's value there,
-//   made up in the sums' factors.  (The conversion instructions run at a
-//   sixteenth of the rate: 2700 cycles a stage of MXFP4 where HBM needs 730.)
-//   x and h are fp16 too, times a power of two that puts the largest of a token
-//   (of 128 values of h) at 2^14: a bf16 x fits exactly down to 2^-29 of the
-//   largest and to 2^-40 of it below; h goes in as two terms (22 bits).
+//   e4m3 codes go into the MMA as they are (m16n8k32, fp32 sums as exact as
+//   bf16's), MXFP4 codes as e4m3 values, by moving their bits: exponent and
+//   mantissa read 2^-6 times the code's value there.  (As fp16, through the
+//   conversion instructions, which run at a sixteenth of the rate, or by moving
+//   bits with two MMAs for one, the decoding bound the kernel at 2 to 3.8 TB/s.)
+//   The activations go in as sums of e4m3 terms, each rounding what is left, with
+//   4 bits more: x in three, h in six, after a power of two has put the largest
+//   of a token (of 128 values of h) between 2^7 and 2^8.  A bf16 x is exact down
+//   to 2^-13 of the largest and to 2^-25 of it below, h to 2^-24 of itself and
+//   2^-37 of the largest.  An infinity has no e4m3 value and goes in as NaN.
 // Block scales multiply fp32 sums.
 #include <algorithm>
 #include <cstdint>
@@ -89,6 +96,10 @@ struct Lists {  // what the routing leaves in shared memory
 struct Control {
   uint64_t full[kStages], empty[kStages];
   uint64_t col_full[2], col_empty[2];
+  uint64_t issued[kStages];   // a stage's chunk is known, its tile on the way
+  uint64_t scaled[kStages];   // its scales are there
+  uint64_t started;           // `first` is there
+  int first;                  // first stage of the routed experts
   uint64_t ready;   // h is there, in all CTAs
   int chunk[kStages];  // which chunk a stage belongs to; -1: the share is done
   uint64_t routed;  // the lists are there
@@ -156,20 +167,20 @@ __device__ __forceinline__ float4 sum_parts(const float* at, int parts) {
 }
 
 // ------------------------------------------------------------ tiles and columns
-template <bool F16>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (F16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint2 b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
 }
 
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
@@ -186,34 +197,16 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-// Four e4m3 codes to two fp16 pairs, bytes (0, 2) and (1, 3), times 2^-8.  The
-// code 0x7f, NaN, is not looked at (it reads 480).
-__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t& even, uint32_t& odd) {
-  even = ((w << 8) & 0x80008000u) | ((w << 7) & 0x3f803f80u);
-  odd = (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
+// Eight MXFP4 codes as e4m3 values times 2^-6: the even codes and the odd ones.
+__device__ __forceinline__ void mx_e4m3(uint32_t w, uint32_t& even, uint32_t& odd) {
+  even = ((w << 4) & 0x80808080u) | ((w << 2) & 0x1c1c1c1cu);
+  odd = (w & 0x80808080u) | ((w >> 2) & 0x1c1c1c1cu);
 }
 
-// The same by the conversion instruction, NaN included.
-__device__ __forceinline__ void e4m3_pairs_nan(uint32_t w, uint32_t& even, uint32_t& odd) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(even), "=r"(odd)
-      : "r"(__byte_perm(w, 0, 0x3120)));
-}
-
-// Eight MXFP4 codes to four fp16 pairs, codes j and j + 4, times 2^-14.
-__device__ __forceinline__ void mx_pairs(uint32_t w, uint32_t (&f)[4]) {
-  f[0] = ((w << 12) & 0x80008000u) | ((w << 9) & 0x0e000e00u);
-  f[1] = ((w << 8) & 0x80008000u) | ((w << 5) & 0x0e000e00u);
-  f[2] = ((w << 4) & 0x80008000u) | ((w << 1) & 0x0e000e00u);
-  f[3] = (w & 0x80008000u) | ((w >> 3) & 0x0e000e00u);
-}
-
-__device__ __forceinline__ void lds(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+__device__ __forceinline__ uint2 lds8(uint32_t addr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
+  return r;
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -235,22 +228,60 @@ __device__ __forceinline__ void scales_of(uint32_t w, float (&f)[4]) {
   f[3] = ptx::bf16_hi(hi);
 }
 
-// Place of step k in a column of B that this kernel writes: in order, but for
-// MXFP4 with 8c + j and 8c + j + 4 side by side, as the codes come apart.
+// Four e4m3 values, steps k to k + 3 (k a multiple of 4) of a column, to their
+// places: lane c of an MMA takes 8 bytes in a row of each 32 steps, for e4m3
+// weights (which ldmatrix.trans brings two steps of eight at a time) steps 2c and
+// 2c + 1 of each eight, for MXFP4 the even ones of 8c to 8c + 7 and then the odd.
 template <int WT>
-__device__ __forceinline__ int place_of(int k) {
-  if (WT == kFewMxfp4) return (k & ~7) + 2 * (k & 3) + ((k >> 2) & 1);
-  return k;
+__device__ __forceinline__ void store_e4m3(uint8_t* column, int k, uint32_t v) {
+  uint8_t* block = column + (k & ~31);
+  uint16_t first, second;
+  int at, gap;
+  if (WT == kFewMxfp4) {
+    at = (k & 24) + ((k & 4) >> 1);
+    gap = 4;
+    first = (uint16_t)__byte_perm(v, 0, 0x4420);
+    second = (uint16_t)__byte_perm(v, 0, 0x4431);
+  } else {
+    at = 4 * (k & 7) + ((k >> 3) & 3) * 2;
+    gap = 8;
+    first = (uint16_t)v;
+    second = (uint16_t)(v >> 16);
+  }
+  *reinterpret_cast<uint16_t*>(block + at) = first;
+  *reinterpret_cast<uint16_t*>(block + at + gap) = second;
 }
 
-// Values k and k + 1 (k even) in a column.
-template <int WT>
-__device__ __forceinline__ void store_pair(uint16_t* column, int k, uint32_t v) {
-  if (WT == kFewMxfp4) {
-    column[place_of<WT>(k)] = (uint16_t)v;
-    column[place_of<WT>(k + 1)] = (uint16_t)(v >> 16);
-  } else {
-    *reinterpret_cast<uint32_t*>(column + place_of<WT>(k)) = v;
+// Two values as e4m3, the first in the low byte, and back as fp16.
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3_values(uint32_t pair) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)pair));
+  return r;
+}
+
+// Four values to N terms, the columns `ld` bytes apart.
+template <int WT, int N>
+__device__ __forceinline__ void store_terms8(uint8_t* column, int64_t ld, int k, const float (&value)[4], float factor) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool finite = (__float_as_uint(value[i]) & 0x7f800000u) != 0x7f800000u;
+    v[i] = finite ? value[i] * factor : __uint_as_float(0x7fffffffu);
+  }
+#pragma unroll
+  for (int t = 0; t < N; ++t) {
+    const uint32_t q01 = e4m3_pair(v[0], v[1]), q23 = e4m3_pair(v[2], v[3]);
+    store_e4m3<WT>(column + t * ld, k, q01 | (q23 << 16));
+    const uint32_t lo = e4m3_values(q01), hi = e4m3_values(q23);
+    const uint32_t back[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (v[i] - __half2float(__ushort_as_half((uint16_t)back[i]))) * 16.0f;
   }
 }
 
@@ -273,62 +304,34 @@ __device__ __forceinline__ void stage_bf16(uint32_t tile, uint32_t cols, int pit
     uint32_t a[4];
     ldsm_t(a, tile + ((warp >> 2) & 1) * 8192 + k * 128 + ((chunk ^ (k & 7)) << 4));
 #pragma unroll
-    for (int j = 0; j < NT; ++j) mma<false>(acc[j], a, b[j][2 * q], b[j][2 * q + 1]);
+    for (int j = 0; j < NT; ++j) mma_bf16(acc[j], a, b[j][2 * q], b[j][2 * q + 1]);
   }
 }
 
 // e4m3: [steps][128 columns] codes; a 16-bit unit of ldmatrix is two columns of
-// one step, so a register holds columns 2g and 2g + 1 of steps 2c and 2c + 1.
-// True where the tile has a code 0x7f, whose sums are to be done again with NANS.
-template <int NT, bool NANS>
-__device__ __forceinline__ bool e4m3_sums(uint32_t tile, uint32_t cols, int pitch, int last, float (&part)[NT][4]) {
+// one step, so a register holds columns 2g and 2g + 1 of two steps of eight, and
+// two registers make one of the MMA's, four steps of a column.
+// f[j]: the block's scale times the columns' factor.
+template <int NT>
+__device__ __forceinline__ void stage_e4m3(uint32_t tile, uint32_t cols, int pitch, int last, const float (&f)[NT],
+                                           float (&acc)[NT][4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = lane >> 3, r = lane & 7;
-  uint32_t seen = 0;  // a byte's top bit, which adding 1 flips where the seven others are set
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) part[j][e] = 0.0f;
+  const int i = lane >> 3, r = lane & 7, g = lane >> 2, c = lane & 3;
+  float part[NT][4] = {};
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int k0 = (warp >> 3) * 64 + 32 * q, k = k0 + 8 * i + r;
-    uint32_t w[4], a[4][2];
+    uint32_t w[4];
     ldsm_t(w, tile + k * 128 + (((warp & 7) ^ (k & 7)) << 4));
+    const uint32_t a[4] = {__byte_perm(w[0], w[1], 0x6420), __byte_perm(w[0], w[1], 0x7531),
+                           __byte_perm(w[2], w[3], 0x6420), __byte_perm(w[2], w[3], 0x7531)};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (NANS) {
-        e4m3_pairs_nan(w[e], a[e][0], a[e][1]);
-      } else {
-        e4m3_pairs(w[e], a[e][0], a[e][1]);
-        seen |= (w[e] + 0x01010101u) ^ w[e];
-      }
-    }
-    const uint32_t a0[4] = {a[0][0], a[0][1], a[1][0], a[1][1]}, a1[4] = {a[2][0], a[2][1], a[3][0], a[3][1]};
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      uint32_t b[4];
-      ldsm(b, cols + min(8 * j + r, last) * pitch + (k0 + 8 * i) * 2);
-      mma<true>(part[j], a0, b[0], b[1]);
-      mma<true>(part[j], a1, b[2], b[3]);
-    }
-  }
-  return (seen & 0x80808080u) != 0;
-}
-
-// scale: the block's; f[j]: the columns' factor.
-template <int NT>
-__device__ __forceinline__ void stage_e4m3(uint32_t tile, uint32_t cols, int pitch, int last, float scale,
-                                           const float (&f)[NT], float (&acc)[NT][4]) {
-  float part[NT][4];
-  float up = 256.0f * scale;
-  if (__any_sync(0xffffffffu, e4m3_sums<NT, false>(tile, cols, pitch, last, part))) {
-    e4m3_sums<NT, true>(tile, cols, pitch, last, part);
-    up = scale;
+    for (int j = 0; j < NT; ++j) mma_e4m3(part[j], a, lds8(cols + min(8 * j + g, last) * pitch + k0 + 8 * c));
   }
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(part[j][e], f[j] * up, acc[j][e]);
+    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(part[j][e], f[j], acc[j][e]);
 }
 
 // MXFP4: [128 columns][steps / 2] codes; lane (g, c) holds the eight codes 8c of
@@ -352,17 +355,13 @@ __device__ __forceinline__ void stage_mxfp4(uint32_t tile, uint32_t cols, int pi
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int blk = 2 * p + q;
-      uint32_t x[4], y[4];
-      mx_pairs(w[2 * q], x);
-      mx_pairs(w[2 * q + 1], y);
-      const uint32_t a0[4] = {x[0], y[0], x[1], y[1]}, a1[4] = {x[2], y[2], x[3], y[3]};
+      uint32_t a[4];
+      mx_e4m3(w[2 * q], a[0], a[2]);
+      mx_e4m3(w[2 * q + 1], a[1], a[3]);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        uint32_t b[4];
-        lds(b, cols + min(8 * j + g, last) * pitch + ((warp >> 3) * 128 + blk * 32 + 8 * c) * 2);
         float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        mma<true>(part, a0, b[0], b[1]);
-        mma<true>(part, a1, b[2], b[3]);
+        mma_e4m3(part, a, lds8(cols + min(8 * j + g, last) * pitch + (warp >> 3) * 128 + blk * 32 + 8 * c));
         sum[j][0] = fmaf(part[0], s0[blk], sum[j][0]);
         sum[j][1] = fmaf(part[1], s0[blk], sum[j][1]);
         sum[j][2] = fmaf(part[2], s1[blk], sum[j][2]);
@@ -373,12 +372,14 @@ __device__ __forceinline__ void stage_mxfp4(uint32_t tile, uint32_t cols, int pi
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(sum[j][e], f[j] * 16384.0f, acc[j][e]);
+    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(sum[j][e], f[j] * 64.0f, acc[j][e]);
 }
 
 // ------------------------------------------------------------ shares and pieces
-// B columns that a row of h takes.
-__host__ __device__ constexpr int terms(int weights) { return weights == kFewBf16 ? 3 : 2; }
+// B columns that a row of x and of h takes, and the bytes of a step.
+__host__ __device__ constexpr int x_terms(int weights) { return weights == kFewBf16 ? 1 : 3; }
+__host__ __device__ constexpr int h_terms(int weights) { return weights == kFewBf16 ? 3 : 6; }
+__host__ __device__ constexpr int step_bytes(int weights) { return weights == kFewBf16 ? 2 : 1; }
 
 // A chunk, or one pass over it: units [step0, step1) of 128 output columns of
 // one matrix, for `rows` rows of `group` B columns each.
@@ -424,15 +425,16 @@ struct Share {
     q.expert = SHARED ? 0 : ls.expert[ei];
     q.first = SHARED ? 0 : ls.start[ei];
     q.rows = SHARED ? p.T : ls.start[ei + 1] - q.first;
-    q.group = DOWN ? terms(WT) : 1;
+    q.group = DOWN ? h_terms(WT) : x_terms(WT);
     q.again = q.rows > kPass;
     q.ld = (int64_t)per_expert * split.parts * kFewCols;
     q.out = buf + q.first * q.ld + ((int64_t)in * split.parts + part) * kFewCols;
     return q;
   }
-  // At most 8 rows of the down projections a pass (more read the weights again,
-  // from L2 mostly: only the shared expert and crowded small layers have them).
-  static constexpr int kPass = DOWN ? 8 : kFewMaxTokens;
+  // Rows of a pass: 24 B columns at most (more rows read the weights again, from
+  // L2 mostly: only the shared expert and crowded small layers have them).
+  static constexpr int kPass =
+      DOWN ? kMaxCols / h_terms(WT) : WT == kFewBf16 ? kFewMaxTokens : kMaxCols / x_terms(WT);
   template <typename F>
   __device__ __forceinline__ bool passes(Piece q, F f) const {
     const int all = q.rows;
@@ -450,8 +452,8 @@ struct Share {
 // in bytes: a pad keeps the reads of 8 columns off each other's banks.
 template <int WT>
 struct ColumnPlan {
-  static constexpr int kUnitBytes = 2 * few_unit_steps(WT);
-  static constexpr int kPad = WT == kFewMxfp4 ? 64 : 16;
+  static constexpr int kUnitBytes = step_bytes(WT) * few_unit_steps(WT);
+  static constexpr int kPad = WT == kFewBf16 ? 16 : 32;
   int units, pitch;
   __device__ __forceinline__ explicit ColumnPlan(const Piece& q) {
     const int cols = q.rows * q.group;
@@ -460,14 +462,25 @@ struct ColumnPlan {
   }
 };
 // every piece has room for one unit's columns
-static_assert((int)kColBytes / kMaxCols >= 2 * 64 + 16 && (int)kColBytes / 16 >= 2 * 256 + 64, "B columns");
+static_assert((int)kColBytes / kMaxCols >= 256 + 32, "B columns");
 
-// The rings' positions: stages and column buffers handed over so far.
+// The rings' positions: stages and column buffers handed over so far, and which
+// phase of its `scaled` barrier each stage is in (only routed stages have one).
 struct Ring {
   int n = 0, cols = 0;
+  uint32_t scaled = 0;
+};
+
+// What goes with a stage's tile of codes: MXFP4's scale bytes of both halves of
+// the steps for each of the 128 columns, and a factor for each row of h (e4m3: for
+// each row, the block's scale times it) and half.
+struct StageScales {
+  uint32_t words[kFewCols][2];
+  float factor[kMaxCols / 3][2];
 };
 
 struct Smem {
+  StageScales* scales;
   uint8_t* stages;
   uint8_t* cols;
   float* red;
@@ -491,30 +504,11 @@ __device__ __forceinline__ void load_tile(const FewMaps& m, const FewParams& p, 
   }
 }
 
-// Brings the scales of a unit into L2 (a row of MXFP4's is 32 bytes for four
-// units), where the consumers' loads, one stage ahead of their use, find them.
-template <int WT>
-__device__ __forceinline__ void prefetch_scales(const FewParams& p, const Piece& q, int step, int K, int N) {
-  const int lane = threadIdx.x & 31;
-  const uint8_t* s = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
-  if (WT == kFewE4m3) {
-    const int64_t at = ((int64_t)q.expert * (K / 128) + step) * (N / 128) + q.col0 / 128;
-    if (lane == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(s + 4 * at));
-  } else if (WT == kFewMxfp4) {
-    if (step != q.step0 && (step & 3) != 0) return;
-    const uint8_t* row = s + ((int64_t)q.expert * N + q.col0 + lane) * (K / 32) + 8 * step;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + (int64_t)i * 32 * (K / 32)));
-  }
-}
-
 template <int WT, bool SHARED, bool DOWN>
 __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring,
                         uint32_t* counter) {
   const int lane = threadIdx.x & 31;
   const uint64_t once = ptx::policy_evict_first(), more = ptx::policy_evict_normal();
-  const int inner = SHARED ? p.S : p.I;
-  const int K = DOWN ? inner : p.d, N = DOWN ? p.d : inner;
   Control& c = *sm.c;
   const Share<WT, SHARED, DOWN> share(p, ls);
   auto slot_free = [&] {
@@ -532,11 +526,11 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
         if (!slot_free()) return false;
         if (lane == 0) {
           c.chunk[s] = id;
+          ptx::mbar_arrive(&c.issued[s]);
           ptx::mbar_arrive_expect_tx(&c.full[s], kTileBytes);
           load_tile<WT, SHARED>(m, p, q, step, sm.stages + s * kTileBytes, &c.full[s], q.again ? more : once);
         }
         __syncwarp();
-        prefetch_scales<WT>(p, q, step, K, N);
       }
       return true;
     });
@@ -546,6 +540,7 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
   if (!slot_free()) return false;
   if (lane == 0) {
     c.chunk[ring.n % kStages] = -1;
+    ptx::mbar_arrive(&c.issued[ring.n % kStages]);
     ptx::mbar_arrive(&c.full[ring.n % kStages]);
   }
   ++ring.n;
@@ -573,91 +568,148 @@ __device__ bool bring_columns(const FewParams& p, const Lists& ls, const Smem& s
   int id = blockIdx.x < share.total ? (int)blockIdx.x : -1;  // the first chunk needs no tile to be known by
   while (true) {
     if (id < 0) {
-      if (!wait(&c.full[ring.n % kStages], ring.n / kStages)) return false;
+      if (!wait(&c.issued[ring.n % kStages], ring.n / kStages)) return false;
       next_stage();
       return true;
     }
     const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
       const ColumnPlan<WT> plan(q);
       const int cols = q.rows * q.group;
-      const uint16_t* src = nullptr;
+      const uint8_t* src = nullptr;
       if (lane < cols) {
         if (DOWN)
-          src = (SHARED ? p.h_s : p.h_r) + ((int64_t)q.first * terms(WT) + lane) * share.K;
+          src = (SHARED ? p.h_s : p.h_r) + ((int64_t)q.first * h_terms(WT) + lane) * share.K * step_bytes(WT);
         else
-          src = (WT == kFewBf16 ? p.x : p.x16) + (int64_t)(SHARED ? lane : ls.ent[q.first + lane] / p.k) * p.d;
+          src = (WT == kFewBf16 ? p.x : p.x8) +
+                ((SHARED ? q.first + lane : ls.ent[q.first + lane / x_terms(WT)] / p.k) * x_terms(WT) +
+                 lane % x_terms(WT)) * (int64_t)p.d * step_bytes(WT);
       }
       for (int step = q.step0; step < q.step1; ++step) {
         if ((step - q.step0) % plan.units == 0) {
           const int buf = ring.cols & 1;
           if (!wait(&c.col_empty[buf], (ring.cols >> 1) + 1)) return false;
           const int last = min(q.step1, step + plan.units);
-          const uint32_t bytes = 2 * (min(share.K, last * kSteps) - step * kSteps);
+          const uint32_t bytes = step_bytes(WT) * (min(share.K, last * kSteps) - step * kSteps);
           if (lane == 0) ptx::mbar_arrive_expect_tx(&c.col_full[buf], bytes * cols);
           __syncwarp();
           if (lane < cols)
-            bulk_load(ptx::smem_u32(sm.cols) + buf * kColBytes + lane * plan.pitch, src + step * kSteps, bytes,
+            bulk_load(ptx::smem_u32(sm.cols) + buf * kColBytes + lane * plan.pitch, src + step * kSteps * step_bytes(WT), bytes,
                       &c.col_full[buf]);
           ++ring.cols;
         }
-        if (!wait(&c.full[ring.n % kStages], ring.n / kStages)) return false;
+        if (!wait(&c.issued[ring.n % kStages], ring.n / kStages)) return false;
         next_stage();
       }
       return true;
     });
-    if (!ok || !wait(&c.full[ring.n % kStages], ring.n / kStages)) return false;
+    if (!ok || !wait(&c.issued[ring.n % kStages], ring.n / kStages)) return false;
+    id = c.chunk[ring.n % kStages];
+  }
+}
+
+// ------------------------------------------------------------ scales
+// The scales of a routed share, by the router's warps: MXFP4's by all 64 threads,
+// two columns each, e4m3's by the first warp.
+template <int WT, bool DOWN>
+__device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
+  constexpr int kGroup = WT == kFewMxfp4 ? 4 : 8;  // units whose loads go together
+  const int lane = threadIdx.x & 31;
+  const int tid = threadIdx.x - kAllThreads + 32 * kRouterWarps;
+  const Share<WT, false, DOWN> share(p, ls);
+  Control& c = *sm.c;
+  auto wait = [&](int n) {
+    if (warp_wait(&c.issued[n % kStages], (n / kStages) & 1, &c.abort)) return true;
+    if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
+    return false;
+  };
+  auto hand_over = [&] {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&c.scaled[ring.n % kStages]);
+    ++ring.n;
+  };
+  const int words = share.K / 128;
+  int id = blockIdx.x < share.total ? (int)blockIdx.x : -1;
+  while (true) {
+    if (id < 0) {
+      if (!wait(ring.n)) return false;
+      hand_over();
+      return true;
+    }
+    const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
+      const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
+      for (int step0 = q.step0; step0 < q.step1; step0 += kGroup) {
+        if constexpr (WT == kFewE4m3) {
+          // lane 4 u + r: unit u of the group, row r of the piece
+          const int step = step0 + (lane >> 2), row = lane & 3;
+          float f = 0.0f;
+          if (step < q.step1) {
+            f = __ldg(reinterpret_cast<const float*>(scales) +
+                      ((int64_t)q.expert * (share.K / 128) + step) * (share.N / 128) + q.col0 / 128);
+            if (DOWN && row < q.rows) f *= __ldcg(p.h_scale + (int64_t)(q.first + row) * (share.K / 128) + step);
+          }
+          for (int u = 0; u < kGroup && step0 + u < q.step1; ++u) {
+            if (!wait(ring.n)) return false;
+            if ((lane >> 2) == u && tid < 32) {
+              float* to = sm.scales[ring.n % kStages].factor[row];
+              to[0] = f;
+              to[1] = f;
+            }
+            hand_over();
+          }
+        } else {
+          uint32_t w[kGroup][2][2];
+          float f[kGroup];
+          const int row = (tid >> 1) & 3, half = tid & 1;
+#pragma unroll
+          for (int u = 0; u < kGroup; ++u) {
+            const int step = step0 + u;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t* at = reinterpret_cast<const uint32_t*>(scales) +
+                                   ((int64_t)q.expert * share.N + q.col0 + tid + 64 * i) * words + 2 * step;
+              if (step >= q.step1) {
+                w[u][i][0] = w[u][i][1] = 0u;
+              } else if ((words & 1) == 0) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+                w[u][i][0] = v.x;
+                w[u][i][1] = v.y;
+              } else {
+                w[u][i][0] = __ldg(at);
+                w[u][i][1] = 2 * step + 1 < words ? __ldg(at + 1) : 0u;
+              }
+            }
+            f[u] = 1.0f;
+            if (DOWN && tid < 8 && row < q.rows && step < q.step1 && 2 * step + half < words)
+              f[u] = __ldcg(p.h_scale + (int64_t)(q.first + row) * words + 2 * step + half);
+          }
+#pragma unroll
+          for (int u = 0; u < kGroup; ++u) {
+            if (step0 + u < q.step1) {
+              if (!wait(ring.n)) return false;
+              StageScales& to = sm.scales[ring.n % kStages];
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<uint2*>(to.words[tid + 64 * i]) = make_uint2(w[u][i][0], w[u][i][1]);
+              if (tid < 8) to.factor[row][half] = f[u];
+              hand_over();
+            }
+          }
+        }
+      }
+      return true;
+    });
+    if (!ok || !wait(ring.n)) return false;
     id = c.chunk[ring.n % kStages];
   }
 }
 
 // ------------------------------------------------------------ consumers
 template <int WT, int NT, bool DOWN>
-__device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q, const uint8_t* scales, int K, int N,
-                                              const Smem& sm, Ring& ring) {
+__device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q, int K, const Smem& sm, Ring& ring) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3, half = warp >> 3;
   Control& ct = *sm.c;
   float acc[NT][4] = {};
-  const float* hp[NT];  // factors of the row that columns 2c and 2c + 1 belong to
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const bool in = DOWN && WT != kFewBf16 && 4 * j + c < q.rows;
-    hp[j] = in ? p.h_scale + (int64_t)(q.first + 4 * j + c) * (K / 128) : nullptr;
-  }
-  const float* sf = nullptr;
-  const uint32_t* sw = nullptr;
-  int64_t sld = 0;
-  if constexpr (WT == kFewE4m3) {
-    sld = N / 128;
-    sf = reinterpret_cast<const float*>(scales) + (int64_t)q.expert * (K / 128) * sld + q.col0 / 128;
-  } else if constexpr (WT == kFewMxfp4) {
-    sld = K / 128;  // words of four scales in a row
-    sw = reinterpret_cast<const uint32_t*>(scales) +
-         ((int64_t)q.expert * N + q.col0 + (warp & 7) * 16 + g) * sld + half;
-  }
-  // scales and factors are fetched while the unit before is multiplied; of
-  // MXFP4's last unit there may be one half only
-  struct Beside {
-    float f[NT];
-    float scale;
-    uint32_t s[2];
-  };
-  auto there = [&](int step) { return WT != kFewMxfp4 || 2 * step + half < sld; };
-  auto fetch = [&](Beside& x, int step) {
-    if (!there(step)) return;
-    if constexpr (WT != kFewBf16) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        x.f[j] = 1.0f;
-        if (DOWN && hp[j]) x.f[j] = hp[j][WT == kFewMxfp4 ? 2 * step + half : step];
-      }
-    }
-    if constexpr (WT == kFewE4m3) x.scale = __ldg(sf + step * sld);
-    if constexpr (WT == kFewMxfp4) {
-      x.s[0] = __ldg(sw + 2 * step);
-      x.s[1] = __ldg(sw + 8 * sld + 2 * step);
-    }
-  };
   const ColumnPlan<WT> plan(q);
   const int last = q.rows * q.group - 1;
   int left = 0;  // units whose columns are in the buffer
@@ -668,7 +720,7 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
   auto arrived = [&](uint64_t* bar, uint32_t parity) {
     if (!ptx::wait_bounded(bar, parity, &ct.abort)) raise_status(p.status, &ct.abort, kStatusTimeout);
   };
-  auto use = [&](const Beside& x, int step) {
+  for (int step = q.step0; step < q.step1; ++step) {
     if (left == 0) {
       const int buf = ring.cols & 1;
       arrived(&ct.col_full[buf], (ring.cols >> 1) & 1);
@@ -678,10 +730,22 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
     const int slot = ring.n % kStages;
     arrived(&ct.full[slot], (ring.n / kStages) & 1);
     const uint32_t tile = ptx::smem_u32(sm.stages) + slot * kTileBytes;
-    if constexpr (WT == kFewBf16) stage_bf16<NT>(tile, cols, plan.pitch, last, acc);
-    if constexpr (WT == kFewE4m3) stage_e4m3<NT>(tile, cols, plan.pitch, last, x.scale, x.f, acc);
-    if constexpr (WT == kFewMxfp4) {
-      if (there(step)) stage_mxfp4<NT>(tile, cols, plan.pitch, last, x.s, x.f, acc);
+    if constexpr (WT == kFewBf16) {
+      stage_bf16<NT>(tile, cols, plan.pitch, last, acc);
+    } else {
+      arrived(&ct.scaled[slot], (ring.scaled >> slot) & 1);
+      ring.scaled ^= 1u << slot;
+      const StageScales& sc = sm.scales[slot];
+      float f[NT];  // of the row that columns 2c and 2c + 1 belong to
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        f[j] = sc.factor[DOWN ? min((8 * j + 2 * c) / h_terms(WT), kMaxCols / h_terms(WT) - 1) : 0][half];
+      if constexpr (WT == kFewE4m3) {
+        stage_e4m3<NT>(tile, cols, plan.pitch, last, f, acc);
+      } else if (2 * step + half < K / 128) {  // the last unit may be half of one
+        const uint32_t s[2] = {sc.words[(warp & 7) * 16 + g][half], sc.words[(warp & 7) * 16 + g + 8][half]};
+        stage_mxfp4<NT>(tile, cols, plan.pitch, last, s, f, acc);
+      }
     }
     cols += ColumnPlan<WT>::kUnitBytes;
     __syncwarp();
@@ -690,17 +754,6 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
     if (--left == 0) {
       if (lane == 0) ptx::mbar_arrive(&ct.col_empty[ring.cols & 1]);
       ++ring.cols;
-    }
-  };
-  // two buffers by name: a copy from one to the other would wait for its loads
-  Beside even, odd;
-  fetch(even, q.step0);
-  for (int step = q.step0; step < q.step1; step += 2) {
-    if (step + 1 < q.step1) fetch(odd, step + 1);
-    use(even, step);
-    if (step + 1 < q.step1) {
-      if (step + 2 < q.step1) fetch(even, step + 2);
-      use(odd, step + 1);
     }
   }
   // the two halves of the steps, and the terms of each row, are joined by the
@@ -719,10 +772,13 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
   ptx::named_barrier(1 + pair, 64);
   for (int i = half * 32 + lane; i < q.rows * 16; i += 64) {
     const int r = i >> 4, col = i & 15;
+    // from the last term to the first: each is 2^-4 of the one before (bf16's
+    // terms carry their own exponents)
+    constexpr float kNext = WT == kFewBf16 ? 1.0f : 0.0625f;
     float a = 0.0f;
-    for (int t = 0; t < q.group; ++t) {
+    for (int t = q.group - 1; t >= 0; --t) {
       const float* x = red + (r * q.group + t) * kRedPitch + col;
-      a += x[0] + x[kMaxCols * kRedPitch];
+      a = fmaf(a, kNext, x[0] + x[kMaxCols * kRedPitch]);
     }
     q.out[r * q.ld + pair * 16 + col] = a;
   }
@@ -732,7 +788,6 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
 template <int WT, bool SHARED, bool DOWN>
 __device__ bool consume(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
   const Share<WT, SHARED, DOWN> share(p, ls);
-  const int K = share.K, N = share.N;
   Control& ct = *sm.c;
   volatile uint32_t* abort = &ct.abort;
   while (true) {
@@ -743,20 +798,24 @@ __device__ bool consume(const FewParams& p, const Lists& ls, const Smem& sm, Rin
     if (!ptx::named_barrier_and(1 + ((threadIdx.x >> 5) & 7), 64, there && *abort == 0)) return false;
     const int id = ct.chunk[slot];
     if (id < 0) {
+      if (WT != kFewBf16) {  // the scales' warps still read the mark
+        if (!ptx::wait_bounded(&ct.scaled[slot], (ring.scaled >> slot) & 1, &ct.abort))
+          raise_status(p.status, &ct.abort, kStatusTimeout);
+        ring.scaled ^= 1u << slot;
+      }
       __syncwarp();
       if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&ct.empty[slot]);
       ++ring.n;
       return true;
     }
     share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
-      const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
       const int cols = q.rows * q.group;
       if (cols <= 8)
-        consume_piece<WT, 1, DOWN>(p, q, scales, K, N, sm, ring);
-      else if (cols <= 16 || terms(WT) == 2)
-        consume_piece<WT, 2, DOWN>(p, q, scales, K, N, sm, ring);
+        consume_piece<WT, 1, DOWN>(p, q, share.K, sm, ring);
+      else if (cols <= 16)
+        consume_piece<WT, 2, DOWN>(p, q, share.K, sm, ring);
       else
-        consume_piece<WT, terms(WT) == 2 ? 2 : 3, DOWN>(p, q, scales, K, N, sm, ring);
+        consume_piece<WT, 3, DOWN>(p, q, share.K, sm, ring);
       return true;
     });
   }
@@ -778,11 +837,11 @@ __device__ void logits_share(const FewParams& p, double* red) {
     const int e = job % p.E, t0 = job / p.E * group, n = min(group, p.T - t0);
     double acc[kG] = {};
     for (int v = tid; v < nv; v += 256) {
-      const uint4 wv = __ldg(reinterpret_cast<const uint4*>(p.Wg + (int64_t)e * p.d) + v);
+      const uint4 wv = __ldg(reinterpret_cast<const uint4*>(p.Wg + (int64_t)e * p.d * 2) + v);
       uint4 xv[kG];
 #pragma unroll
       for (int t = 0; t < kG; ++t)
-        if (t < n) xv[t] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(t0 + t) * p.d) + v);
+        if (t < n) xv[t] = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(t0 + t) * p.d * 2) + v);
       const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
       double w[8];
 #pragma unroll
@@ -1002,12 +1061,12 @@ __device__ __forceinline__ void terms_of(float v, uint32_t (&t)[3]) {
   t[2] = __float_as_uint(q) >> 16;
 }
 
-// The power of two 2^(14 - e) for a largest magnitude of exponent e, as the
-// factor and its inverse; both normal numbers.
-__device__ __forceinline__ void fp16_factor(uint32_t top, float& factor, float& inverse) {
-  const uint32_t field = max(top >> 23, 15u);
-  factor = __uint_as_float((268u - field) << 23);
-  inverse = __uint_as_float((field - 14u) << 23);
+// The power of two 2^(7 - e) for a largest magnitude of exponent e, as the factor
+// and its inverse; both normal numbers.
+__device__ __forceinline__ void e4m3_factor(uint32_t top, float& factor, float& inverse) {
+  const uint32_t field = max(top >> 23, 8u);
+  factor = __uint_as_float((261u - field) << 23);
+  inverse = __uint_as_float((field - 7u) << 23);
 }
 
 // Bits of |v| where v is finite, 0 otherwise.
@@ -1016,26 +1075,17 @@ __device__ __forceinline__ uint32_t finite_bits(float v) {
   return b < 0x7f800000u ? b : 0u;
 }
 
-__device__ __forceinline__ uint32_t fp16_pair(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ float fp16_lo(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)v)); }
-__device__ __forceinline__ float fp16_hi(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)(v >> 16))); }
-
-// x of this CTA's tokens in fp16, each token times a power of two, for the
-// routed experts' codes.
+// x of this CTA's tokens as e4m3 terms, for the routed experts' codes.
 template <int WT>
-__device__ void fp16_tokens(const FewParams& p, uint32_t* red) {
+__device__ void e4m3_tokens(const FewParams& p, uint32_t* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int t = gridDim.x - 1 - blockIdx.x; t < p.T; t += gridDim.x) {
-    const uint32_t* x = reinterpret_cast<const uint32_t*>(p.x + (int64_t)t * p.d);
+    const uint2* x = reinterpret_cast<const uint2*>(p.x + (int64_t)t * p.d * 2);
     uint32_t top = 0;
-    for (int i = threadIdx.x; i < p.d / 2; i += kThreads) {
-      const uint32_t v = __ldg(x + i);
-      top = max(top, max(finite_bits(ptx::bf16_lo(v)), finite_bits(ptx::bf16_hi(v))));
+    for (int i = threadIdx.x; i < p.d / 4; i += kThreads) {
+      const uint2 v = __ldg(x + i);
+      top = max(top, max(max(finite_bits(ptx::bf16_lo(v.x)), finite_bits(ptx::bf16_hi(v.x))),
+                         max(finite_bits(ptx::bf16_lo(v.y)), finite_bits(ptx::bf16_hi(v.y)))));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -1045,44 +1095,26 @@ __device__ void fp16_tokens(const FewParams& p, uint32_t* red) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     float factor, inverse;
-    fp16_factor(top, factor, inverse);
+    e4m3_factor(top, factor, inverse);
     if (threadIdx.x == 0) p.x_scale[t] = inverse;
-    for (int i = threadIdx.x; i < p.d / 2; i += kThreads) {
-      const uint32_t v = __ldg(x + i);
-      store_pair<WT>(p.x16 + (int64_t)t * p.d, 2 * i, fp16_pair(ptx::bf16_lo(v) * factor, ptx::bf16_hi(v) * factor));
+    for (int i = threadIdx.x; i < p.d / 4; i += kThreads) {
+      const uint2 v = __ldg(x + i);
+      const float f[4] = {ptx::bf16_lo(v.x), ptx::bf16_hi(v.x), ptx::bf16_lo(v.y), ptx::bf16_hi(v.y)};
+      store_terms8<WT, x_terms(WT)>(p.x8 + (int64_t)t * x_terms(WT) * p.d, p.d, 4 * i, f, factor);
     }
     consumer_sync();
   }
 }
 
-// Four values of h, columns k to k + 3, to a row's terms [terms][K].
-template <int WT>
-__device__ __forceinline__ void store_terms(uint16_t* to, int K, int k, const float (&h)[4]) {
-  uint32_t w[3][2];
-  if (WT == kFewBf16) {
-    uint32_t t[4][3];
+// Four values of h, columns k to k + 3, to a row's three bf16 terms [3][K].
+__device__ __forceinline__ void store_terms(uint8_t* to, int K, int k, const float (&h)[4]) {
+  uint32_t t[4][3];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) terms_of(h[i], t[i]);
+  for (int i = 0; i < 4; ++i) terms_of(h[i], t[i]);
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      w[q][0] = t[0][q] | (t[1][q] << 16);
-      w[q][1] = t[2][q] | (t[3][q] << 16);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float a = h[2 * i], b = h[2 * i + 1];
-      w[0][i] = fp16_pair(a, b);
-      // the second term of an infinity or NaN is none
-      const float ra = finite_bits(a) == (__float_as_uint(a) & 0x7fffffffu) ? a - fp16_lo(w[0][i]) : 0.0f;
-      const float rb = finite_bits(b) == (__float_as_uint(b) & 0x7fffffffu) ? b - fp16_hi(w[0][i]) : 0.0f;
-      w[1][i] = fp16_pair(ra, rb);
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < terms(WT); ++q)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) store_pair<WT>(to + (int64_t)q * K, k + 2 * i, w[q][i]);
+  for (int q = 0; q < 3; ++q)
+    *reinterpret_cast<uint2*>(to + ((int64_t)q * K + k) * 2) =
+        make_uint2(t[0][q] | (t[1][q] << 16), t[2][q] | (t[3][q] << 16));
 }
 
 // h of every row, four columns a lane and 128 a warp.
@@ -1104,22 +1136,20 @@ __device__ void activations(const FewParams& p, const Lists& ls) {
     const int parts = shared ? p.split_up_s.parts : p.split_up_r.parts;
     const float4 g = sum_parts(buf + ((int64_t)(row * 2) * blocks + block) * parts * kFewCols, parts);
     const float4 u = sum_parts(buf + ((int64_t)(row * 2 + 1) * blocks + block) * parts * kFewCols, parts);
-    float h[4] = {gated(g.x * f, u.x * f), gated(g.y * f, u.y * f), gated(g.z * f, u.z * f), gated(g.w * f, u.w * f)};
+    const float h[4] = {gated(g.x * f, u.x * f), gated(g.y * f, u.y * f), gated(g.z * f, u.z * f), gated(g.w * f, u.w * f)};
     const int k = block * kFewCols + 4 * lane;
     if (shared) {
-      store_terms<kFewBf16>(p.h_s + (int64_t)row * 3 * p.S, p.S, k, h);
+      store_terms(p.h_s + (int64_t)row * 3 * p.S * 2, p.S, k, h);
+    } else if constexpr (WT == kFewBf16) {
+      store_terms(p.h_r + (int64_t)row * 3 * p.I * 2, p.I, k, h);
     } else {
-      if (WT != kFewBf16) {
-        uint32_t top = max(max(finite_bits(h[0]), finite_bits(h[1])), max(finite_bits(h[2]), finite_bits(h[3])));
+      uint32_t top = max(max(finite_bits(h[0]), finite_bits(h[1])), max(finite_bits(h[2]), finite_bits(h[3])));
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float factor, inverse;
-        fp16_factor(top, factor, inverse);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] *= factor;
-        if (lane == 0) p.h_scale[(int64_t)row * rb + block] = inverse;
-      }
-      store_terms<WT>(p.h_r + (int64_t)row * terms(WT) * p.I, p.I, k, h);
+      for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      float factor, inverse;
+      e4m3_factor(top, factor, inverse);
+      if (lane == 0) p.h_scale[(int64_t)row * rb + block] = inverse;
+      store_terms8<WT, h_terms(WT)>(p.h_r + (int64_t)row * h_terms(WT) * p.I, p.I, k, h, factor);
     }
   }
 }
@@ -1173,18 +1203,23 @@ __global__ void __launch_bounds__(kAllThreads, 1)
   sm.cols = sm.stages + kStages * kTileBytes;
   sm.red = reinterpret_cast<float*>(sm.cols + 2 * kColBytes);
   sm.c = &ct;
+  // the router's keys, and where it is done, the scales
   uint64_t* keys = reinterpret_cast<uint64_t*>(sm.red + 8 * kRedFloats);
+  sm.scales = reinterpret_cast<StageScales*>(keys);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&ct.full[s], 1);
       ptx::mbar_init(&ct.empty[s], kWarps + 1);
+      ptx::mbar_init(&ct.issued[s], 1);
+      ptx::mbar_init(&ct.scaled[s], kRouterWarps);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&ct.col_full[b], 1);
       ptx::mbar_init(&ct.col_empty[b], kWarps);
     }
     ptx::mbar_init(&ct.ready, 1);
+    ptx::mbar_init(&ct.started, 1);
     ptx::mbar_init(&ct.routed, 32 * kRouterWarps);
     ct.abort = 0u;
     ct.never = 0u;
@@ -1208,6 +1243,10 @@ __global__ void __launch_bounds__(kAllThreads, 1)
       ok = false;
     }
     ok = ok && __all_sync(0xffffffffu, *abort == 0);  // the router gave up: there are no lists
+    if ((threadIdx.x & 31) == 0) {
+      ct.first = ring.n;
+      ptx::mbar_arrive(&ct.started);
+    }
     if (ok) ok = produce<RT, false, false>(maps, p, ls, sm, ring, p.bar + 5);
     if (ok) ok = produce<RT, false, true>(maps, p, ls, sm, ring, p.bar + 6);
     if (ok && p.S > 0) produce<kFewBf16, true, true>(maps, p, ls, sm, ring, p.bar + 7);
@@ -1222,7 +1261,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     bool ok = true;
     auto wait = [&](uint64_t* bar) {
       if (warp_wait(bar, 0, abort) && __all_sync(0xffffffffu, *abort == 0)) {
-        ptx::fence_proxy_async_all();  // x in fp16, and h, were written by ordinary stores
+        ptx::fence_proxy_async_all();  // x's terms and h were written by ordinary stores
         return true;
       }
       raise_status(p.status, abort, kStatusTimeout);
@@ -1242,12 +1281,23 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     router_sync();
     if (*abort == 0) route(p, ls, keys);
     ptx::mbar_arrive(&ct.routed);
+    if constexpr (RT != kFewBf16) {
+      auto wait = [&](uint64_t* bar) {
+        return warp_wait(bar, 0, abort) && __all_sync(0xffffffffu, *abort == 0);
+      };
+      // both warps are done with the keys, and the share has begun
+      Ring ring;
+      if (wait(&ct.routed) && wait(&ct.started)) {
+        ring.n = ct.first;
+        if (bring_scales<RT, false>(p, ls, sm, ring) && wait(&ct.ready)) bring_scales<RT, true>(p, ls, sm, ring);
+      }
+    }
   } else {
     // ---------------------------------------------- consumers
     Ring ring;
     logits_share(p, reinterpret_cast<double*>(sm.red));
     if (RT != kFewBf16) {
-      fp16_tokens<RT>(p, reinterpret_cast<uint32_t*>(sm.red));
+      e4m3_tokens<RT>(p, reinterpret_cast<uint32_t*>(sm.red));
       ptx::fence_proxy_async_all();  // bulk copies will read them
     }
     grid_arrive(p.bar + 0);
@@ -1274,7 +1324,8 @@ __global__ void __launch_bounds__(kAllThreads, 1)
 template <int RT>
 cudaError_t launch(const FewParams& p, const FewMaps& maps, int sms, cudaStream_t stream) {
   // stages, the pairs' joins, the columns, a routing key and a logit per expert and router warp
-  const size_t smem = 1024 + kStages * kTileBytes + 2 * kColBytes + 8 * kRedFloats * 4 + (size_t)kRouterWarps * p.E * 12;
+  const size_t smem = 1024 + kStages * kTileBytes + 2 * kColBytes + 8 * kRedFloats * 4 + 
+                      std::max((size_t)kRouterWarps * p.E * 12, kStages * sizeof(StageScales));
   auto kernel = few_kernel<RT>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;

@@ -44,8 +44,8 @@ struct FewParams {
   int route, n_group, topk_group, group_topn;
   float route_scale;
   int y_bf16;
-  const uint16_t* x;
-  const uint16_t* Wg;
+  const uint8_t* x;  // bf16 [T, d]
+  const uint8_t* Wg;
   const float* bias;  // may be null
   const uint8_t *s1, *s3, *s2;  // fp32 block scales or scale bytes
   void* y;
@@ -57,10 +57,10 @@ struct FewParams {
   FewSplit split_up_r, split_up_s, split_dn_r, split_dn_s;
   float* logits;       // [T, E]
   float *up_r, *up_s, *dn_r, *dn_s;  // the chunks' sums, [row][segment][part][kFewCols]
-  uint16_t* h_r;       // [T * k][terms][I] terms of the routed rows' activations: 3 bf16 or 2 fp16
-  uint16_t* h_s;       // [T][3][S] bf16
-  // fp16 weights' codes: x in fp16, and the powers of two that undo its and h's scaling
-  uint16_t* x16;       // [T, d]
+  uint8_t* h_r;        // [T * k][terms][I]: three bf16 terms of the routed rows' activations, or six e4m3 ones
+  uint8_t* h_s;        // [T][3][S] bf16
+  // e4m3 and MXFP4 weights: x's e4m3 terms, and the powers of two that undo its and h's scaling
+  uint8_t* x8;         // [T][3][d]
   float* x_scale;      // [T]
   float* h_scale;      // [T * k][I / 128]
 };

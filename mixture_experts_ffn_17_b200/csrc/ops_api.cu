@@ -36,7 +36,7 @@ int few_weights(const moe_shape& s) {
 
 struct FewLayout {
   FewSplit split_up_r, split_up_s, split_dn_r, split_dn_s;
-  size_t logits, up_r, up_s, dn_r, dn_s, h_r, h_s, x16, x_scale, h_scale, total;
+  size_t logits, up_r, up_s, dn_r, dn_s, h_r, h_s, x8, x_scale, h_scale, total;
 };
 
 FewLayout few_layout(const moe_shape& s) {
@@ -62,7 +62,7 @@ FewLayout few_layout(const moe_shape& s) {
   L.dn_s = take(s.shared_inter > 0 ? sums(T * bd, L.split_dn_s) : 0);
   L.h_r = take((size_t)rows * 3 * s.inter * 2);
   L.h_s = take((size_t)T * 3 * s.shared_inter * 2);
-  L.x16 = take((size_t)T * s.d * 2);
+  L.x8 = take((size_t)T * 3 * s.d);
   L.x_scale = take((size_t)T * 4);
   L.h_scale = take((size_t)rows * bi * 4);
   L.total = off;
@@ -204,8 +204,8 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.route_scale = s.route_scale;
   p.y_bf16 = s.y_dtype == MOE_BF16;
   auto bytes = [](const void* q) { return static_cast<const uint8_t*>(q); };
-  p.x = static_cast<const uint16_t*>(x);
-  p.Wg = static_cast<const uint16_t*>(Wg);
+  p.x = bytes(x);
+  p.Wg = bytes(Wg);
   p.bias = s.route == MOE_ROUTE_SIGMOID_GROUP ? bias : nullptr;
   p.s1 = bytes(s1);
   p.s3 = bytes(s3);
@@ -225,9 +225,9 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.up_s = at<float>(ws, L.up_s);
   p.dn_r = at<float>(ws, L.dn_r);
   p.dn_s = at<float>(ws, L.dn_s);
-  p.h_r = at<uint16_t>(ws, L.h_r);
-  p.h_s = at<uint16_t>(ws, L.h_s);
-  p.x16 = at<uint16_t>(ws, L.x16);
+  p.h_r = at<uint8_t>(ws, L.h_r);
+  p.h_s = at<uint8_t>(ws, L.h_s);
+  p.x8 = at<uint8_t>(ws, L.x8);
   p.x_scale = at<float>(ws, L.x_scale);
   p.h_scale = at<float>(ws, L.h_scale);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
