@@ -41,7 +41,8 @@
 // columns by 16 steps, ldmatrix from the stage) and the activations as B's
 // columns, 8 at a time.  (tcgen05 would pad the columns to 16 and could not take
 // these codes unconverted; the tensor pipe is idle either way.)  Consumer warp w
-// takes columns 16 (w % 8) of a tile and one half of its steps (w / 8).
+// takes columns 16 (w % 8) of every second tile (w / 8): a tile's chain of waits,
+// loads and MMAs is longer than the time HBM needs for one.
 //   bf16 weights: x is bf16 as it comes; h is fp32 and goes in as three bf16
 //   terms (8 bits each: 24 in all).
 //   e4m3 codes go into the MMA as they are (m16n8k32, fp32 sums as exact as
@@ -96,12 +97,15 @@ struct Lists {  // what the routing leaves in shared memory
 struct Control {
   uint64_t full[kStages], empty[kStages];
   uint64_t col_full[2], col_empty[2];
-  uint64_t issued[kStages];   // a stage's chunk is known, its tile on the way
+  // a stage's chunk is known, its tile on the way: two turns of the ring, since
+  // who has no part in a stage may still be looking at it when the stage's place
+  // is filled again, but not when the place after it is
+  uint64_t issued[2 * kStages];
   uint64_t scaled[kStages];   // its scales are there
   uint64_t started;           // `first` is there
   int first;                  // first stage of the routed experts
   uint64_t ready;   // h is there, in all CTAs
-  int chunk[kStages];  // which chunk a stage belongs to; -1: the share is done
+  int chunk[2 * kStages];  // which chunk a stage belongs to; -1: the share is done
   uint64_t routed;  // the lists are there
   uint32_t abort, never;
 };
@@ -285,26 +289,28 @@ __device__ __forceinline__ void store_terms8(uint8_t* column, int64_t ld, int k,
   }
 }
 
-// One stage of a piece: this warp's sums over its half of the steps.  cols: the
-// stage's part of the first B column, the others `pitch` bytes apart, up to column
-// `last` (which stands in for those that do not exist: an MMA's columns do not mix).
+// One stage of a piece: a warp's sums for its 16 columns.  cols: the stage's part of
+// the first B column, the others `pitch` bytes apart, up to column `last` (which
+// stands in for those that do not exist: an MMA's columns do not mix).
 // bf16: two boxes of 64 columns, [steps][64 columns].
 template <int NT>
 __device__ __forceinline__ void stage_bf16(uint32_t tile, uint32_t cols, int pitch, int last, float (&acc)[NT][4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane >> 3, r = lane & 7;
-  const int k0 = (warp >> 3) * 32;
-  uint32_t b[NT][4];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) ldsm(b[j], cols + min(8 * j + r, last) * pitch + (k0 + 8 * i) * 2);
+  for (int p = 0; p < 2; ++p) {
+    uint32_t b[NT][4];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int k = k0 + 16 * q + (i >> 1) * 8 + r;
-    const int chunk = (warp & 3) * 2 + (i & 1);
-    uint32_t a[4];
-    ldsm_t(a, tile + ((warp >> 2) & 1) * 8192 + k * 128 + ((chunk ^ (k & 7)) << 4));
+    for (int j = 0; j < NT; ++j) ldsm(b[j], cols + min(8 * j + r, last) * pitch + (32 * p + 8 * i) * 2);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) mma_bf16(acc[j], a, b[j][2 * q], b[j][2 * q + 1]);
+    for (int q = 0; q < 2; ++q) {
+      const int k = 32 * p + 16 * q + (i >> 1) * 8 + r;
+      const int chunk = (warp & 3) * 2 + (i & 1);
+      uint32_t a[4];
+      ldsm_t(a, tile + ((warp >> 2) & 1) * 8192 + k * 128 + ((chunk ^ (k & 7)) << 4));
+#pragma unroll
+      for (int j = 0; j < NT; ++j) mma_bf16(acc[j], a, b[j][2 * q], b[j][2 * q + 1]);
+    }
   }
 }
 
@@ -317,29 +323,29 @@ __device__ __forceinline__ void stage_e4m3(uint32_t tile, uint32_t cols, int pit
                                            float (&acc)[NT][4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane >> 3, r = lane & 7, g = lane >> 2, c = lane & 3;
-  float part[NT][4] = {};
+  float part[2][NT][4] = {};  // two sums: an MMA that adds to the one before it waits for it
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int k0 = (warp >> 3) * 64 + 32 * q, k = k0 + 8 * i + r;
+  for (int q = 0; q < 4; ++q) {
+    const int k = 32 * q + 8 * i + r;
     uint32_t w[4];
     ldsm_t(w, tile + k * 128 + (((warp & 7) ^ (k & 7)) << 4));
     const uint32_t a[4] = {__byte_perm(w[0], w[1], 0x6420), __byte_perm(w[0], w[1], 0x7531),
                            __byte_perm(w[2], w[3], 0x6420), __byte_perm(w[2], w[3], 0x7531)};
 #pragma unroll
-    for (int j = 0; j < NT; ++j) mma_e4m3(part[j], a, lds8(cols + min(8 * j + g, last) * pitch + k0 + 8 * c));
+    for (int j = 0; j < NT; ++j) mma_e4m3(part[q & 1][j], a, lds8(cols + min(8 * j + g, last) * pitch + 32 * q + 8 * c));
   }
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(part[j][e], f[j], acc[j][e]);
+    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(part[0][j][e] + part[1][j][e], f[j], acc[j][e]);
 }
 
-// MXFP4: [128 columns][steps / 2] codes; lane (g, c) holds the eight codes 8c of
-// a scale block for columns g and g + 8, whose scale bytes are in s[0], s[1].
-// f[j]: the columns' factor.
+// MXFP4: [128 columns][steps / 2] codes, one half of the steps; lane (g, c) holds
+// the eight codes 8c of a scale block for columns g and g + 8, whose scale bytes
+// are in s[0], s[1].  f[j]: the columns' factor.
 template <int NT>
-__device__ __forceinline__ void stage_mxfp4(uint32_t tile, uint32_t cols, int pitch, int last, const uint32_t (&s)[2],
-                                            const float (&f)[NT], float (&acc)[NT][4]) {
+__device__ __forceinline__ void stage_mxfp4(uint32_t tile, int half, uint32_t cols, int pitch, int last,
+                                            const uint32_t (&s)[2], const float (&f)[NT], float (&acc)[NT][4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = lane >> 3, r = lane & 7, g = lane >> 2, c = lane & 3;
   const int n = (warp & 7) * 16 + (i & 1) * 8 + r;
@@ -350,7 +356,7 @@ __device__ __forceinline__ void stage_mxfp4(uint32_t tile, uint32_t cols, int pi
 #pragma unroll
   for (int p = 0; p < 2; ++p) {  // two scale blocks
     uint32_t w[4];
-    const int chunk = (warp >> 3) * 4 + 2 * p + (i >> 1);
+    const int chunk = half * 4 + 2 * p + (i >> 1);
     ldsm(w, tile + n * 128 + ((chunk ^ (n & 7)) << 4));
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -361,7 +367,7 @@ __device__ __forceinline__ void stage_mxfp4(uint32_t tile, uint32_t cols, int pi
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        mma_e4m3(part, a, lds8(cols + min(8 * j + g, last) * pitch + (warp >> 3) * 128 + blk * 32 + 8 * c));
+        mma_e4m3(part, a, lds8(cols + min(8 * j + g, last) * pitch + half * 128 + blk * 32 + 8 * c));
         sum[j][0] = fmaf(part[0], s0[blk], sum[j][0]);
         sum[j][1] = fmaf(part[1], s0[blk], sum[j][1]);
         sum[j][2] = fmaf(part[2], s1[blk], sum[j][2]);
@@ -525,8 +531,8 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
         const int s = ring.n % kStages;
         if (!slot_free()) return false;
         if (lane == 0) {
-          c.chunk[s] = id;
-          ptx::mbar_arrive(&c.issued[s]);
+          c.chunk[ring.n % (2 * kStages)] = id;
+          ptx::mbar_arrive(&c.issued[ring.n % (2 * kStages)]);
           ptx::mbar_arrive_expect_tx(&c.full[s], kTileBytes);
           load_tile<WT, SHARED>(m, p, q, step, sm.stages + s * kTileBytes, &c.full[s], q.again ? more : once);
         }
@@ -539,8 +545,8 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
   }
   if (!slot_free()) return false;
   if (lane == 0) {
-    c.chunk[ring.n % kStages] = -1;
-    ptx::mbar_arrive(&c.issued[ring.n % kStages]);
+    c.chunk[ring.n % (2 * kStages)] = -1;
+    ptx::mbar_arrive(&c.issued[ring.n % (2 * kStages)]);
     ptx::mbar_arrive(&c.full[ring.n % kStages]);
   }
   ++ring.n;
@@ -568,7 +574,7 @@ __device__ bool bring_columns(const FewParams& p, const Lists& ls, const Smem& s
   int id = blockIdx.x < share.total ? (int)blockIdx.x : -1;  // the first chunk needs no tile to be known by
   while (true) {
     if (id < 0) {
-      if (!wait(&c.issued[ring.n % kStages], ring.n / kStages)) return false;
+      if (!wait(&c.issued[ring.n % (2 * kStages)], ring.n / (2 * kStages))) return false;
       next_stage();
       return true;
     }
@@ -597,13 +603,13 @@ __device__ bool bring_columns(const FewParams& p, const Lists& ls, const Smem& s
                       &c.col_full[buf]);
           ++ring.cols;
         }
-        if (!wait(&c.issued[ring.n % kStages], ring.n / kStages)) return false;
+        if (!wait(&c.issued[ring.n % (2 * kStages)], ring.n / (2 * kStages))) return false;
         next_stage();
       }
       return true;
     });
-    if (!ok || !wait(&c.issued[ring.n % kStages], ring.n / kStages)) return false;
-    id = c.chunk[ring.n % kStages];
+    if (!ok || !wait(&c.issued[ring.n % (2 * kStages)], ring.n / (2 * kStages))) return false;
+    id = c.chunk[ring.n % (2 * kStages)];
   }
 }
 
@@ -618,7 +624,7 @@ __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm
   const Share<WT, false, DOWN> share(p, ls);
   Control& c = *sm.c;
   auto wait = [&](int n) {
-    if (warp_wait(&c.issued[n % kStages], (n / kStages) & 1, &c.abort)) return true;
+    if (warp_wait(&c.issued[n % (2 * kStages)], (n / (2 * kStages)) & 1, &c.abort)) return true;
     if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
     return false;
   };
@@ -699,7 +705,7 @@ __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm
       return true;
     });
     if (!ok || !wait(ring.n)) return false;
-    id = c.chunk[ring.n % kStages];
+    id = c.chunk[ring.n % (2 * kStages)];
   }
 }
 
@@ -707,7 +713,7 @@ __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm
 template <int WT, int NT, bool DOWN>
 __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q, int K, const Smem& sm, Ring& ring) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, c = lane & 3, half = warp >> 3;
+  const int g = lane >> 2, c = lane & 3, team = warp >> 3;
   Control& ct = *sm.c;
   float acc[NT][4] = {};
   const ColumnPlan<WT> plan(q);
@@ -728,40 +734,46 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
       left = min(plan.units, q.step1 - step);
     }
     const int slot = ring.n % kStages;
-    arrived(&ct.full[slot], (ring.n / kStages) & 1);
-    const uint32_t tile = ptx::smem_u32(sm.stages) + slot * kTileBytes;
-    if constexpr (WT == kFewBf16) {
-      stage_bf16<NT>(tile, cols, plan.pitch, last, acc);
-    } else {
-      arrived(&ct.scaled[slot], (ring.scaled >> slot) & 1);
-      ring.scaled ^= 1u << slot;
-      const StageScales& sc = sm.scales[slot];
-      float f[NT];  // of the row that columns 2c and 2c + 1 belong to
+    if ((ring.n & 1) == team) {
+      arrived(&ct.full[slot], (ring.n / kStages) & 1);
+      const uint32_t tile = ptx::smem_u32(sm.stages) + slot * kTileBytes;
+      if constexpr (WT == kFewBf16) {
+        stage_bf16<NT>(tile, cols, plan.pitch, last, acc);
+      } else {
+        arrived(&ct.scaled[slot], (ring.scaled >> slot) & 1);
+        const StageScales& sc = sm.scales[slot];
+        const int halves = WT == kFewMxfp4 && 2 * step + 1 < K / 128 ? 2 : 1;  // MXFP4's last unit may be half of one
+        for (int h = 0; h < halves; ++h) {
+          float f[NT];  // of the row that columns 2c and 2c + 1 belong to
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        f[j] = sc.factor[DOWN ? min((8 * j + 2 * c) / h_terms(WT), kMaxCols / h_terms(WT) - 1) : 0][half];
-      if constexpr (WT == kFewE4m3) {
-        stage_e4m3<NT>(tile, cols, plan.pitch, last, f, acc);
-      } else if (2 * step + half < K / 128) {  // the last unit may be half of one
-        const uint32_t s[2] = {sc.words[(warp & 7) * 16 + g][half], sc.words[(warp & 7) * 16 + g + 8][half]};
-        stage_mxfp4<NT>(tile, cols, plan.pitch, last, s, f, acc);
+          for (int j = 0; j < NT; ++j)
+            f[j] = sc.factor[DOWN ? min((8 * j + 2 * c) / h_terms(WT), kMaxCols / h_terms(WT) - 1) : 0][h];
+          if constexpr (WT == kFewE4m3) {
+            stage_e4m3<NT>(tile, cols, plan.pitch, last, f, acc);
+          } else {
+            const uint32_t s[2] = {sc.words[(warp & 7) * 16 + g][h], sc.words[(warp & 7) * 16 + g + 8][h]};
+            stage_mxfp4<NT>(tile, h, cols, plan.pitch, last, s, f, acc);
+          }
+        }
       }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&ct.empty[slot]);
     }
+    if (WT != kFewBf16) ring.scaled ^= 1u << slot;
     cols += ColumnPlan<WT>::kUnitBytes;
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&ct.empty[slot]);
     ++ring.n;
     if (--left == 0) {
+      __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&ct.col_empty[ring.cols & 1]);
       ++ring.cols;
     }
   }
-  // the two halves of the steps, and the terms of each row, are joined by the
+  // the two teams' sums, and the terms of each row, are joined by the
   // pair of warps that has these 16 columns
   const int pair = warp & 7;
   float* red = sm.red + pair * kRedFloats;
   const int lo = WT == kFewE4m3 ? 2 * g : g, hi = WT == kFewE4m3 ? 2 * g + 1 : g + 8;
-  float* to = red + half * kMaxCols * kRedPitch;
+  float* to = red + team * kMaxCols * kRedPitch;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     to[(8 * j + 2 * c) * kRedPitch + lo] = acc[j][0];
@@ -770,7 +782,7 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
     to[(8 * j + 2 * c + 1) * kRedPitch + hi] = acc[j][3];
   }
   ptx::named_barrier(1 + pair, 64);
-  for (int i = half * 32 + lane; i < q.rows * 16; i += 64) {
+  for (int i = team * 32 + lane; i < q.rows * 16; i += 64) {
     const int r = i >> 4, col = i & 15;
     // from the last term to the first: each is 2^-4 of the one before (bf16's
     // terms carry their own exponents)
@@ -791,20 +803,21 @@ __device__ bool consume(const FewParams& p, const Lists& ls, const Smem& sm, Rin
   Control& ct = *sm.c;
   volatile uint32_t* abort = &ct.abort;
   while (true) {
-    const int slot = ring.n % kStages;
-    const bool there = warp_wait(&ct.full[slot], (ring.n / kStages) & 1, &ct.abort);
+    const int at = ring.n % (2 * kStages);
+    const bool there = warp_wait(&ct.issued[at], (ring.n / (2 * kStages)) & 1, &ct.abort);
     if (!there) raise_status(p.status, &ct.abort, kStatusTimeout);
     // both warps of a pair take the chunk or neither
     if (!ptx::named_barrier_and(1 + ((threadIdx.x >> 5) & 7), 64, there && *abort == 0)) return false;
-    const int id = ct.chunk[slot];
+    const int id = ct.chunk[at];
     if (id < 0) {
+      const int slot = ring.n % kStages;
       if (WT != kFewBf16) {  // the scales' warps still read the mark
         if (!ptx::wait_bounded(&ct.scaled[slot], (ring.scaled >> slot) & 1, &ct.abort))
           raise_status(p.status, &ct.abort, kStatusTimeout);
         ring.scaled ^= 1u << slot;
       }
       __syncwarp();
-      if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&ct.empty[slot]);
+      if ((threadIdx.x & 31) == 0 && (ring.n & 1) == (threadIdx.x >> 8)) ptx::mbar_arrive(&ct.empty[slot]);
       ++ring.n;
       return true;
     }
@@ -1210,8 +1223,9 @@ __global__ void __launch_bounds__(kAllThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&ct.full[s], 1);
-      ptx::mbar_init(&ct.empty[s], kWarps + 1);
+      ptx::mbar_init(&ct.empty[s], kWarps / 2 + 1);
       ptx::mbar_init(&ct.issued[s], 1);
+      ptx::mbar_init(&ct.issued[s + kStages], 1);
       ptx::mbar_init(&ct.scaled[s], kRouterWarps);
     }
     for (int b = 0; b < 2; ++b) {
