@@ -45,16 +45,14 @@
 // loads and MMAs is longer than the time HBM needs for one.
 //   bf16 weights: x is bf16 as it comes; h is fp32 and goes in as three bf16
 //   terms (8 bits each: 24 in all).
-//   e4m3 codes go into the MMA as they are (m16n8k32, fp32 sums as exact as
-//   bf16's), MXFP4 codes as e4m3 values, by moving their bits: exponent and
-//   mantissa read 2^-6 times the code's value there.  (As fp16, through the
-//   conversion instructions, which run at a sixteenth of the rate, or by moving
-//   bits with two MMAs for one, the decoding bound the kernel at 2 to 3.8 TB/s.)
-//   The activations go in as sums of e4m3 terms, each rounding what is left, with
-//   4 bits more: x in three, h in six, after a power of two has put the largest
-//   of a token (of 128 values of h) between 2^7 and 2^8.  A bf16 x is exact down
-//   to 2^-13 of the largest and to 2^-25 of it below, h to 2^-24 of itself and
-//   2^-37 of the largest.  An infinity has no e4m3 value and goes in as NaN.
+//   e4m3 and MXFP4 codes become fp16, which holds them exactly, by moving their
+//   bits: exponent and mantissa read 2^-8 and 2^-14 times the code's value there,
+//   made up in the sums' factors.  (The conversion instructions run at a sixteenth
+//   of the rate; e4m3 MMAs are made of conversions and fp16 ones on this GPU, 2280
+//   instructions a stage.)  x and h are fp16 too, times a power of two that puts
+//   the largest of a token (of 128 values of h) between 2^14 and 2^15: a bf16 x
+//   fits exactly down to 2^-28 of the largest and to 2^-39 of it below; h goes in
+//   as two terms (22 bits).
 // Block scales multiply fp32 sums.
 #include <algorithm>
 #include <cstdint>
@@ -179,12 +177,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint2 b) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
@@ -201,16 +199,33 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-// Eight MXFP4 codes as e4m3 values times 2^-6: the even codes and the odd ones.
-__device__ __forceinline__ void mx_e4m3(uint32_t w, uint32_t& even, uint32_t& odd) {
-  even = ((w << 4) & 0x80808080u) | ((w << 2) & 0x1c1c1c1cu);
-  odd = (w & 0x80808080u) | ((w >> 2) & 0x1c1c1c1cu);
+// Four e4m3 codes to two fp16 pairs, bytes (0, 2) and (1, 3), times 2^-8.  The
+// code 0x7f, NaN, is not looked at (it reads 480).
+__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t& even, uint32_t& odd) {
+  even = ((w << 8) & 0x80008000u) | ((w << 7) & 0x3f803f80u);
+  odd = (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
 }
 
-__device__ __forceinline__ uint2 lds8(uint32_t addr) {
-  uint2 r;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
+// The same times 1 by the conversion instruction, NaN included.
+__device__ __forceinline__ uint32_t e4m3_values(uint32_t two_codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two_codes));
   return r;
+}
+
+// Eight MXFP4 codes to four fp16 pairs, codes j and j + 4, times 2^-14.
+__device__ __forceinline__ void mx_pairs(uint32_t w, uint32_t (&f)[4]) {
+  f[0] = ((w << 12) & 0x80008000u) | ((w << 9) & 0x0e000e00u);
+  f[1] = ((w << 8) & 0x80008000u) | ((w << 5) & 0x0e000e00u);
+  f[2] = ((w << 4) & 0x80008000u) | ((w << 1) & 0x0e000e00u);
+  f[3] = (w & 0x80008000u) | ((w >> 3) & 0x0e000e00u);
+}
+
+__device__ __forceinline__ void lds(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -232,60 +247,16 @@ __device__ __forceinline__ void scales_of(uint32_t w, float (&f)[4]) {
   f[3] = ptx::bf16_hi(hi);
 }
 
-// Four e4m3 values, steps k to k + 3 (k a multiple of 4) of a column, to their
-// places: lane c of an MMA takes 8 bytes in a row of each 32 steps, for e4m3
-// weights (which ldmatrix.trans brings two steps of eight at a time) steps 2c and
-// 2c + 1 of each eight, for MXFP4 the even ones of 8c to 8c + 7 and then the odd.
+// Values k and k + 1 (k even) of a column of fp16: in order, but for MXFP4 with
+// steps 8c + j and 8c + j + 4 side by side, as the codes come apart.
 template <int WT>
-__device__ __forceinline__ void store_e4m3(uint8_t* column, int k, uint32_t v) {
-  uint8_t* block = column + (k & ~31);
-  uint16_t first, second;
-  int at, gap;
+__device__ __forceinline__ void store_pair(uint16_t* column, int k, uint32_t v) {
   if (WT == kFewMxfp4) {
-    at = (k & 24) + ((k & 4) >> 1);
-    gap = 4;
-    first = (uint16_t)__byte_perm(v, 0, 0x4420);
-    second = (uint16_t)__byte_perm(v, 0, 0x4431);
+    uint16_t* to = column + (k & ~7) + 2 * (k & 3) + ((k >> 2) & 1);
+    to[0] = (uint16_t)v;
+    to[2] = (uint16_t)(v >> 16);
   } else {
-    at = 4 * (k & 7) + ((k >> 3) & 3) * 2;
-    gap = 8;
-    first = (uint16_t)v;
-    second = (uint16_t)(v >> 16);
-  }
-  *reinterpret_cast<uint16_t*>(block + at) = first;
-  *reinterpret_cast<uint16_t*>(block + at + gap) = second;
-}
-
-// Two values as e4m3, the first in the low byte, and back as fp16.
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t e4m3_values(uint32_t pair) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)pair));
-  return r;
-}
-
-// Four values to N terms, the columns `ld` bytes apart.
-template <int WT, int N>
-__device__ __forceinline__ void store_terms8(uint8_t* column, int64_t ld, int k, const float (&value)[4], float factor) {
-  float v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool finite = (__float_as_uint(value[i]) & 0x7f800000u) != 0x7f800000u;
-    v[i] = finite ? value[i] * factor : __uint_as_float(0x7fffffffu);
-  }
-#pragma unroll
-  for (int t = 0; t < N; ++t) {
-    const uint32_t q01 = e4m3_pair(v[0], v[1]), q23 = e4m3_pair(v[2], v[3]);
-    store_e4m3<WT>(column + t * ld, k, q01 | (q23 << 16));
-    const uint32_t lo = e4m3_values(q01), hi = e4m3_values(q23);
-    const uint32_t back[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (v[i] - __half2float(__ushort_as_half((uint16_t)back[i]))) * 16.0f;
+    *reinterpret_cast<uint32_t*>(column + k) = v;
   }
 }
 
@@ -315,29 +286,58 @@ __device__ __forceinline__ void stage_bf16(uint32_t tile, uint32_t cols, int pit
 }
 
 // e4m3: [steps][128 columns] codes; a 16-bit unit of ldmatrix is two columns of
-// one step, so a register holds columns 2g and 2g + 1 of two steps of eight, and
-// two registers make one of the MMA's, four steps of a column.
+// one step, so a register holds columns 2g and 2g + 1 of steps 2c and 2c + 1.
+// True where the tile has a code 0x7f, whose sums are to be done again with NANS.
+template <int NT, bool NANS>
+__device__ __forceinline__ bool e4m3_sums(uint32_t tile, uint32_t cols, int pitch, int last, float (&part)[NT][4]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i = lane >> 3, r = lane & 7;
+  uint32_t seen = 0;  // a byte's top bit, which adding 1 flips where the seven others are set
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[j][e] = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int k = 32 * q + 8 * i + r;
+    uint32_t w[4], a[4][2];
+    ldsm_t(w, tile + k * 128 + (((warp & 7) ^ (k & 7)) << 4));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (NANS) {
+        a[e][0] = e4m3_values(__byte_perm(w[e], 0, 0x4420));
+        a[e][1] = e4m3_values(__byte_perm(w[e], 0, 0x4431));
+      } else {
+        e4m3_pairs(w[e], a[e][0], a[e][1]);
+        seen |= (w[e] + 0x01010101u) ^ w[e];
+      }
+    }
+    const uint32_t a0[4] = {a[0][0], a[0][1], a[1][0], a[1][1]}, a1[4] = {a[2][0], a[2][1], a[3][0], a[3][1]};
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      uint32_t b[4];
+      ldsm(b, cols + min(8 * j + r, last) * pitch + (32 * q + 8 * i) * 2);
+      mma_f16(part[j], a0, b[0], b[1]);
+      mma_f16(part[j], a1, b[2], b[3]);
+    }
+  }
+  return (seen & 0x80808080u) != 0;
+}
+
 // f[j]: the block's scale times the columns' factor.
 template <int NT>
 __device__ __forceinline__ void stage_e4m3(uint32_t tile, uint32_t cols, int pitch, int last, const float (&f)[NT],
                                            float (&acc)[NT][4]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = lane >> 3, r = lane & 7, g = lane >> 2, c = lane & 3;
-  float part[2][NT][4] = {};  // two sums: an MMA that adds to the one before it waits for it
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int k = 32 * q + 8 * i + r;
-    uint32_t w[4];
-    ldsm_t(w, tile + k * 128 + (((warp & 7) ^ (k & 7)) << 4));
-    const uint32_t a[4] = {__byte_perm(w[0], w[1], 0x6420), __byte_perm(w[0], w[1], 0x7531),
-                           __byte_perm(w[2], w[3], 0x6420), __byte_perm(w[2], w[3], 0x7531)};
-#pragma unroll
-    for (int j = 0; j < NT; ++j) mma_e4m3(part[q & 1][j], a, lds8(cols + min(8 * j + g, last) * pitch + 32 * q + 8 * c));
+  float part[NT][4];
+  float up = 256.0f;
+  if (__any_sync(0xffffffffu, e4m3_sums<NT, false>(tile, cols, pitch, last, part))) {
+    e4m3_sums<NT, true>(tile, cols, pitch, last, part);
+    up = 1.0f;
   }
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(part[0][j][e] + part[1][j][e], f[j], acc[j][e]);
+    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(part[j][e], f[j] * up, acc[j][e]);
 }
 
 // MXFP4: [128 columns][steps / 2] codes, one half of the steps; lane (g, c) holds
@@ -361,13 +361,17 @@ __device__ __forceinline__ void stage_mxfp4(uint32_t tile, int half, uint32_t co
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int blk = 2 * p + q;
-      uint32_t a[4];
-      mx_e4m3(w[2 * q], a[0], a[2]);
-      mx_e4m3(w[2 * q + 1], a[1], a[3]);
+      uint32_t x[4], y[4];
+      mx_pairs(w[2 * q], x);
+      mx_pairs(w[2 * q + 1], y);
+      const uint32_t a0[4] = {x[0], y[0], x[1], y[1]}, a1[4] = {x[2], y[2], x[3], y[3]};
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
+        uint32_t b[4];
+        lds(b, cols + min(8 * j + g, last) * pitch + (half * 128 + blk * 32 + 8 * c) * 2);
         float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        mma_e4m3(part, a, lds8(cols + min(8 * j + g, last) * pitch + half * 128 + blk * 32 + 8 * c));
+        mma_f16(part, a0, b[0], b[1]);
+        mma_f16(part, a1, b[2], b[3]);
         sum[j][0] = fmaf(part[0], s0[blk], sum[j][0]);
         sum[j][1] = fmaf(part[1], s0[blk], sum[j][1]);
         sum[j][2] = fmaf(part[2], s1[blk], sum[j][2]);
@@ -378,14 +382,12 @@ __device__ __forceinline__ void stage_mxfp4(uint32_t tile, int half, uint32_t co
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(sum[j][e], f[j] * 64.0f, acc[j][e]);
+    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(sum[j][e], f[j] * 16384.0f, acc[j][e]);
 }
 
 // ------------------------------------------------------------ shares and pieces
-// B columns that a row of x and of h takes, and the bytes of a step.
-__host__ __device__ constexpr int x_terms(int weights) { return weights == kFewBf16 ? 1 : 3; }
-__host__ __device__ constexpr int h_terms(int weights) { return weights == kFewBf16 ? 3 : 6; }
-__host__ __device__ constexpr int step_bytes(int weights) { return weights == kFewBf16 ? 2 : 1; }
+// B columns that a row of h takes.
+__host__ __device__ constexpr int terms(int weights) { return weights == kFewBf16 ? 3 : 2; }
 
 // A chunk, or one pass over it: units [step0, step1) of 128 output columns of
 // one matrix, for `rows` rows of `group` B columns each.
@@ -431,16 +433,16 @@ struct Share {
     q.expert = SHARED ? 0 : ls.expert[ei];
     q.first = SHARED ? 0 : ls.start[ei];
     q.rows = SHARED ? p.T : ls.start[ei + 1] - q.first;
-    q.group = DOWN ? h_terms(WT) : x_terms(WT);
+    q.group = DOWN ? terms(WT) : 1;
     q.again = q.rows > kPass;
     q.ld = (int64_t)per_expert * split.parts * kFewCols;
     q.out = buf + q.first * q.ld + ((int64_t)in * split.parts + part) * kFewCols;
     return q;
   }
-  // Rows of a pass: 24 B columns at most (more rows read the weights again, from
-  // L2 mostly: only the shared expert and crowded small layers have them).
-  static constexpr int kPass =
-      DOWN ? kMaxCols / h_terms(WT) : WT == kFewBf16 ? kFewMaxTokens : kMaxCols / x_terms(WT);
+  // Rows of a pass: at most 8 in the down projections (more read the weights
+  // again, from L2 mostly: only the shared expert and crowded small layers have
+  // them).
+  static constexpr int kPass = DOWN ? 8 : kFewMaxTokens;
   template <typename F>
   __device__ __forceinline__ bool passes(Piece q, F f) const {
     const int all = q.rows;
@@ -458,8 +460,8 @@ struct Share {
 // in bytes: a pad keeps the reads of 8 columns off each other's banks.
 template <int WT>
 struct ColumnPlan {
-  static constexpr int kUnitBytes = step_bytes(WT) * few_unit_steps(WT);
-  static constexpr int kPad = WT == kFewBf16 ? 16 : 32;
+  static constexpr int kUnitBytes = 2 * few_unit_steps(WT);
+  static constexpr int kPad = WT == kFewMxfp4 ? 64 : 16;
   int units, pitch;
   __device__ __forceinline__ explicit ColumnPlan(const Piece& q) {
     const int cols = q.rows * q.group;
@@ -468,7 +470,7 @@ struct ColumnPlan {
   }
 };
 // every piece has room for one unit's columns
-static_assert((int)kColBytes / kMaxCols >= 256 + 32, "B columns");
+static_assert((int)kColBytes / kMaxCols >= 2 * 64 + 16 && (int)kColBytes / 16 >= 2 * 256 + 64, "B columns");
 
 // The rings' positions: stages and column buffers handed over so far, and which
 // phase of its `scaled` barrier each stage is in (only routed stages have one).
@@ -482,7 +484,7 @@ struct Ring {
 // each row, the block's scale times it) and half.
 struct StageScales {
   uint32_t words[kFewCols][2];
-  float factor[kMaxCols / 3][2];
+  float factor[8][2];
 };
 
 struct Smem {
@@ -584,22 +586,20 @@ __device__ bool bring_columns(const FewParams& p, const Lists& ls, const Smem& s
       const uint8_t* src = nullptr;
       if (lane < cols) {
         if (DOWN)
-          src = (SHARED ? p.h_s : p.h_r) + ((int64_t)q.first * h_terms(WT) + lane) * share.K * step_bytes(WT);
+          src = (SHARED ? p.h_s : p.h_r) + ((int64_t)q.first * terms(WT) + lane) * share.K * 2;
         else
-          src = (WT == kFewBf16 ? p.x : p.x8) +
-                ((SHARED ? q.first + lane : ls.ent[q.first + lane / x_terms(WT)] / p.k) * x_terms(WT) +
-                 lane % x_terms(WT)) * (int64_t)p.d * step_bytes(WT);
+          src = (WT == kFewBf16 ? p.x : p.x16) + (SHARED ? q.first + lane : ls.ent[q.first + lane] / p.k) * (int64_t)p.d * 2;
       }
       for (int step = q.step0; step < q.step1; ++step) {
         if ((step - q.step0) % plan.units == 0) {
           const int buf = ring.cols & 1;
           if (!wait(&c.col_empty[buf], (ring.cols >> 1) + 1)) return false;
           const int last = min(q.step1, step + plan.units);
-          const uint32_t bytes = step_bytes(WT) * (min(share.K, last * kSteps) - step * kSteps);
+          const uint32_t bytes = 2 * (min(share.K, last * kSteps) - step * kSteps);
           if (lane == 0) ptx::mbar_arrive_expect_tx(&c.col_full[buf], bytes * cols);
           __syncwarp();
           if (lane < cols)
-            bulk_load(ptx::smem_u32(sm.cols) + buf * kColBytes + lane * plan.pitch, src + step * kSteps * step_bytes(WT), bytes,
+            bulk_load(ptx::smem_u32(sm.cols) + buf * kColBytes + lane * plan.pitch, src + step * kSteps * 2, bytes,
                       &c.col_full[buf]);
           ++ring.cols;
         }
@@ -618,7 +618,7 @@ __device__ bool bring_columns(const FewParams& p, const Lists& ls, const Smem& s
 // two columns each, e4m3's by the first warp.
 template <int WT, bool DOWN>
 __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
-  constexpr int kGroup = WT == kFewMxfp4 ? 4 : 8;  // units whose loads go together
+  constexpr int kGroup = 4;  // units whose loads go together
   const int lane = threadIdx.x & 31;
   const int tid = threadIdx.x - kAllThreads + 32 * kRouterWarps;
   const Share<WT, false, DOWN> share(p, ls);
@@ -645,8 +645,8 @@ __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm
       const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
       for (int step0 = q.step0; step0 < q.step1; step0 += kGroup) {
         if constexpr (WT == kFewE4m3) {
-          // lane 4 u + r: unit u of the group, row r of the piece
-          const int step = step0 + (lane >> 2), row = lane & 3;
+          // lane 8 u + r: unit u of the group, row r of the piece
+          const int step = step0 + (lane >> 3), row = lane & 7;
           float f = 0.0f;
           if (step < q.step1) {
             f = __ldg(reinterpret_cast<const float*>(scales) +
@@ -655,7 +655,7 @@ __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm
           }
           for (int u = 0; u < kGroup && step0 + u < q.step1; ++u) {
             if (!wait(ring.n)) return false;
-            if ((lane >> 2) == u && tid < 32) {
+            if ((lane >> 3) == u && tid < 32) {
               float* to = sm.scales[ring.n % kStages].factor[row];
               to[0] = f;
               to[1] = f;
@@ -665,7 +665,7 @@ __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm
         } else {
           uint32_t w[kGroup][2][2];
           float f[kGroup];
-          const int row = (tid >> 1) & 3, half = tid & 1;
+          const int row = (tid >> 1) & 7, half = tid & 1;
 #pragma unroll
           for (int u = 0; u < kGroup; ++u) {
             const int step = step0 + u;
@@ -685,7 +685,7 @@ __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm
               }
             }
             f[u] = 1.0f;
-            if (DOWN && tid < 8 && row < q.rows && step < q.step1 && 2 * step + half < words)
+            if (DOWN && tid < 16 && row < q.rows && step < q.step1 && 2 * step + half < words)
               f[u] = __ldcg(p.h_scale + (int64_t)(q.first + row) * words + 2 * step + half);
           }
 #pragma unroll
@@ -696,7 +696,7 @@ __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm
 #pragma unroll
               for (int i = 0; i < 2; ++i)
                 *reinterpret_cast<uint2*>(to.words[tid + 64 * i]) = make_uint2(w[u][i][0], w[u][i][1]);
-              if (tid < 8) to.factor[row][half] = f[u];
+              if (tid < 16) to.factor[row][half] = f[u];
               hand_over();
             }
           }
@@ -747,7 +747,7 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
           float f[NT];  // of the row that columns 2c and 2c + 1 belong to
 #pragma unroll
           for (int j = 0; j < NT; ++j)
-            f[j] = sc.factor[DOWN ? min((8 * j + 2 * c) / h_terms(WT), kMaxCols / h_terms(WT) - 1) : 0][h];
+            f[j] = sc.factor[DOWN && NT <= 2 ? 4 * j + c : 0][h];
           if constexpr (WT == kFewE4m3) {
             stage_e4m3<NT>(tile, cols, plan.pitch, last, f, acc);
           } else {
@@ -784,13 +784,10 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
   ptx::named_barrier(1 + pair, 64);
   for (int i = team * 32 + lane; i < q.rows * 16; i += 64) {
     const int r = i >> 4, col = i & 15;
-    // from the last term to the first: each is 2^-4 of the one before (bf16's
-    // terms carry their own exponents)
-    constexpr float kNext = WT == kFewBf16 ? 1.0f : 0.0625f;
     float a = 0.0f;
-    for (int t = q.group - 1; t >= 0; --t) {
+    for (int t = 0; t < q.group; ++t) {
       const float* x = red + (r * q.group + t) * kRedPitch + col;
-      a = fmaf(a, kNext, x[0] + x[kMaxCols * kRedPitch]);
+      a += x[0] + x[kMaxCols * kRedPitch];
     }
     q.out[r * q.ld + pair * 16 + col] = a;
   }
@@ -825,10 +822,10 @@ __device__ bool consume(const FewParams& p, const Lists& ls, const Smem& sm, Rin
       const int cols = q.rows * q.group;
       if (cols <= 8)
         consume_piece<WT, 1, DOWN>(p, q, share.K, sm, ring);
-      else if (cols <= 16)
+      else if (cols <= 16 || terms(WT) == 2)
         consume_piece<WT, 2, DOWN>(p, q, share.K, sm, ring);
       else
-        consume_piece<WT, 3, DOWN>(p, q, share.K, sm, ring);
+        consume_piece<WT, terms(WT) == 2 ? 2 : 3, DOWN>(p, q, share.K, sm, ring);
       return true;
     });
   }
@@ -1074,12 +1071,12 @@ __device__ __forceinline__ void terms_of(float v, uint32_t (&t)[3]) {
   t[2] = __float_as_uint(q) >> 16;
 }
 
-// The power of two 2^(7 - e) for a largest magnitude of exponent e, as the factor
+// The power of two 2^(14 - e) for a largest magnitude of exponent e, as the factor
 // and its inverse; both normal numbers.
-__device__ __forceinline__ void e4m3_factor(uint32_t top, float& factor, float& inverse) {
-  const uint32_t field = max(top >> 23, 8u);
-  factor = __uint_as_float((261u - field) << 23);
-  inverse = __uint_as_float((field - 7u) << 23);
+__device__ __forceinline__ void fp16_factor(uint32_t top, float& factor, float& inverse) {
+  const uint32_t field = max(top >> 23, 15u);
+  factor = __uint_as_float((268u - field) << 23);
+  inverse = __uint_as_float((field - 14u) << 23);
 }
 
 // Bits of |v| where v is finite, 0 otherwise.
@@ -1088,17 +1085,25 @@ __device__ __forceinline__ uint32_t finite_bits(float v) {
   return b < 0x7f800000u ? b : 0u;
 }
 
-// x of this CTA's tokens as e4m3 terms, for the routed experts' codes.
+__device__ __forceinline__ uint32_t fp16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float fp16_lo(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)v)); }
+__device__ __forceinline__ float fp16_hi(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)(v >> 16))); }
+
+// x of this CTA's tokens in fp16, for the routed experts' codes.
 template <int WT>
-__device__ void e4m3_tokens(const FewParams& p, uint32_t* red) {
+__device__ void fp16_tokens(const FewParams& p, uint32_t* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int t = gridDim.x - 1 - blockIdx.x; t < p.T; t += gridDim.x) {
-    const uint2* x = reinterpret_cast<const uint2*>(p.x + (int64_t)t * p.d * 2);
+    const uint32_t* x = reinterpret_cast<const uint32_t*>(p.x + (int64_t)t * p.d * 2);
     uint32_t top = 0;
-    for (int i = threadIdx.x; i < p.d / 4; i += kThreads) {
-      const uint2 v = __ldg(x + i);
-      top = max(top, max(max(finite_bits(ptx::bf16_lo(v.x)), finite_bits(ptx::bf16_hi(v.x))),
-                         max(finite_bits(ptx::bf16_lo(v.y)), finite_bits(ptx::bf16_hi(v.y)))));
+    for (int i = threadIdx.x; i < p.d / 2; i += kThreads) {
+      const uint32_t v = __ldg(x + i);
+      top = max(top, max(finite_bits(ptx::bf16_lo(v)), finite_bits(ptx::bf16_hi(v))));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -1108,12 +1113,12 @@ __device__ void e4m3_tokens(const FewParams& p, uint32_t* red) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     float factor, inverse;
-    e4m3_factor(top, factor, inverse);
+    fp16_factor(top, factor, inverse);
     if (threadIdx.x == 0) p.x_scale[t] = inverse;
-    for (int i = threadIdx.x; i < p.d / 4; i += kThreads) {
-      const uint2 v = __ldg(x + i);
-      const float f[4] = {ptx::bf16_lo(v.x), ptx::bf16_hi(v.x), ptx::bf16_lo(v.y), ptx::bf16_hi(v.y)};
-      store_terms8<WT, x_terms(WT)>(p.x8 + (int64_t)t * x_terms(WT) * p.d, p.d, 4 * i, f, factor);
+    uint16_t* to = reinterpret_cast<uint16_t*>(p.x16 + (int64_t)t * p.d * 2);
+    for (int i = threadIdx.x; i < p.d / 2; i += kThreads) {
+      const uint32_t v = __ldg(x + i);
+      store_pair<WT>(to, 2 * i, fp16_pair(ptx::bf16_lo(v) * factor, ptx::bf16_hi(v) * factor));
     }
     consumer_sync();
   }
@@ -1128,6 +1133,21 @@ __device__ __forceinline__ void store_terms(uint8_t* to, int K, int k, const flo
   for (int q = 0; q < 3; ++q)
     *reinterpret_cast<uint2*>(to + ((int64_t)q * K + k) * 2) =
         make_uint2(t[0][q] | (t[1][q] << 16), t[2][q] | (t[3][q] << 16));
+}
+
+// The same as two fp16 terms [2][K]; the second of an infinity or NaN is none.
+template <int WT>
+__device__ __forceinline__ void store_terms16(uint8_t* to, int K, int k, const float (&h)[4], float factor) {
+  uint16_t* column = reinterpret_cast<uint16_t*>(to);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float a = h[2 * i] * factor, b = h[2 * i + 1] * factor;
+    const uint32_t first = fp16_pair(a, b);
+    const float ra = finite_bits(a) == (__float_as_uint(a) & 0x7fffffffu) ? a - fp16_lo(first) : 0.0f;
+    const float rb = finite_bits(b) == (__float_as_uint(b) & 0x7fffffffu) ? b - fp16_hi(first) : 0.0f;
+    store_pair<WT>(column, k + 2 * i, first);
+    store_pair<WT>(column + K, k + 2 * i, fp16_pair(ra, rb));
+  }
 }
 
 // h of every row, four columns a lane and 128 a warp.
@@ -1160,9 +1180,9 @@ __device__ void activations(const FewParams& p, const Lists& ls) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       float factor, inverse;
-      e4m3_factor(top, factor, inverse);
+      fp16_factor(top, factor, inverse);
       if (lane == 0) p.h_scale[(int64_t)row * rb + block] = inverse;
-      store_terms8<WT, h_terms(WT)>(p.h_r + (int64_t)row * h_terms(WT) * p.I, p.I, k, h, factor);
+      store_terms16<WT>(p.h_r + (int64_t)row * 2 * p.I * 2, p.I, k, h, factor);
     }
   }
 }
@@ -1275,7 +1295,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     bool ok = true;
     auto wait = [&](uint64_t* bar) {
       if (warp_wait(bar, 0, abort) && __all_sync(0xffffffffu, *abort == 0)) {
-        ptx::fence_proxy_async_all();  // x's terms and h were written by ordinary stores
+        ptx::fence_proxy_async_all();  // x in fp16 and h were written by ordinary stores
         return true;
       }
       raise_status(p.status, abort, kStatusTimeout);
@@ -1311,7 +1331,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     Ring ring;
     logits_share(p, reinterpret_cast<double*>(sm.red));
     if (RT != kFewBf16) {
-      e4m3_tokens<RT>(p, reinterpret_cast<uint32_t*>(sm.red));
+      fp16_tokens<RT>(p, reinterpret_cast<uint32_t*>(sm.red));
       ptx::fence_proxy_async_all();  // bulk copies will read them
     }
     grid_arrive(p.bar + 0);

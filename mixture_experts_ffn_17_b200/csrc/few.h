@@ -57,10 +57,10 @@ struct FewParams {
   FewSplit split_up_r, split_up_s, split_dn_r, split_dn_s;
   float* logits;       // [T, E]
   float *up_r, *up_s, *dn_r, *dn_s;  // the chunks' sums, [row][segment][part][kFewCols]
-  uint8_t* h_r;        // [T * k][terms][I]: three bf16 terms of the routed rows' activations, or six e4m3 ones
+  uint8_t* h_r;        // [T * k][terms][I] terms of the routed rows' activations: three bf16 or two fp16
   uint8_t* h_s;        // [T][3][S] bf16
-  // e4m3 and MXFP4 weights: x's e4m3 terms, and the powers of two that undo its and h's scaling
-  uint8_t* x8;         // [T][3][d]
+  // e4m3 and MXFP4 weights: x in fp16, and the powers of two that undo its and h's scaling
+  uint8_t* x16;        // [T, d]
   float* x_scale;      // [T]
   float* h_scale;      // [T * k][I / 128]
 };

@@ -36,7 +36,7 @@ int few_weights(const moe_shape& s) {
 
 struct FewLayout {
   FewSplit split_up_r, split_up_s, split_dn_r, split_dn_s;
-  size_t logits, up_r, up_s, dn_r, dn_s, h_r, h_s, x8, x_scale, h_scale, total;
+  size_t logits, up_r, up_s, dn_r, dn_s, h_r, h_s, x16, x_scale, h_scale, total;
 };
 
 FewLayout few_layout(const moe_shape& s) {
@@ -62,7 +62,7 @@ FewLayout few_layout(const moe_shape& s) {
   L.dn_s = take(s.shared_inter > 0 ? sums(T * bd, L.split_dn_s) : 0);
   L.h_r = take((size_t)rows * 3 * s.inter * 2);
   L.h_s = take((size_t)T * 3 * s.shared_inter * 2);
-  L.x8 = take((size_t)T * 3 * s.d);
+  L.x16 = take((size_t)T * s.d * 2);
   L.x_scale = take((size_t)T * 4);
   L.h_scale = take((size_t)rows * bi * 4);
   L.total = off;
@@ -227,7 +227,7 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.dn_s = at<float>(ws, L.dn_s);
   p.h_r = at<uint8_t>(ws, L.h_r);
   p.h_s = at<uint8_t>(ws, L.h_s);
-  p.x8 = at<uint8_t>(ws, L.x8);
+  p.x16 = at<uint8_t>(ws, L.x16);
   p.x_scale = at<float>(ws, L.x_scale);
   p.h_scale = at<float>(ws, L.h_scale);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
