@@ -169,8 +169,21 @@ __device__ __forceinline__ float4 sum_parts(const float* at, int parts) {
 }
 
 // ------------------------------------------------------------ tiles and columns
+// The loads and MMAs of a stage are left to the compiler to arrange; these two keep
+// them between the wait for the stage and its release.
+__device__ __forceinline__ void after_wait(uint32_t& tile, uint32_t& cols) {
+  asm volatile("" : "+r"(tile), "+r"(cols)::"memory");
+}
+
+template <int NT>
+__device__ __forceinline__ void before_release(float (&acc)[NT][4]) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    asm volatile("" : "+f"(acc[j][0]), "+f"(acc[j][1]), "+f"(acc[j][2]), "+f"(acc[j][3])::"memory");
+}
+
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -178,7 +191,7 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -186,17 +199,15 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 }
 
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+  asm("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 
 __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+  asm("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 
 // Four e4m3 codes to two fp16 pairs, bytes (0, 2) and (1, 3), times 2^-8.  The
@@ -222,10 +233,9 @@ __device__ __forceinline__ void mx_pairs(uint32_t w, uint32_t (&f)[4]) {
 }
 
 __device__ __forceinline__ void lds(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -736,11 +746,13 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
     const int slot = ring.n % kStages;
     if ((ring.n & 1) == team) {
       arrived(&ct.full[slot], (ring.n / kStages) & 1);
-      const uint32_t tile = ptx::smem_u32(sm.stages) + slot * kTileBytes;
+      uint32_t tile = ptx::smem_u32(sm.stages) + slot * kTileBytes;
       if constexpr (WT == kFewBf16) {
+        after_wait(tile, cols);
         stage_bf16<NT>(tile, cols, plan.pitch, last, acc);
       } else {
         arrived(&ct.scaled[slot], (ring.scaled >> slot) & 1);
+        after_wait(tile, cols);
         const StageScales& sc = sm.scales[slot];
         const int halves = WT == kFewMxfp4 && 2 * step + 1 < K / 128 ? 2 : 1;  // MXFP4's last unit may be half of one
         for (int h = 0; h < halves; ++h) {
@@ -756,6 +768,7 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
           }
         }
       }
+      before_release<NT>(acc);
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&ct.empty[slot]);
     }
