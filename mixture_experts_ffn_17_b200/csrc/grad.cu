@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(kThreads)
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   const double ratio = (double)max_norm / (norm + 1e-6);
   const float f = ratio >= 1.0 ? 1.0f : (float)ratio;  // a NaN norm gives a NaN factor
+  if (f == 1.0f && b.in_place) return;
   const uint32_t total = b.first[b.n];
   for (uint32_t i = blockIdx.x; i < total; i += gridDim.x) {
     const uint32_t c = total - 1 - i;
@@ -231,14 +232,11 @@ __global__ void __launch_bounds__(kThreads)
 }  // namespace
 
 int64_t grad_chunks(int64_t count, bool bf16) {
-  // one chunk more than the elements need where the head takes some of the first
   const int64_t ch = bf16 ? Elem<true>::kChunk : Elem<false>::kChunk;
   return count > 0 ? (count + ch - 1) / ch : 0;
 }
 
-int grad_grid(uint32_t chunks, int sms) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(chunks, (int64_t)sms * kGradCtasPerSm));
-}
+int grad_grid(uint32_t chunks, int ctas) { return (int)std::max<int64_t>(1, std::min<int64_t>(chunks, ctas)); }
 
 cudaError_t launch_grad_squares(const GradBatch& b, double* part, int grid, cudaStream_t stream) {
   return launch_chained(grad_square_kernel, dim3(grid), dim3(kThreads), 0, stream, b, part);

@@ -42,12 +42,6 @@ __device__ __forceinline__ float inverse_scale(uint32_t s) {
   return s == 255u ? 0.0f : __uint_as_float((254u - s) << 23);
 }
 
-// 2^(s - 127); NaN for s = 255.
-__device__ __forceinline__ float scale_value(uint32_t s) {
-  if (s == 255u) return __uint_as_float(0x7fffffffu);
-  return s == 0 ? __uint_as_float(1u << 22) : __uint_as_float(s << 23);
-}
-
 // Codes of eight values, the first in the lowest four bits.
 __device__ __forceinline__ uint32_t codes_of(const float (&v)[8], float inv, bool bad) {
   uint32_t c = 0;
@@ -99,38 +93,60 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) 
   }
 }
 
-// One thread quantises 8 values, four neighbouring threads a block: their
-// largest magnitude is joined by two shuffles.  Loads are 16 bytes wide
-// (VEC: base and row stride allow it) and a warp's codes one 128-byte line.
-template <bool BF16, bool VEC, bool GATED>
+// silu(g) * u: the exponential is good to one step of fp32, the reciprocal and the
+// products add four halves.
+__device__ __forceinline__ float gated(float g, float u) { return g * u * __fdividef(1.0f, 1.0f + expf(-g)); }
+
+// Groups of 8 values in flight per thread: 2048 threads of an SM with 16 bytes each
+// do not cover HBM's latency (58% of its rate, with 64 bytes 84%).
+template <bool BF16, bool GATED>
+constexpr int kGroups = (BF16 ? 4 : 2) / (GATED ? 2 : 1);
+
+// One thread quantises 8 values of a group, four neighbouring threads a block: their
+// largest magnitude is joined by two shuffles.  Loads are 16 bytes wide (VEC: base
+// and row stride allow it) and a warp's codes one 128-byte line.  DENSE: rows follow
+// one another, so that a group's place needs no division.
+template <bool BF16, bool VEC, bool GATED, bool DENSE>
 __global__ void __launch_bounds__(256)
     mx_quantise_kernel(const void* __restrict__ src, const void* __restrict__ up, int64_t groups, int per_row,
                        int64_t ld, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  constexpr int U = kGroups<BF16, GATED>;
   grid_dependency_wait();
   // groups is a multiple of 4, so the four threads of a block leave together
-  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t g0 = (int64_t)blockIdx.x * blockDim.x; g0 < groups; g0 += stride) {
-    const int64_t g = g0 + threadIdx.x;
-    const bool in = g < groups;
-    float v[8] = {};
-    if (in) {
-      const int64_t row = groups <= 0xffffffffll ? (int64_t)((uint32_t)g / (uint32_t)per_row) : g / per_row;
-      const int64_t at = row * ld + (g - row * per_row) * 8;
-      load8<BF16, VEC>(src, at, v);
-      if (GATED) {
-        float u[8];
-        load8<BF16, VEC>(up, at, u);
+  const int64_t stride = (int64_t)gridDim.x * blockDim.x * U;
+  for (int64_t g0 = (int64_t)blockIdx.x * blockDim.x * U; g0 < groups; g0 += stride) {
+    float v[U][8], w[GATED ? U : 1][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.0f + expf(-v[i])) * u[i];
+    for (int u = 0; u < U; ++u) {
+      const int64_t g = g0 + u * 256 + threadIdx.x;
+      if (g < groups) {
+        int64_t at = g * 8;
+        if (!DENSE) {
+          const int64_t row = groups <= 0xffffffffll ? (int64_t)((uint32_t)g / (uint32_t)per_row) : g / per_row;
+          at = row * ld + (g - row * per_row) * 8;
+        }
+        load8<BF16, VEC>(src, at, v[u]);
+        if (GATED) load8<BF16, VEC>(up, at, w[u % (GATED ? U : 1)]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = w[u % (GATED ? U : 1)][i] = 0.0f;
       }
     }
-    uint32_t top = top_bits(v);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const uint32_t s = scale_byte(top);
-    if (in) {
-      codes[g] = codes_of(v, inverse_scale(s), s == 255u);
-      if ((threadIdx.x & 3) == 0) scales[g >> 2] = (uint8_t)s;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t g = g0 + u * 256 + threadIdx.x;
+      if (GATED) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = gated(v[u][i], w[u % (GATED ? U : 1)][i]);
+      }
+      uint32_t top = top_bits(v[u]);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t s = scale_byte(top);
+      if (g < groups) {
+        codes[g] = codes_of(v[u], inverse_scale(s), s == 255u);
+        if ((threadIdx.x & 3) == 0) scales[g >> 2] = (uint8_t)s;
+      }
     }
   }
 }
@@ -157,37 +173,44 @@ __global__ void __launch_bounds__(256)
   const int k0 = k_base + warp * kMxBlock;
   const int n0 = n_base + 2 * lane;
   if (k0 < K) {
-    float a[kMxBlock], b[kMxBlock];
+    // bf16 values stay packed, two columns to a register: half the registers, so
+    // twice the threads, whose loads are in flight
+    uint32_t raw[BF16 ? kMxBlock : 1];
+    float fa[BF16 ? 1 : kMxBlock], fb[BF16 ? 1 : kMxBlock];
     const int64_t at = (e * K + k0) * (int64_t)N + n0;
 #pragma unroll
     for (int i = 0; i < kMxBlock; ++i) {
       const int64_t p = at + (int64_t)i * N;
-      if (VEC) {  // N even and the base aligned: n0 < N implies n0 + 1 < N
-        if (BF16) {
-          const uint32_t r = n0 < N ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(W) + p)) : 0u;
-          a[i] = ptx::bf16_lo(r);
-          b[i] = ptx::bf16_hi(r);
-        } else {
-          const float2 r = n0 < N ? __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(W) + p))
-                                  : make_float2(0.0f, 0.0f);
-          a[i] = r.x;
-          b[i] = r.y;
-        }
-      } else if (BF16) {
+      if (BF16) {
         const uint16_t* q = static_cast<const uint16_t*>(W) + p;
-        a[i] = n0 < N ? __uint_as_float((uint32_t)__ldg(q) << 16) : 0.0f;
-        b[i] = n0 + 1 < N ? __uint_as_float((uint32_t)__ldg(q + 1) << 16) : 0.0f;
+        uint32_t r = 0;
+        if (VEC) {  // N even and the base aligned: n0 < N implies n0 + 1 < N
+          if (n0 < N) r = __ldg(reinterpret_cast<const uint32_t*>(q));
+        } else {
+          if (n0 < N) r = __ldg(q);
+          if (n0 + 1 < N) r |= (uint32_t)__ldg(q + 1) << 16;
+        }
+        raw[i % (BF16 ? kMxBlock : 1)] = r;
       } else {
         const float* q = static_cast<const float*>(W) + p;
-        a[i] = n0 < N ? __ldg(q) : 0.0f;
-        b[i] = n0 + 1 < N ? __ldg(q + 1) : 0.0f;
+        float2 r = make_float2(0.0f, 0.0f);
+        if (VEC) {
+          if (n0 < N) r = __ldg(reinterpret_cast<const float2*>(q));
+        } else {
+          if (n0 < N) r.x = __ldg(q);
+          if (n0 + 1 < N) r.y = __ldg(q + 1);
+        }
+        fa[i % (BF16 ? 1 : kMxBlock)] = r.x;
+        fb[i % (BF16 ? 1 : kMxBlock)] = r.y;
       }
     }
+    auto left = [&](int i) { return BF16 ? ptx::bf16_lo(raw[i % (BF16 ? kMxBlock : 1)]) : fa[i % (BF16 ? 1 : kMxBlock)]; };
+    auto right = [&](int i) { return BF16 ? ptx::bf16_hi(raw[i % (BF16 ? kMxBlock : 1)]) : fb[i % (BF16 ? 1 : kMxBlock)]; };
     uint32_t ta = 0, tb = 0;
 #pragma unroll
     for (int i = 0; i < kMxBlock; ++i) {
-      ta = max(ta, __float_as_uint(a[i]) & 0x7fffffffu);
-      tb = max(tb, __float_as_uint(b[i]) & 0x7fffffffu);
+      ta = max(ta, __float_as_uint(left(i)) & 0x7fffffffu);
+      tb = max(tb, __float_as_uint(right(i)) & 0x7fffffffu);
     }
     const uint32_t sa = scale_byte(ta), sb = scale_byte(tb);
     const float ia = inverse_scale(sa), ib = inverse_scale(sb);
@@ -197,8 +220,8 @@ __global__ void __launch_bounds__(256)
       float v[8], w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[i] = a[8 * q + i];
-        w[i] = b[8 * q + i];
+        v[i] = left(8 * q + i);
+        w[i] = right(8 * q + i);
       }
       ca[q] = codes_of(v, ia, sa == 255u);
       cb[q] = codes_of(w, ib, sb == 255u);
@@ -222,47 +245,89 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// One thread reads 8 codes: 16 or 32 consecutive bytes of output.
+// One thread reads 8 codes, 16 or 32 consecutive bytes of output, of each of
+// kReads groups.  The codes come apart in pairs j and j + 4 whose exponent and
+// mantissa bits, moved to bf16's, read 2^-126 times their value; two exact
+// multiplications make up for that and apply the scale (bf16 holds every value
+// and every scale), and byte permutes put neighbours together.
+constexpr int kReads = 8;
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(256)
     mx_dequantise_kernel(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t groups,
                          void* __restrict__ dst) {
   grid_dependency_wait();
-  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; g < groups; g += stride) {
-    const uint32_t c = __ldg(codes + g);
-    const float s = scale_value(__ldg(scales + (g >> 2)));
-    float v[8];
+  const int64_t stride = (int64_t)gridDim.x * blockDim.x * kReads;
+  for (int64_t b0 = (int64_t)blockIdx.x * blockDim.x * kReads; b0 < groups; b0 += stride) {
+    const int64_t g0 = b0 + threadIdx.x;
+    uint32_t c[kReads], s[kReads];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // magnitude of the code's low three bits: e = 0: m / 2, else 2^(e - 1) (1 + m / 2)
-      const uint32_t q = (c >> (4 * i)) & 15u, e = (q >> 1) & 3u, m = q & 1u;
-      const uint32_t bits = e ? ((126u + e) << 23) | (m << 22) : (m ? 0x3f000000u : 0u);
-      v[i] = __uint_as_float(bits | ((q & 8u) << 28)) * s;
+    for (int u = 0; u < kReads; ++u) {
+      const int64_t g = g0 + u * 256;
+      if (g < groups) {
+        c[u] = __ldg(codes + g);
+        s[u] = __ldg(scales + (g >> 2));
+      }
     }
-    if (BF16) {
-      static_cast<uint4*>(dst)[g] = make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]),
-                                               ptx::pack_bf16x2(v[4], v[5]), ptx::pack_bf16x2(v[6], v[7]));
-    } else {
-      static_cast<float4*>(dst)[2 * g] = make_float4(v[0], v[1], v[2], v[3]);
-      static_cast<float4*>(dst)[2 * g + 1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int u = 0; u < kReads; ++u) {
+      const int64_t g = g0 + u * 256;
+      const uint32_t lanes = __ballot_sync(0xffffffffu, g < groups);
+      if (g >= groups) continue;
+      const uint32_t w = c[u];
+      uint32_t p[4] = {((w << 12) & 0x80008000u) | ((w << 6) & 0x01c001c0u),
+                       ((w << 8) & 0x80008000u) | ((w << 2) & 0x01c001c0u),
+                       ((w << 4) & 0x80008000u) | ((w >> 2) & 0x01c001c0u), (w & 0x80008000u) | ((w >> 6) & 0x01c001c0u)};
+      // 2^(s - 127) as bf16, 2^-127 as its subnormal; 255 is NaN
+      const uint32_t f = s[u] == 255u ? 0x7fffu : s[u] == 0 ? 0x0040u : s[u] << 7;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = mul_bf16x2(mul_bf16x2(p[i], 0x7e807e80u), f * 0x00010001u);
+      const uint32_t o[4] = {__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                             __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632)};
+      if (BF16) {
+        static_cast<uint4*>(dst)[g] = make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+        // two neighbouring threads write one's 32 bytes and then the other's, so
+        // that each store fills whole sectors
+        const bool odd = threadIdx.x & 1;
+        const uint32_t give0 = odd ? o[0] : o[2], give1 = odd ? o[1] : o[3];
+        const uint32_t got0 = __shfl_xor_sync(lanes, give0, 1), got1 = __shfl_xor_sync(lanes, give1, 1);
+        float4* to = static_cast<float4*>(dst) + 2 * (g & ~(int64_t)1) + (odd ? 1 : 0);
+        const uint32_t a0 = odd ? got0 : o[0], a1 = odd ? got1 : o[1], b0 = odd ? o[2] : got0, b1 = odd ? o[3] : got1;
+        to[0] = make_float4(ptx::bf16_lo(a0), ptx::bf16_hi(a0), ptx::bf16_lo(a1), ptx::bf16_hi(a1));
+        to[2] = make_float4(ptx::bf16_lo(b0), ptx::bf16_hi(b0), ptx::bf16_lo(b1), ptx::bf16_hi(b1));
+      }
     }
   }
 }
 
+// CTAs for `items` threads' work.
 int grid_for(int64_t items, int sms) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>((items + 255) / 256, (int64_t)sms * 32));
+  return (int)std::max<int64_t>(1, std::min<int64_t>((items + 255) / 256, (int64_t)sms * 16));
+}
+
+template <bool BF16, bool VEC, bool GATED>
+cudaError_t launch_quantise(const void* src, const void* up, int64_t groups, int per_row, int64_t ld, uint8_t* codes,
+                            uint8_t* scales, int sms, cudaStream_t stream) {
+  constexpr int U = kGroups<BF16, GATED>;
+  const dim3 grid(grid_for((groups + U - 1) / U, sms));
+  uint32_t* c = reinterpret_cast<uint32_t*>(codes);
+  auto kernel = ld == (int64_t)per_row * 8 ? mx_quantise_kernel<BF16, VEC, GATED, true>
+                                           : mx_quantise_kernel<BF16, VEC, GATED, false>;
+  return launch_chained(kernel, grid, dim3(256), 0, stream, src, up, groups, per_row, ld, c, scales);
 }
 
 template <bool BF16, bool VEC>
 cudaError_t launch_quantise(const void* src, const void* up, int64_t groups, int per_row, int64_t ld, uint8_t* codes,
                             uint8_t* scales, int sms, cudaStream_t stream) {
-  const dim3 grid(grid_for(groups, sms));
-  uint32_t* c = reinterpret_cast<uint32_t*>(codes);
-  return up ? launch_chained(mx_quantise_kernel<BF16, VEC, true>, grid, dim3(256), 0, stream, src, up, groups, per_row,
-                             ld, c, scales)
-            : launch_chained(mx_quantise_kernel<BF16, VEC, false>, grid, dim3(256), 0, stream, src, up, groups,
-                             per_row, ld, c, scales);
+  return up ? launch_quantise<BF16, VEC, true>(src, up, groups, per_row, ld, codes, scales, sms, stream)
+            : launch_quantise<BF16, VEC, false>(src, up, groups, per_row, ld, codes, scales, sms, stream);
 }
 
 }  // namespace
@@ -293,8 +358,7 @@ cudaError_t launch_mx_dequantise(const uint8_t* codes, const uint8_t* scales, in
                                  bool bf16, int sms, cudaStream_t stream) {
   const int64_t groups = rows * (cols / 8);
   const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
-  return launch_chained(bf16 ? mx_dequantise_kernel<true> : mx_dequantise_kernel<false>, dim3(grid_for(groups, sms)),
-                        dim3(256), 0, stream, c, scales, groups, dst);
+  return launch_chained(bf16 ? mx_dequantise_kernel<true> : mx_dequantise_kernel<false>, dim3(grid_for((groups + kReads - 1) / kReads, sms)), dim3(256), 0, stream, c, scales, groups, dst);
 }
 
 }  // namespace moe

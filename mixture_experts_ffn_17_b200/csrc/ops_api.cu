@@ -130,15 +130,17 @@ moe_status check_tensors(const moe_tensor* t, int n, bool clip) {
 
 int grad_batches(int n) { return std::max(1, (n + kGradBatch - 1) / kGradBatch); }
 
-size_t grad_ws_bytes(int n) { return (size_t)grad_batches(n) * kGradMaxSms * kGradCtasPerSm * sizeof(double); }
+size_t grad_ws_bytes(int n) { return (size_t)grad_batches(n) * kGradMaxSms * kGradNormCtas * sizeof(double); }
 
 bool fill_batch(GradBatch& b, const moe_tensor* t, int n, int first) {
   b.n = std::min(kGradBatch, n - first);
+  b.in_place = true;
   int64_t chunks = 0;
   for (int i = 0; i < b.n; ++i) {
     const moe_tensor& x = t[first + i];
     b.src[i] = x.data;
     b.dst[i] = x.out ? x.out : x.data;
+    b.in_place = b.in_place && b.dst[i] == x.data;
     b.count[i] = x.count;
     b.bf16[i] = x.dtype == MOE_BF16;
     b.first[i] = (uint32_t)chunks;
@@ -155,7 +157,7 @@ moe_status grad_squares(const moe_tensor* t, int n, double* part, int sms, int* 
   for (int b = 0; b < grad_batches(n); ++b) {
     GradBatch batch;
     if (!fill_batch(batch, t, n, b * kGradBatch)) return MOE_ERR_UNSUPPORTED;
-    const int grid = grad_grid(batch.first[batch.n], sms);
+    const int grid = grad_grid(batch.first[batch.n], sms * kGradNormCtas);
     MOE_CUDA(launch_grad_squares(batch, part + *parts, grid, st));
     *parts += grid;
   }
@@ -364,7 +366,7 @@ moe_status moe_grad_clip(const moe_tensor* tensors, int n, float max_norm, float
     GradBatch batch;
     fill_batch(batch, tensors, n, b * kGradBatch);
     MOE_CUDA(launch_grad_scale(batch, part, parts, max_norm, b == 0 ? norm_out : nullptr,
-                               grad_grid(batch.first[batch.n], sms), st));
+                               grad_grid(batch.first[batch.n], sms * kGradScaleCtas), st));
   }
   return MOE_OK;
 }
