@@ -11,22 +11,18 @@
 //   consumers (16 warps)  logits of a share of the experts, then the products
 //                         and the two joins, with grid barriers between them;
 //   producer (1 warp)     fills a ring of stages with weight tiles by TMA, ahead
-//                         of the consumers and across the ends of pieces and
+//                         of the consumers and across the ends of chunks and
 //                         phases: the shared expert's up projections need no
 //                         routing and stream while it is found, and the first
 //                         tiles of the down projections are in the ring before
 //                         the barriers that the activations wait for;
 //   columns (1 warp)      follows the tiles and brings the activations that go with
-//                         them, several stages' at a time (bulk copies; copies of
-//                         single stages, 128 bytes each, cost more than the
-//                         weights: 710 instead of 455 us at T = 8 with 28 experts
-//                         of 7168 x 2048 in bf16);
+//                         them (for bf16 weights several stages' at a time, by bulk
+//                         copies: single stages' copies of 128 bytes cost more than
+//                         the weights, 710 instead of 455 us at T = 8 with 28
+//                         experts of 7168 x 2048);
 //   router (2 warps)      waits for all logits, finds the top-k (in every CTA)
-//                         and the list of chosen experts and their rows; then
-//                         brings the block scales of coded weights, and h's
-//                         factors, beside the tiles (a consumer's own load one
-//                         stage ahead comes too late: 0.6 us a stage of e4m3
-//                         where HBM needs 0.37).
+//                         and the list of chosen experts and their rows.
 //
 // Split of the work.  A segment is 128 output columns of one matrix of one
 // expert, a unit the part of its contraction that one stage holds (16 KB of
@@ -37,23 +33,24 @@
 // sums go to a place of its own and who needs a segment adds its chunks in order:
 // no floating-point atomics, and equal inputs give equal bits.
 //
-// Arithmetic: mma.sync m16n8k16 with the weights as the A operand (16 output
-// columns by 16 steps, ldmatrix from the stage) and the activations as B's
-// columns, 8 at a time.  (tcgen05 would pad the columns to 16 and could not take
-// these codes unconverted; the tensor pipe is idle either way.)  Consumer warp w
-// takes columns 16 (w % 8) of every second tile (w / 8): a tile's chain of waits,
-// loads and MMAs is longer than the time HBM needs for one.
-//   bf16 weights: x is bf16 as it comes; h is fp32 and goes in as three bf16
+// Arithmetic.
+//   bf16 weights: mma.sync m16n8k16 with the weights as the A operand (16 output
+//   columns by 16 steps, ldmatrix from the stage) and the activations as B's
+//   columns, 8 at a time.  Consumer warp w takes columns 16 (w % 8) of every second
+//   tile (w / 8): a tile's chain of waits, loads and MMAs is longer than the time
+//   HBM needs for one.  x is bf16 as it comes; h is fp32 and goes in as three bf16
 //   terms (8 bits each: 24 in all).
-//   e4m3 and MXFP4 codes become fp16, which holds them exactly, by moving their
-//   bits: exponent and mantissa read 2^-8 and 2^-14 times the code's value there,
-//   made up in the sums' factors.  (The conversion instructions run at a sixteenth
-//   of the rate; e4m3 MMAs are made of conversions and fp16 ones on this GPU, 2280
-//   instructions a stage.)  x and h are fp16 too, times a power of two that puts
-//   the largest of a token (of 128 values of h) between 2^14 and 2^15: a bf16 x
-//   fits exactly down to 2^-28 of the largest and to 2^-39 of it below; h goes in
-//   as two terms (22 bits).
-// Block scales multiply fp32 sums.
+//   e4m3 and MXFP4 weights: tcgen05.mma takes the codes as they are, M = 128
+//   output columns, kind::f8f6f4 and kind::mxf4 (with its block scales).  It wants
+//   activations of the same kind, so these go in as sums of rounded terms, each
+//   term one more B column that rounds what the ones before left: x in three e4m3
+//   terms and h in six (4 bits each, after a power of two has put the largest of
+//   128 values between 2^7 and 2^8), or both in twelve MXFP4 terms (2 bits each,
+//   every block of 32 with a scale of its own): 24 bits of a block's largest value
+//   in h, and for e4m3 2^-25 of it in x.  The columns cost nothing beside the
+//   weights, and no code is converted: mma.sync needs fp16 operands made of the
+//   codes, which bound the kernel at 2.6 (MXFP4) and 3.9 TB/s (e4m3).
+//   An infinity has no code and goes in as NaN.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_fp16.h>
@@ -73,12 +70,34 @@ constexpr int kMaxCols = 8 * kMaxNT;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxRows = kFewMaxTokens * 32;  // T * k
 constexpr uint32_t kTileBytes = 16384;
+constexpr int kMaxStages = 8;
 
-constexpr int kStages = 8;
-constexpr uint32_t kColBytes = 16384;  // of a buffer of B columns; there are two
+// The ring of a call with these routed weights: beside a tile of codes a stage
+// holds up to 64 rows of 128 bytes of the activations' terms.
+template <int RT>
+struct Cfg {
+  static constexpr bool kCoded = RT != kFewBf16;
+  static constexpr int kStages = kCoded ? 6 : kMaxStages;
+  static constexpr uint32_t kStageBytes = kTileBytes + (kCoded ? 8192 : 0);
+  static constexpr uint32_t kColBytes = kCoded ? 8192 : 16384;  // of a buffer of B columns; there are two
+};
+
+// Terms of the activations for coded weights: rows that x and h take in the arrays
+// (whole swizzle atoms), and terms that are in use.
+constexpr int kTermRows8 = few_term_rows(kFewE4m3), kTermRows4 = few_term_rows(kFewMxfp4);
+constexpr int kXTerms8 = 3, kHTerms8 = 6, kTerms4 = 12;
 
 constexpr int kRedPitch = 17;  // floats of one B column of a warp pair's 16 output columns
 constexpr int kRedFloats = 2 * kMaxCols * kRedPitch;  // of a pair of warps
+
+// TMEM of coded calls: accumulators (MXFP4: one for a pass, two in turn; e4m3: one
+// for a unit, whose sums get their scales in registers, four in turn), then MXFP4's
+// scales, 8 columns of the weights' and 8 of the terms' for each stage.
+constexpr int kAccCols = 64;
+template <int RT>
+constexpr int kAccs = RT == kFewE4m3 ? 4 : 2;
+constexpr int kSfCols = 16;
+constexpr int kTmemCols = 256;
 
 struct Lists {  // what the routing leaves in shared memory
   int32_t idx[kMaxRows];      // [T][k]
@@ -93,19 +112,20 @@ struct Lists {  // what the routing leaves in shared memory
 };
 
 struct Control {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t col_full[2], col_empty[2];
   // a stage's chunk is known, its tile on the way: two turns of the ring, since
   // who has no part in a stage may still be looking at it when the stage's place
   // is filled again, but not when the place after it is
-  uint64_t issued[2 * kStages];
-  uint64_t scaled[kStages];   // its scales are there
-  uint64_t started;           // `first` is there
-  int first;                  // first stage of the routed experts
+  uint64_t issued[2 * kMaxStages];
+  uint64_t scaled[kMaxStages];  // MXFP4: a stage's scales are in TMEM
+  uint64_t acc_full[4], acc_empty[4];
   uint64_t ready;   // h is there, in all CTAs
-  int chunk[2 * kStages];  // which chunk a stage belongs to; -1: the share is done
   uint64_t routed;  // the lists are there
-  uint32_t abort, never;
+  int chunk[2 * kMaxStages];  // which chunk a stage belongs to; -1: the share is done
+  int acc_chunk[4], acc_pass[4], acc_step[4];  // what an accumulator holds
+  int position;  // stages handed over when a coded share ended
+  uint32_t tmem, abort, never;
 };
 
 __device__ __forceinline__ void consumer_sync() { ptx::named_barrier(9, kThreads); }
@@ -190,14 +210,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
   asm("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -210,64 +222,15 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr));
 }
 
-// Four e4m3 codes to two fp16 pairs, bytes (0, 2) and (1, 3), times 2^-8.  The
-// code 0x7f, NaN, is not looked at (it reads 480).
-__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t& even, uint32_t& odd) {
-  even = ((w << 8) & 0x80008000u) | ((w << 7) & 0x3f803f80u);
-  odd = (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
-}
-
-// The same times 1 by the conversion instruction, NaN included.
-__device__ __forceinline__ uint32_t e4m3_values(uint32_t two_codes) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two_codes));
-  return r;
-}
-
-// Eight MXFP4 codes to four fp16 pairs, codes j and j + 4, times 2^-14.
-__device__ __forceinline__ void mx_pairs(uint32_t w, uint32_t (&f)[4]) {
-  f[0] = ((w << 12) & 0x80008000u) | ((w << 9) & 0x0e000e00u);
-  f[1] = ((w << 8) & 0x80008000u) | ((w << 5) & 0x0e000e00u);
-  f[2] = ((w << 4) & 0x80008000u) | ((w << 1) & 0x0e000e00u);
-  f[3] = (w & 0x80008000u) | ((w >> 3) & 0x0e000e00u);
-}
-
-__device__ __forceinline__ void lds(uint32_t (&r)[4], uint32_t addr) {
-  asm("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
                : "memory");
 }
 
-// Four scale bytes as 2^(byte - 127), 255 as NaN: through bf16, which holds them all.
-__device__ __forceinline__ void scales_of(uint32_t w, float (&f)[4]) {
-  uint32_t lo, hi;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.bf16x2.ue8m0x2 %0, l;\n\tcvt.rn.bf16x2.ue8m0x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-  f[0] = ptx::bf16_lo(lo);
-  f[1] = ptx::bf16_hi(lo);
-  f[2] = ptx::bf16_lo(hi);
-  f[3] = ptx::bf16_hi(hi);
-}
-
-// Values k and k + 1 (k even) of a column of fp16: in order, but for MXFP4 with
-// steps 8c + j and 8c + j + 4 side by side, as the codes come apart.
-template <int WT>
-__device__ __forceinline__ void store_pair(uint16_t* column, int k, uint32_t v) {
-  if (WT == kFewMxfp4) {
-    uint16_t* to = column + (k & ~7) + 2 * (k & 3) + ((k >> 2) & 1);
-    to[0] = (uint16_t)v;
-    to[2] = (uint16_t)(v >> 16);
-  } else {
-    *reinterpret_cast<uint32_t*>(column + k) = v;
-  }
+// `count` arrivals at once.
+__device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(ptx::smem_u32(bar)), "r"(count) : "memory");
 }
 
 // One stage of a piece: a warp's sums for its 16 columns.  cols: the stage's part of
@@ -295,110 +258,7 @@ __device__ __forceinline__ void stage_bf16(uint32_t tile, uint32_t cols, int pit
   }
 }
 
-// e4m3: [steps][128 columns] codes; a 16-bit unit of ldmatrix is two columns of
-// one step, so a register holds columns 2g and 2g + 1 of steps 2c and 2c + 1.
-// True where the tile has a code 0x7f, whose sums are to be done again with NANS.
-template <int NT, bool NANS>
-__device__ __forceinline__ bool e4m3_sums(uint32_t tile, uint32_t cols, int pitch, int last, float (&part)[NT][4]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = lane >> 3, r = lane & 7;
-  uint32_t seen = 0;  // a byte's top bit, which adding 1 flips where the seven others are set
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) part[j][e] = 0.0f;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int k = 32 * q + 8 * i + r;
-    uint32_t w[4], a[4][2];
-    ldsm_t(w, tile + k * 128 + (((warp & 7) ^ (k & 7)) << 4));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (NANS) {
-        a[e][0] = e4m3_values(__byte_perm(w[e], 0, 0x4420));
-        a[e][1] = e4m3_values(__byte_perm(w[e], 0, 0x4431));
-      } else {
-        e4m3_pairs(w[e], a[e][0], a[e][1]);
-        seen |= (w[e] + 0x01010101u) ^ w[e];
-      }
-    }
-    const uint32_t a0[4] = {a[0][0], a[0][1], a[1][0], a[1][1]}, a1[4] = {a[2][0], a[2][1], a[3][0], a[3][1]};
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      uint32_t b[4];
-      ldsm(b, cols + min(8 * j + r, last) * pitch + (32 * q + 8 * i) * 2);
-      mma_f16(part[j], a0, b[0], b[1]);
-      mma_f16(part[j], a1, b[2], b[3]);
-    }
-  }
-  return (seen & 0x80808080u) != 0;
-}
-
-// f[j]: the block's scale times the columns' factor.
-template <int NT>
-__device__ __forceinline__ void stage_e4m3(uint32_t tile, uint32_t cols, int pitch, int last, const float (&f)[NT],
-                                           float (&acc)[NT][4]) {
-  float part[NT][4];
-  float up = 256.0f;
-  if (__any_sync(0xffffffffu, e4m3_sums<NT, false>(tile, cols, pitch, last, part))) {
-    e4m3_sums<NT, true>(tile, cols, pitch, last, part);
-    up = 1.0f;
-  }
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(part[j][e], f[j] * up, acc[j][e]);
-}
-
-// MXFP4: [128 columns][steps / 2] codes, one half of the steps; lane (g, c) holds
-// the eight codes 8c of a scale block for columns g and g + 8, whose scale bytes
-// are in s[0], s[1].  f[j]: the columns' factor.
-template <int NT>
-__device__ __forceinline__ void stage_mxfp4(uint32_t tile, int half, uint32_t cols, int pitch, int last,
-                                            const uint32_t (&s)[2], const float (&f)[NT], float (&acc)[NT][4]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = lane >> 3, r = lane & 7, g = lane >> 2, c = lane & 3;
-  const int n = (warp & 7) * 16 + (i & 1) * 8 + r;
-  float sum[NT][4] = {};
-  float s0[4], s1[4];
-  scales_of(s[0], s0);
-  scales_of(s[1], s1);
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {  // two scale blocks
-    uint32_t w[4];
-    const int chunk = half * 4 + 2 * p + (i >> 1);
-    ldsm(w, tile + n * 128 + ((chunk ^ (n & 7)) << 4));
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int blk = 2 * p + q;
-      uint32_t x[4], y[4];
-      mx_pairs(w[2 * q], x);
-      mx_pairs(w[2 * q + 1], y);
-      const uint32_t a0[4] = {x[0], y[0], x[1], y[1]}, a1[4] = {x[2], y[2], x[3], y[3]};
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        uint32_t b[4];
-        lds(b, cols + min(8 * j + g, last) * pitch + (half * 128 + blk * 32 + 8 * c) * 2);
-        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        mma_f16(part, a0, b[0], b[1]);
-        mma_f16(part, a1, b[2], b[3]);
-        sum[j][0] = fmaf(part[0], s0[blk], sum[j][0]);
-        sum[j][1] = fmaf(part[1], s0[blk], sum[j][1]);
-        sum[j][2] = fmaf(part[2], s1[blk], sum[j][2]);
-        sum[j][3] = fmaf(part[3], s1[blk], sum[j][3]);
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(sum[j][e], f[j] * 16384.0f, acc[j][e]);
-}
-
 // ------------------------------------------------------------ shares and pieces
-// B columns that a row of h takes.
-__host__ __device__ constexpr int terms(int weights) { return weights == kFewBf16 ? 3 : 2; }
-
 // A chunk, or one pass over it: units [step0, step1) of 128 output columns of
 // one matrix, for `rows` rows of `group` B columns each.
 struct Piece {
@@ -443,67 +303,66 @@ struct Share {
     q.expert = SHARED ? 0 : ls.expert[ei];
     q.first = SHARED ? 0 : ls.start[ei];
     q.rows = SHARED ? p.T : ls.start[ei + 1] - q.first;
-    q.group = DOWN ? terms(WT) : 1;
+    q.group = DOWN ? 3 : 1;
     q.again = q.rows > kPass;
     q.ld = (int64_t)per_expert * split.parts * kFewCols;
     q.out = buf + q.first * q.ld + ((int64_t)in * split.parts + part) * kFewCols;
     return q;
   }
-  // Rows of a pass: at most 8 in the down projections (more read the weights
+  // Rows of a pass: 24 bf16 columns or 64 rows of terms (more rows read the weights
   // again, from L2 mostly: only the shared expert and crowded small layers have
   // them).
-  static constexpr int kPass = DOWN ? 8 : kFewMaxTokens;
+  static constexpr int kPass = WT == kFewBf16 ? (DOWN ? kMaxCols / 3 : kFewMaxTokens) : 64 / few_term_rows(WT);
+  static __device__ __forceinline__ void cut(Piece& q, int all, int r0) {
+    q.rows = min(kPass, all - r0);
+    q.first += r0;
+    q.out += r0 * q.ld;
+  }
   template <typename F>
-  __device__ __forceinline__ bool passes(Piece q, F f) const {
-    const int all = q.rows;
-    for (int r0 = 0; r0 < all; r0 += kPass) {
-      q.rows = min(kPass, all - r0);
+  __device__ __forceinline__ bool passes(const Piece& whole, F f) const {
+    for (int r0 = 0; r0 < whole.rows; r0 += kPass) {
+      Piece q = whole;
+      cut(q, whole.rows, r0);
       if (!f(q)) return false;
-      q.first += kPass;
-      q.out += kPass * q.ld;
     }
     return true;
   }
 };
 
-// How many units' columns a buffer takes for a piece, and the columns' distance
-// in bytes: a pad keeps the reads of 8 columns off each other's banks.
-template <int WT>
+// bf16 columns: how many units' a buffer takes for a piece, and their distance in
+// bytes: a pad keeps the reads of 8 columns off each other's banks.
+template <int RT>
 struct ColumnPlan {
-  static constexpr int kUnitBytes = 2 * few_unit_steps(WT);
-  static constexpr int kPad = WT == kFewMxfp4 ? 64 : 16;
+  static constexpr int kUnitBytes = 2 * few_unit_steps(kFewBf16);
+  static constexpr int kPad = 16;
   int units, pitch;
   __device__ __forceinline__ explicit ColumnPlan(const Piece& q) {
     const int cols = q.rows * q.group;
-    units = min(q.step1 - q.step0, ((int)kColBytes / cols - kPad) / kUnitBytes);
+    units = min(q.step1 - q.step0, ((int)Cfg<RT>::kColBytes / cols - kPad) / kUnitBytes);
     pitch = units * kUnitBytes + kPad;
   }
+  static_assert((int)Cfg<RT>::kColBytes / kMaxCols >= kUnitBytes + kPad, "room for one unit's columns");
 };
-// every piece has room for one unit's columns
-static_assert((int)kColBytes / kMaxCols >= 2 * 64 + 16 && (int)kColBytes / 16 >= 2 * 256 + 64, "B columns");
 
-// The rings' positions: stages and column buffers handed over so far, and which
-// phase of its `scaled` barrier each stage is in (only routed stages have one).
+// The rings' positions: stages and column buffers handed over so far, and
+// accumulators.
 struct Ring {
-  int n = 0, cols = 0;
-  uint32_t scaled = 0;
-};
-
-// What goes with a stage's tile of codes: MXFP4's scale bytes of both halves of
-// the steps for each of the 128 columns, and a factor for each row of h (e4m3: for
-// each row, the block's scale times it) and half.
-struct StageScales {
-  uint32_t words[kFewCols][2];
-  float factor[8][2];
+  int n = 0, cols = 0, accs = 0;
 };
 
 struct Smem {
-  StageScales* scales;
   uint8_t* stages;
   uint8_t* cols;
   float* red;
+  uint32_t* exchange;  // MXFP4: two groups of scales on their way from rows to lanes
   Control* c;
 };
+
+template <int RT>
+__device__ __forceinline__ bool wait_issued(Control& c, int n) {
+  constexpr int kTurns = 2 * Cfg<RT>::kStages;
+  return warp_wait(&c.issued[n % kTurns], (n / kTurns) & 1, &c.abort);
+}
 
 // ------------------------------------------------------------ producer
 // The weight tile of unit `step` of a piece.
@@ -522,15 +381,16 @@ __device__ __forceinline__ void load_tile(const FewMaps& m, const FewParams& p, 
   }
 }
 
-template <int WT, bool SHARED, bool DOWN>
+template <int WT, int RT, bool SHARED, bool DOWN>
 __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring,
                         uint32_t* counter) {
+  constexpr int S = Cfg<RT>::kStages;
   const int lane = threadIdx.x & 31;
   const uint64_t once = ptx::policy_evict_first(), more = ptx::policy_evict_normal();
   Control& c = *sm.c;
   const Share<WT, SHARED, DOWN> share(p, ls);
   auto slot_free = [&] {
-    if (warp_wait(&c.empty[ring.n % kStages], ((ring.n / kStages) & 1) ^ 1, &c.abort)) return true;
+    if (warp_wait(&c.empty[ring.n % S], ((ring.n / S) & 1) ^ 1, &c.abort)) return true;
     if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
     return false;
   };
@@ -539,14 +399,16 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
     int claimed = 0;
     if (lane == 0) claimed = (int)atomicAdd(counter, 1u) + gridDim.x;  // used after this chunk
     const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
+      // the columns' warp adds the terms to a stage of codes
+      const uint32_t bytes = kTileBytes + (WT == kFewBf16 ? 0 : q.rows * few_term_rows(WT) * 128);
       for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
-        const int s = ring.n % kStages;
+        const int s = ring.n % S;
         if (!slot_free()) return false;
         if (lane == 0) {
-          c.chunk[ring.n % (2 * kStages)] = id;
-          ptx::mbar_arrive(&c.issued[ring.n % (2 * kStages)]);
-          ptx::mbar_arrive_expect_tx(&c.full[s], kTileBytes);
-          load_tile<WT, SHARED>(m, p, q, step, sm.stages + s * kTileBytes, &c.full[s], q.again ? more : once);
+          ptx::mbar_arrive_expect_tx(&c.full[s], bytes);
+          c.chunk[ring.n % (2 * S)] = id;
+          ptx::mbar_arrive(&c.issued[ring.n % (2 * S)]);
+          load_tile<WT, SHARED>(m, p, q, step, sm.stages + s * Cfg<RT>::kStageBytes, &c.full[s], q.again ? more : once);
         }
         __syncwarp();
       }
@@ -557,176 +419,127 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
   }
   if (!slot_free()) return false;
   if (lane == 0) {
-    c.chunk[ring.n % (2 * kStages)] = -1;
-    ptx::mbar_arrive(&c.issued[ring.n % (2 * kStages)]);
-    ptx::mbar_arrive(&c.full[ring.n % kStages]);
+    c.chunk[ring.n % (2 * S)] = -1;
+    ptx::mbar_arrive(&c.issued[ring.n % (2 * S)]);
+    ptx::mbar_arrive(&c.full[ring.n % S]);
   }
   ++ring.n;
   return true;
 }
 
 // ------------------------------------------------------------ columns
-template <int WT, bool SHARED, bool DOWN>
-__device__ bool bring_columns(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
-  constexpr int kSteps = few_unit_steps(WT);
-  const int lane = threadIdx.x & 31;
+// Walks a share's chunks: f for every pass, ring.n being its first stage.
+template <int WT, int RT, bool SHARED, bool DOWN, typename F>
+__device__ __forceinline__ bool follow_chunks(const FewParams& p, const Lists& ls, const Smem& sm, const Ring& ring, F f) {
   const Share<WT, SHARED, DOWN> share(p, ls);
   Control& c = *sm.c;
-  auto wait = [&](uint64_t* bar, int n) {
-    if (warp_wait(bar, n & 1, &c.abort)) return true;
+  int id = blockIdx.x < share.total ? (int)blockIdx.x : -1;  // the first chunk needs no tile to be known by
+  while (id >= 0) {
+    if (!share.passes(share.chunk(p, ls, id), f)) return false;
+    if (!wait_issued<RT>(c, ring.n)) {
+      if ((threadIdx.x & 31) == 0) raise_status(p.status, &c.abort, kStatusTimeout);
+      return false;
+    }
+    id = c.chunk[ring.n % (2 * Cfg<RT>::kStages)];
+  }
+  return true;
+}
+
+// The columns of bf16 shares.  A stage is also released by this warp, so that its
+// chunk is still to be read when it gets there.
+template <int RT, bool SHARED, bool DOWN>
+__device__ bool bring_columns(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
+  constexpr int kSteps = few_unit_steps(kFewBf16);
+  const int lane = threadIdx.x & 31;
+  const int K = DOWN ? (SHARED ? p.S : p.I) : p.d;
+  Control& c = *sm.c;
+  auto give_up = [&] {
     if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
     return false;
   };
-  // a stage is also released by this warp, so that its chunk is still to be read
   auto next_stage = [&] {
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&c.empty[ring.n % kStages]);
+    if (lane == 0) ptx::mbar_arrive(&c.empty[ring.n % Cfg<RT>::kStages]);
     ++ring.n;
   };
-  int id = blockIdx.x < share.total ? (int)blockIdx.x : -1;  // the first chunk needs no tile to be known by
-  while (true) {
-    if (id < 0) {
-      if (!wait(&c.issued[ring.n % (2 * kStages)], ring.n / (2 * kStages))) return false;
-      next_stage();
-      return true;
+  const bool ok = follow_chunks<kFewBf16, RT, SHARED, DOWN>(p, ls, sm, ring, [&](const Piece& q) {
+    const ColumnPlan<RT> plan(q);
+    const int cols = q.rows * q.group;
+    const uint8_t* src = nullptr;
+    if (lane < cols) {
+      if (DOWN)
+        src = (SHARED ? p.h_s : p.h_r) + ((int64_t)q.first * 3 + lane) * K * 2;
+      else
+        src = p.x + (SHARED ? q.first + lane : ls.ent[q.first + lane] / p.k) * (int64_t)p.d * 2;
     }
-    const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
-      const ColumnPlan<WT> plan(q);
-      const int cols = q.rows * q.group;
-      const uint8_t* src = nullptr;
-      if (lane < cols) {
-        if (DOWN)
-          src = (SHARED ? p.h_s : p.h_r) + ((int64_t)q.first * terms(WT) + lane) * share.K * 2;
-        else
-          src = (WT == kFewBf16 ? p.x : p.x16) + (SHARED ? q.first + lane : ls.ent[q.first + lane] / p.k) * (int64_t)p.d * 2;
+    for (int step = q.step0; step < q.step1; ++step) {
+      if ((step - q.step0) % plan.units == 0) {
+        const int buf = ring.cols & 1;
+        if (!warp_wait(&c.col_empty[buf], ((ring.cols >> 1) & 1) ^ 1, &c.abort)) return give_up();
+        const uint32_t bytes = 2 * kSteps * (min(q.step1, step + plan.units) - step);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&c.col_full[buf], bytes * cols);
+        __syncwarp();
+        if (lane < cols)
+          bulk_load(ptx::smem_u32(sm.cols) + buf * Cfg<RT>::kColBytes + lane * plan.pitch, src + step * kSteps * 2, bytes,
+                    &c.col_full[buf]);
+        ++ring.cols;
       }
-      for (int step = q.step0; step < q.step1; ++step) {
-        if ((step - q.step0) % plan.units == 0) {
-          const int buf = ring.cols & 1;
-          if (!wait(&c.col_empty[buf], (ring.cols >> 1) + 1)) return false;
-          const int last = min(q.step1, step + plan.units);
-          const uint32_t bytes = 2 * (min(share.K, last * kSteps) - step * kSteps);
-          if (lane == 0) ptx::mbar_arrive_expect_tx(&c.col_full[buf], bytes * cols);
-          __syncwarp();
-          if (lane < cols)
-            bulk_load(ptx::smem_u32(sm.cols) + buf * kColBytes + lane * plan.pitch, src + step * kSteps * 2, bytes,
-                      &c.col_full[buf]);
-          ++ring.cols;
-        }
-        if (!wait(&c.issued[ring.n % (2 * kStages)], ring.n / (2 * kStages))) return false;
-        next_stage();
-      }
-      return true;
-    });
-    if (!ok || !wait(&c.issued[ring.n % (2 * kStages)], ring.n / (2 * kStages))) return false;
-    id = c.chunk[ring.n % (2 * kStages)];
-  }
+      if (!wait_issued<RT>(c, ring.n)) return give_up();
+      next_stage();
+    }
+    return true;
+  });
+  if (!ok || !wait_issued<RT>(c, ring.n)) return give_up();
+  next_stage();  // the mark of the end
+  return true;
 }
 
-// ------------------------------------------------------------ scales
-// The scales of a routed share, by the router's warps: MXFP4's by all 64 threads,
-// two columns each, e4m3's by the first warp.
-template <int WT, bool DOWN>
-__device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
-  constexpr int kGroup = 4;  // units whose loads go together
+// The terms of coded shares, into the stages themselves: a row's are one or two
+// swizzle atoms of 8 rows.
+template <int RT, bool DOWN>
+__device__ bool bring_terms(const FewMaps& m, const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
+  constexpr int S = Cfg<RT>::kStages, kRows = few_term_rows(RT);
   const int lane = threadIdx.x & 31;
-  const int tid = threadIdx.x - kAllThreads + 32 * kRouterWarps;
-  const Share<WT, false, DOWN> share(p, ls);
+  const uint64_t policy = ptx::policy_evict_normal();
   Control& c = *sm.c;
-  auto wait = [&](int n) {
-    if (warp_wait(&c.issued[n % (2 * kStages)], (n / (2 * kStages)) & 1, &c.abort)) return true;
+  auto give_up = [&] {
     if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
     return false;
   };
-  auto hand_over = [&] {
+  // this warp's release of a stage, and the seven of the consumer warps that have
+  // no part in coded shares (the MMAs' completion is the last)
+  auto next_stage = [&] {
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&c.scaled[ring.n % kStages]);
+    if (lane == 0) mbar_arrive_many(&c.empty[ring.n % S], 8);
     ++ring.n;
   };
-  const int words = share.K / 128;
-  int id = blockIdx.x < share.total ? (int)blockIdx.x : -1;
-  while (true) {
-    if (id < 0) {
-      if (!wait(ring.n)) return false;
-      hand_over();
-      return true;
+  const bool ok = follow_chunks<RT, RT, false, DOWN>(p, ls, sm, ring, [&](const Piece& q) {
+    int row = 0;
+    if (lane < q.rows) row = (DOWN ? q.first + lane : ls.ent[q.first + lane] / p.k) * kRows;
+    for (int step = q.step0; step < q.step1; ++step) {
+      if (!wait_issued<RT>(c, ring.n)) return give_up();
+      const int s = ring.n % S;
+      if (lane < q.rows)
+        ptx::tma_load_2d(sm.stages + s * Cfg<RT>::kStageBytes + kTileBytes + lane * kRows * 128,
+                         DOWN ? &m.h_terms : &m.x_terms, &c.full[s], step * 128, row, policy);
+      next_stage();
     }
-    const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
-      const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
-      for (int step0 = q.step0; step0 < q.step1; step0 += kGroup) {
-        if constexpr (WT == kFewE4m3) {
-          // lane 8 u + r: unit u of the group, row r of the piece
-          const int step = step0 + (lane >> 3), row = lane & 7;
-          float f = 0.0f;
-          if (step < q.step1) {
-            f = __ldg(reinterpret_cast<const float*>(scales) +
-                      ((int64_t)q.expert * (share.K / 128) + step) * (share.N / 128) + q.col0 / 128);
-            if (DOWN && row < q.rows) f *= __ldcg(p.h_scale + (int64_t)(q.first + row) * (share.K / 128) + step);
-          }
-          for (int u = 0; u < kGroup && step0 + u < q.step1; ++u) {
-            if (!wait(ring.n)) return false;
-            if ((lane >> 3) == u && tid < 32) {
-              float* to = sm.scales[ring.n % kStages].factor[row];
-              to[0] = f;
-              to[1] = f;
-            }
-            hand_over();
-          }
-        } else {
-          uint32_t w[kGroup][2][2];
-          float f[kGroup];
-          const int row = (tid >> 1) & 7, half = tid & 1;
-#pragma unroll
-          for (int u = 0; u < kGroup; ++u) {
-            const int step = step0 + u;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t* at = reinterpret_cast<const uint32_t*>(scales) +
-                                   ((int64_t)q.expert * share.N + q.col0 + tid + 64 * i) * words + 2 * step;
-              if (step >= q.step1) {
-                w[u][i][0] = w[u][i][1] = 0u;
-              } else if ((words & 1) == 0) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
-                w[u][i][0] = v.x;
-                w[u][i][1] = v.y;
-              } else {
-                w[u][i][0] = __ldg(at);
-                w[u][i][1] = 2 * step + 1 < words ? __ldg(at + 1) : 0u;
-              }
-            }
-            f[u] = 1.0f;
-            if (DOWN && tid < 16 && row < q.rows && step < q.step1 && 2 * step + half < words)
-              f[u] = __ldcg(p.h_scale + (int64_t)(q.first + row) * words + 2 * step + half);
-          }
-#pragma unroll
-          for (int u = 0; u < kGroup; ++u) {
-            if (step0 + u < q.step1) {
-              if (!wait(ring.n)) return false;
-              StageScales& to = sm.scales[ring.n % kStages];
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                *reinterpret_cast<uint2*>(to.words[tid + 64 * i]) = make_uint2(w[u][i][0], w[u][i][1]);
-              if (tid < 16) to.factor[row][half] = f[u];
-              hand_over();
-            }
-          }
-        }
-      }
-      return true;
-    });
-    if (!ok || !wait(ring.n)) return false;
-    id = c.chunk[ring.n % (2 * kStages)];
-  }
+    return true;
+  });
+  if (!ok || !wait_issued<RT>(c, ring.n)) return give_up();
+  next_stage();
+  return true;
 }
 
-// ------------------------------------------------------------ consumers
-template <int WT, int NT, bool DOWN>
-__device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q, int K, const Smem& sm, Ring& ring) {
+// ------------------------------------------------------------ consumers: bf16
+template <int RT, int NT>
+__device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q, const Smem& sm, Ring& ring) {
+  constexpr int S = Cfg<RT>::kStages;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3, team = warp >> 3;
   Control& ct = *sm.c;
   float acc[NT][4] = {};
-  const ColumnPlan<WT> plan(q);
+  const ColumnPlan<RT> plan(q);
   const int last = q.rows * q.group - 1;
   int left = 0;  // units whose columns are in the buffer
   uint32_t cols = 0;
@@ -740,40 +553,20 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
     if (left == 0) {
       const int buf = ring.cols & 1;
       arrived(&ct.col_full[buf], (ring.cols >> 1) & 1);
-      cols = ptx::smem_u32(sm.cols) + buf * kColBytes;
+      cols = ptx::smem_u32(sm.cols) + buf * Cfg<RT>::kColBytes;
       left = min(plan.units, q.step1 - step);
     }
-    const int slot = ring.n % kStages;
+    const int slot = ring.n % S;
     if ((ring.n & 1) == team) {
-      arrived(&ct.full[slot], (ring.n / kStages) & 1);
-      uint32_t tile = ptx::smem_u32(sm.stages) + slot * kTileBytes;
-      if constexpr (WT == kFewBf16) {
-        after_wait(tile, cols);
-        stage_bf16<NT>(tile, cols, plan.pitch, last, acc);
-      } else {
-        arrived(&ct.scaled[slot], (ring.scaled >> slot) & 1);
-        after_wait(tile, cols);
-        const StageScales& sc = sm.scales[slot];
-        const int halves = WT == kFewMxfp4 && 2 * step + 1 < K / 128 ? 2 : 1;  // MXFP4's last unit may be half of one
-        for (int h = 0; h < halves; ++h) {
-          float f[NT];  // of the row that columns 2c and 2c + 1 belong to
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            f[j] = sc.factor[DOWN && NT <= 2 ? 4 * j + c : 0][h];
-          if constexpr (WT == kFewE4m3) {
-            stage_e4m3<NT>(tile, cols, plan.pitch, last, f, acc);
-          } else {
-            const uint32_t s[2] = {sc.words[(warp & 7) * 16 + g][h], sc.words[(warp & 7) * 16 + g + 8][h]};
-            stage_mxfp4<NT>(tile, h, cols, plan.pitch, last, s, f, acc);
-          }
-        }
-      }
+      arrived(&ct.full[slot], (ring.n / S) & 1);
+      uint32_t tile = ptx::smem_u32(sm.stages) + slot * Cfg<RT>::kStageBytes;
+      after_wait(tile, cols);
+      stage_bf16<NT>(tile, cols, plan.pitch, last, acc);
       before_release<NT>(acc);
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&ct.empty[slot]);
     }
-    if (WT != kFewBf16) ring.scaled ^= 1u << slot;
-    cols += ColumnPlan<WT>::kUnitBytes;
+    cols += ColumnPlan<RT>::kUnitBytes;
     ++ring.n;
     if (--left == 0) {
       __syncwarp();
@@ -781,18 +574,17 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
       ++ring.cols;
     }
   }
-  // the two teams' sums, and the terms of each row, are joined by the
-  // pair of warps that has these 16 columns
+  // the two teams' sums, and the terms of each row, are joined by the pair of warps
+  // that has these 16 columns
   const int pair = warp & 7;
   float* red = sm.red + pair * kRedFloats;
-  const int lo = WT == kFewE4m3 ? 2 * g : g, hi = WT == kFewE4m3 ? 2 * g + 1 : g + 8;
   float* to = red + team * kMaxCols * kRedPitch;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    to[(8 * j + 2 * c) * kRedPitch + lo] = acc[j][0];
-    to[(8 * j + 2 * c + 1) * kRedPitch + lo] = acc[j][1];
-    to[(8 * j + 2 * c) * kRedPitch + hi] = acc[j][2];
-    to[(8 * j + 2 * c + 1) * kRedPitch + hi] = acc[j][3];
+    to[(8 * j + 2 * c) * kRedPitch + g] = acc[j][0];
+    to[(8 * j + 2 * c + 1) * kRedPitch + g] = acc[j][1];
+    to[(8 * j + 2 * c) * kRedPitch + g + 8] = acc[j][2];
+    to[(8 * j + 2 * c + 1) * kRedPitch + g + 8] = acc[j][3];
   }
   ptx::named_barrier(1 + pair, 64);
   for (int i = team * 32 + lane; i < q.rows * 16; i += 64) {
@@ -807,40 +599,358 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
   ptx::named_barrier(1 + pair, 64);
 }
 
-template <int WT, bool SHARED, bool DOWN>
+template <int RT, bool SHARED, bool DOWN>
 __device__ bool consume(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
-  const Share<WT, SHARED, DOWN> share(p, ls);
+  constexpr int S = Cfg<RT>::kStages;
+  const Share<kFewBf16, SHARED, DOWN> share(p, ls);
   Control& ct = *sm.c;
   volatile uint32_t* abort = &ct.abort;
   while (true) {
-    const int at = ring.n % (2 * kStages);
-    const bool there = warp_wait(&ct.issued[at], (ring.n / (2 * kStages)) & 1, &ct.abort);
+    const bool there = wait_issued<RT>(ct, ring.n);
     if (!there) raise_status(p.status, &ct.abort, kStatusTimeout);
     // both warps of a pair take the chunk or neither
     if (!ptx::named_barrier_and(1 + ((threadIdx.x >> 5) & 7), 64, there && *abort == 0)) return false;
-    const int id = ct.chunk[at];
+    const int id = ct.chunk[ring.n % (2 * S)];
     if (id < 0) {
-      const int slot = ring.n % kStages;
-      if (WT != kFewBf16) {  // the scales' warps still read the mark
-        if (!ptx::wait_bounded(&ct.scaled[slot], (ring.scaled >> slot) & 1, &ct.abort))
-          raise_status(p.status, &ct.abort, kStatusTimeout);
-        ring.scaled ^= 1u << slot;
-      }
       __syncwarp();
-      if ((threadIdx.x & 31) == 0 && (ring.n & 1) == (threadIdx.x >> 8)) ptx::mbar_arrive(&ct.empty[slot]);
+      if ((threadIdx.x & 31) == 0 && (ring.n & 1) == (threadIdx.x >> 8)) ptx::mbar_arrive(&ct.empty[ring.n % S]);
       ++ring.n;
       return true;
     }
     share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
       const int cols = q.rows * q.group;
       if (cols <= 8)
-        consume_piece<WT, 1, DOWN>(p, q, share.K, sm, ring);
-      else if (cols <= 16 || terms(WT) == 2)
-        consume_piece<WT, 2, DOWN>(p, q, share.K, sm, ring);
+        consume_piece<RT, 1>(p, q, sm, ring);
+      else if (cols <= 16)
+        consume_piece<RT, 2>(p, q, sm, ring);
       else
-        consume_piece<WT, terms(WT) == 2 ? 2 : 3, DOWN>(p, q, share.K, sm, ring);
+        consume_piece<RT, 3>(p, q, sm, ring);
       return true;
     });
+  }
+}
+
+// ------------------------------------------------------------ consumers: codes
+// kind::f8f6f4 instruction descriptor: fp32 accumulator (bits 4-5 = 1), A and B
+// e4m3 (0), A MN-major (bit 15: weights lie [steps][columns]), B K-major, N >> 3 at
+// bits 17-22, M >> 4 at bits 24-28.
+__device__ __forceinline__ uint32_t idesc_e4m3(int N) {
+  return (1u << 4) | (1u << 15) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// kind::mxf4: A and B e2m1 (bits 7-9 and 10-11 = 1), both K-major, ue8m0 scales (bit
+// 23), M >> 7 at bits 27-28, and which pair of a TMEM word's four scale bytes to
+// use, bits 29-30 (A) and 4-5 (B).
+__device__ __forceinline__ uint32_t idesc_mxf4(int N, uint32_t pair) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) | ((pair * 2) << 29) |
+         ((pair * 2) << 4);
+}
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// Issues a share's MMAs (one warp; one lane issues).
+template <int RT, bool DOWN>
+__device__ bool issue_mmas(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
+  constexpr int S = Cfg<RT>::kStages, kA = kAccs<RT>;
+  const int lane = threadIdx.x & 31;
+  Control& c = *sm.c;
+  const uint32_t base = ptx::smem_u32(sm.stages);
+  const uint64_t a_desc = ptx::sdesc_sw128(base, 16, 1024), b_desc = ptx::sdesc_sw128(base + kTileBytes, 16, 1024);
+  const int K = DOWN ? p.I : p.d;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (warp_wait(bar, parity, &c.abort)) return true;
+    if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
+    return false;
+  };
+  // an accumulator is handed over when its MMAs are done and its labels are there
+  auto take = [&] { return wait(&c.acc_empty[ring.accs % kA], ((ring.accs / kA) & 1) ^ 1); };
+  auto hand_over = [&](int id, int pass, int step) {
+    if (lane == 0) {
+      const int b = ring.accs % kA;
+      ptx::mma_commit(&c.acc_full[b]);
+      c.acc_chunk[b] = id;
+      c.acc_pass[b] = pass;
+      c.acc_step[b] = step;
+      ptx::mbar_arrive(&c.acc_full[b]);
+    }
+    __syncwarp();
+    ++ring.accs;
+  };
+  const Share<RT, false, DOWN> share(p, ls);
+  while (true) {
+    if (!wait(&c.issued[ring.n % (2 * S)], (ring.n / (2 * S)) & 1)) return false;
+    const int id = c.chunk[ring.n % (2 * S)];
+    if (id < 0) break;
+    int pass = 0;
+    const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
+      const int N = (q.rows * few_term_rows(RT) + 15) & ~15;
+      const uint32_t id0 = RT == kFewE4m3 ? idesc_e4m3(N) : idesc_mxf4(N, 0), id1 = idesc_mxf4(N, 1);
+      for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
+        const int s = ring.n % S;
+        if ((RT == kFewE4m3 || step == q.step0) && !take()) return false;
+        if (!wait(&c.full[s], (ring.n / S) & 1)) return false;
+        if (RT == kFewMxfp4) {
+          // every stage of a coded share has scales: its own count of them
+          if (!wait(&c.scaled[s], (ring.cols >> s) & 1)) return false;
+          ring.cols ^= 1 << s;
+        }
+        ptx::tc_fence_after();
+        if (lane == 0) {
+          const uint32_t off = s * (Cfg<RT>::kStageBytes >> 4);
+          const uint64_t a = a_desc + off, b = b_desc + off;
+          const uint32_t d = c.tmem + (ring.accs % kA) * kAccCols;
+          if (RT == kFewE4m3) {
+            // 32 steps: 32 rows of the tile, 32 bytes of a term's row
+            mma_e4m3(d, a, b, id0, 0u);
+            mma_e4m3(d, a + (4096 >> 4), b + 2, id0, 1u);
+            mma_e4m3(d, a + (8192 >> 4), b + 4, id0, 1u);
+            mma_e4m3(d, a + (12288 >> 4), b + 6, id0, 1u);
+          } else {
+            const uint32_t sf = c.tmem + kA * kAccCols + s * kSfCols;
+            mma_mxf4(d, a, b, id0, sf, sf + 8, step != q.step0 ? 1u : 0u);
+            mma_mxf4(d, a + 2, b + 2, id1, sf, sf + 8, 1u);
+            if (K - step * 256 > 128) {  // else the last unit is half of one
+              mma_mxf4(d, a + 4, b + 4, id0, sf + 4, sf + 12, 1u);
+              mma_mxf4(d, a + 6, b + 6, id1, sf + 4, sf + 12, 1u);
+            }
+          }
+          ptx::mma_commit(&c.empty[s]);
+        }
+        __syncwarp();
+        if (RT == kFewE4m3) hand_over(id, pass, step);
+      }
+      if (RT == kFewMxfp4) hand_over(id, pass, q.step1 - 1);
+      ++pass;
+      return true;
+    });
+    if (!ok) return false;
+  }
+  if (!take()) return false;
+  hand_over(-1, 0, 0);
+  if (lane == 0) {
+    ptx::mbar_arrive(&c.empty[ring.n % S]);
+    c.position = ring.n + 1;
+  }
+  __syncwarp();
+  ++ring.n;
+  return true;
+}
+
+// 16 consecutive TMEM columns of this thread's lane as fp32.
+__device__ __forceinline__ void load_sums(uint32_t tmem, float (&v)[16]) {
+  uint32_t r[16];
+  ptx::tmem_ld16(tmem, r);
+  ptx::tmem_ld_wait(r);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Drains a share's accumulators (four warps; a thread has one output column).
+template <int RT, bool DOWN>
+__device__ bool drain(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
+  constexpr int kA = kAccs<RT>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = threadIdx.x & 127;
+  Control& c = *sm.c;
+  const Share<RT, false, DOWN> share(p, ls);
+  float sums[8];     // e4m3: of each row
+  float factor[8];   // e4m3: lane l has unit l's, for each row, of the chunk
+  while (true) {
+    const int b = ring.accs % kA;
+    if (!warp_wait(&c.acc_full[b], (ring.accs / kA) & 1, &c.abort)) {
+      if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
+      return false;
+    }
+    ptx::tc_fence_after();
+    const int id = c.acc_chunk[b], pass = c.acc_pass[b], step = c.acc_step[b];
+    auto release = [&] {
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(&c.acc_empty[b]);
+      ++ring.accs;
+    };
+    if (id < 0) {
+      release();
+      return true;
+    }
+    Piece q = share.chunk(p, ls, id);
+    share.cut(q, q.rows, pass * share.kPass);
+    const uint32_t acc = c.tmem + ((uint32_t)((warp & 3) * 32) << 16) + b * kAccCols;
+    if constexpr (RT == kFewMxfp4) {
+      for (int r = 0; r < q.rows; ++r) {
+        float v[16];
+        load_sums(acc + r * 16, v);
+        // the last terms, the smallest, first
+        float a = 0.0f;
+#pragma unroll
+        for (int t = kTerms4 - 1; t >= 0; --t) a += v[t];
+        q.out[r * q.ld + col] = a;
+      }
+      release();
+    } else {
+      if (step == q.step0) {
+        // the block's scale times the row's factor, unit step0 + lane's
+        const int unit = min(step + lane, share.steps - 1);
+        const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
+        const float f = __ldg(reinterpret_cast<const float*>(scales) +
+                              ((int64_t)q.expert * share.steps + unit) * share.blocks + q.col0 / 128);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          sums[r] = 0.0f;
+          factor[r] = 0.0f;
+          if (r < q.rows) {
+            const int row = DOWN ? q.first + r : ls.ent[q.first + r] / p.k;
+            factor[r] = f * __ldcg((DOWN ? p.h_scale : p.x_scale) + (int64_t)row * share.steps + unit);
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 8; r += 2) {
+        if (r < q.rows) {
+          float v[16];
+          load_sums(acc + r * 8, v);
+          constexpr int kT = DOWN ? kHTerms8 : kXTerms8;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float a = 0.0f;
+#pragma unroll
+            for (int t = kT - 1; t >= 0; --t) a = fmaf(a, 0.0625f, v[8 * i + t]);
+            sums[r + i] = fmaf(a, __shfl_sync(0xffffffffu, factor[r + i], step - q.step0), sums[r + i]);
+          }
+        }
+      }
+      release();
+      if (step == q.step1 - 1) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < q.rows) q.out[r * q.ld + col] = sums[r];
+      }
+    }
+  }
+}
+
+// MXFP4: a share's scales to TMEM (four warps), row r of 128 in lane r % 32 of
+// column r / 32 in all lane quarters, four blocks of 32 steps to a word.  Thread r
+// reads row r of the weights and of the terms, a group of units at a time, and the
+// rows go through shared memory to the lanes that store them.
+template <bool DOWN>
+__device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
+  constexpr int RT = kFewMxfp4, S = Cfg<RT>::kStages, kGroup = 4, kRows = 128 + 64;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = threadIdx.x & 127;
+  Control& c = *sm.c;
+  const Share<RT, false, DOWN> share(p, ls);
+  const int words = share.K / 128;  // of a row, four scales each
+  const uint8_t* terms = DOWN ? p.h_term_scales : p.x_term_scales;
+  int buf = 0;
+  bool ok = true;
+  // A warp whose wait failed goes on without: the others need it at the barriers.
+  // They leave together at the end of a chunk.
+  auto issued = [&] {
+    if (ok && !wait_issued<RT>(c, ring.n)) {
+      if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
+      ok = false;
+    }
+    return ok;
+  };
+  auto pass = [&](const Piece& q) {
+    const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(scales) + ((int64_t)q.expert * share.N + q.col0 + r) * words;
+    const uint32_t* x = nullptr;
+    if (r < q.rows * kTermRows4) {
+      const int row = DOWN ? q.first + r / kTermRows4 : ls.ent[q.first + r / kTermRows4] / p.k;
+      x = reinterpret_cast<const uint32_t*>(terms) + ((int64_t)row * kTermRows4 + r % kTermRows4) * words;
+    }
+    for (int step0 = q.step0; step0 < q.step1; step0 += kGroup) {
+      uint32_t a[2 * kGroup], t[2 * kGroup];
+#pragma unroll
+      for (int i = 0; i < 2 * kGroup; ++i) {
+        const int at = 2 * step0 + i;
+        const bool have = at < words && step0 + i / 2 < q.step1;
+        a[i] = have ? __ldg(w + at) : 0u;
+        t[i] = have && x ? __ldcg(x + at) : 0u;
+      }
+      uint32_t* ex = sm.exchange + buf * (2 * kGroup * kRows);
+#pragma unroll
+      for (int i = 0; i < 2 * kGroup; ++i) {
+        ex[i * kRows + r] = a[i];
+        if (r < 64) ex[i * kRows + 128 + r] = t[i];
+      }
+      ptx::named_barrier(11, 128);
+      for (int u = 0; u < kGroup && step0 + u < q.step1; ++u, ++ring.n) {
+        uint32_t v[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t* line = ex + (2 * u + h) * kRows + lane;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[4 * h + j] = line[32 * j];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[8 + 4 * h + j] = j < 2 ? line[128 + 32 * j] : 0u;
+        }
+        if (!issued()) continue;
+        ptx::tc_fence_after();
+        const uint32_t to = c.tmem + ((uint32_t)((warp & 3) * 32) << 16) + kAccs<RT> * kAccCols + (ring.n % S) * kSfCols;
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+            "%15, %16};" ::"r"(to),
+            "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+            "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+            : "memory");
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&c.scaled[ring.n % S]);
+      }
+      buf ^= 1;
+    }
+    return true;
+  };
+  int id = blockIdx.x < share.total ? (int)blockIdx.x : -1;
+  while (id >= 0) {
+    share.passes(share.chunk(p, ls, id), pass);
+    if (!ptx::named_barrier_and(11, 128, issued())) return false;
+    id = c.chunk[ring.n % (2 * S)];
+  }
+  ++ring.n;  // the mark of the end
+  return true;
+}
+
+// The consumers' part in a routed share, whose warps take different roles for
+// coded weights.
+template <int RT, bool DOWN>
+__device__ bool consume_routed(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring, Ring& coded) {
+  if constexpr (RT == kFewBf16) {
+    return consume<RT, false, DOWN>(p, ls, sm, ring);
+  } else {
+    const int warp = threadIdx.x >> 5;
+    bool ok = true;
+    if (warp < 4) {
+      ok = drain<RT, DOWN>(p, ls, sm, coded);
+    } else if (warp < 8) {
+      if (RT == kFewMxfp4) {
+        coded.n = ring.n;
+        ok = bring_scales<DOWN>(p, ls, sm, coded);
+      }
+    } else if (warp == 8) {
+      coded.n = ring.n;
+      ok = issue_mmas<RT, DOWN>(p, ls, sm, coded);
+    }
+    return ok;
   }
 }
 
@@ -1084,57 +1194,10 @@ __device__ __forceinline__ void terms_of(float v, uint32_t (&t)[3]) {
   t[2] = __float_as_uint(q) >> 16;
 }
 
-// The power of two 2^(14 - e) for a largest magnitude of exponent e, as the factor
-// and its inverse; both normal numbers.
-__device__ __forceinline__ void fp16_factor(uint32_t top, float& factor, float& inverse) {
-  const uint32_t field = max(top >> 23, 15u);
-  factor = __uint_as_float((268u - field) << 23);
-  inverse = __uint_as_float((field - 14u) << 23);
-}
-
 // Bits of |v| where v is finite, 0 otherwise.
 __device__ __forceinline__ uint32_t finite_bits(float v) {
   const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
   return b < 0x7f800000u ? b : 0u;
-}
-
-__device__ __forceinline__ uint32_t fp16_pair(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ float fp16_lo(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)v)); }
-__device__ __forceinline__ float fp16_hi(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)(v >> 16))); }
-
-// x of this CTA's tokens in fp16, for the routed experts' codes.
-template <int WT>
-__device__ void fp16_tokens(const FewParams& p, uint32_t* red) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int t = gridDim.x - 1 - blockIdx.x; t < p.T; t += gridDim.x) {
-    const uint32_t* x = reinterpret_cast<const uint32_t*>(p.x + (int64_t)t * p.d * 2);
-    uint32_t top = 0;
-    for (int i = threadIdx.x; i < p.d / 2; i += kThreads) {
-      const uint32_t v = __ldg(x + i);
-      top = max(top, max(finite_bits(ptx::bf16_lo(v)), finite_bits(ptx::bf16_hi(v))));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) red[warp] = top;
-    consumer_sync();
-    top = red[lane & (kWarps - 1)];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float factor, inverse;
-    fp16_factor(top, factor, inverse);
-    if (threadIdx.x == 0) p.x_scale[t] = inverse;
-    uint16_t* to = reinterpret_cast<uint16_t*>(p.x16 + (int64_t)t * p.d * 2);
-    for (int i = threadIdx.x; i < p.d / 2; i += kThreads) {
-      const uint32_t v = __ldg(x + i);
-      store_pair<WT>(to, 2 * i, fp16_pair(ptx::bf16_lo(v) * factor, ptx::bf16_hi(v) * factor));
-    }
-    consumer_sync();
-  }
 }
 
 // Four values of h, columns k to k + 3, to a row's three bf16 terms [3][K].
@@ -1148,24 +1211,116 @@ __device__ __forceinline__ void store_terms(uint8_t* to, int K, int k, const flo
         make_uint2(t[0][q] | (t[1][q] << 16), t[2][q] | (t[3][q] << 16));
 }
 
-// The same as two fp16 terms [2][K]; the second of an infinity or NaN is none.
-template <int WT>
-__device__ __forceinline__ void store_terms16(uint8_t* to, int K, int k, const float (&h)[4], float factor) {
-  uint16_t* column = reinterpret_cast<uint16_t*>(to);
+// Two values as e4m3, the first in the low byte, and back as fp16.
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3_values(uint32_t pair) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)pair));
+  return r;
+}
+
+__device__ __forceinline__ float fp16_lo(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)v)); }
+__device__ __forceinline__ float fp16_hi(uint32_t v) { return __half2float(__ushort_as_half((uint16_t)(v >> 16))); }
+
+// A warp's 128 values, four a lane from step k on, of row `row` with K steps, as
+// e4m3 terms [row][kTermRows8][K] and the power of two that undoes their scaling.
+template <int N>
+__device__ __forceinline__ void store_e4m3_terms(uint8_t* terms, float* scale, int64_t row, int K, int k,
+                                                 const float (&value)[4]) {
+  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float a = h[2 * i] * factor, b = h[2 * i + 1] * factor;
-    const uint32_t first = fp16_pair(a, b);
-    const float ra = finite_bits(a) == (__float_as_uint(a) & 0x7fffffffu) ? a - fp16_lo(first) : 0.0f;
-    const float rb = finite_bits(b) == (__float_as_uint(b) & 0x7fffffffu) ? b - fp16_hi(first) : 0.0f;
-    store_pair<WT>(column, k + 2 * i, first);
-    store_pair<WT>(column + K, k + 2 * i, fp16_pair(ra, rb));
+  for (int i = 0; i < 4; ++i) top = max(top, finite_bits(value[i]));
+  top = __reduce_max_sync(0xffffffffu, top);
+  // 2^(7 - e) for a largest magnitude of exponent e, and its inverse: normal numbers
+  const uint32_t field = max(top >> 23, 8u);
+  const float factor = __uint_as_float((261u - field) << 23);
+  if ((threadIdx.x & 31) == 0) scale[row * (K / 128) + k / 128] = __uint_as_float((field - 7u) << 23);
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool finite = (__float_as_uint(value[i]) & 0x7f800000u) != 0x7f800000u;
+    v[i] = finite ? value[i] * factor : __uint_as_float(0x7fffffffu);
+  }
+  uint8_t* to = terms + row * kTermRows8 * K + k;
+#pragma unroll
+  for (int t = 0; t < N; ++t) {
+    const uint32_t q0 = e4m3_pair(v[0], v[1]), q1 = e4m3_pair(v[2], v[3]);
+    *reinterpret_cast<uint32_t*>(to + (int64_t)t * K) = q0 | (q1 << 16);
+    const uint32_t b0 = e4m3_values(q0), b1 = e4m3_values(q1);
+    v[0] = (v[0] - fp16_lo(b0)) * 16.0f;
+    v[1] = (v[1] - fp16_hi(b0)) * 16.0f;
+    v[2] = (v[2] - fp16_lo(b1)) * 16.0f;
+    v[3] = (v[3] - fp16_hi(b1)) * 16.0f;
+  }
+}
+
+// The same as MXFP4 terms, codes [row][kTermRows4][K / 2] and scale bytes
+// [row][kTermRows4][K / 32]: each term takes the scale of what is left of its block
+// (as moe_mx_quantise chooses one) and rounds that.
+__device__ __forceinline__ void store_mxfp4_terms(uint8_t* terms, uint8_t* scales, int64_t row, int K, int k,
+                                                  const float (&value)[4]) {
+  float v[4] = {value[0], value[1], value[2], value[3]};
+  uint8_t* codes = terms + row * kTermRows4 * (K / 2) + k / 2;
+  uint8_t* bytes = scales + row * kTermRows4 * (K / 32) + k / 32;
+#pragma unroll
+  for (int t = 0; t < kTerms4; ++t) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t field = top >> 23;
+    const uint32_t s = top >= 0x7f800000u ? 255u : top == 0 ? 127u : field > 2 ? field - 2 : 0u;
+    const float inverse = s == 255u ? 0.0f : __uint_as_float((254u - s) << 23);
+    const float unit = s == 0 ? __uint_as_float(1u << 22) : __uint_as_float(s << 23);
+    uint32_t q = 0;
+    float back[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t c, f;
+      asm("{\n\t.reg .b8 q;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %1, %2;\n\tcvt.u32.u8 %0, q;\n\t}"
+          : "=r"(c)
+          : "f"(v[2 * i + 1] * inverse), "f"(v[2 * i] * inverse));
+      asm("{\n\t.reg .b8 q;\n\tcvt.u8.u32 q, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, q;\n\t}" : "=r"(f) : "r"(c));
+      q |= c << (8 * i);
+      back[2 * i] = fp16_lo(f);
+      back[2 * i + 1] = fp16_hi(f);
+    }
+    if (s == 255u) q = 0;  // the scale is NaN: all of the block is, here and in all later terms
+    *reinterpret_cast<uint16_t*>(codes + (int64_t)t * (K / 2)) = (uint16_t)q;
+    if ((threadIdx.x & 7) == 0) bytes[(int64_t)t * (K / 32)] = (uint8_t)s;
+    if (s != 255u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fmaf(-back[i], unit, v[i]);
+    }
+  }
+}
+
+// The terms of x, 128 values a warp.
+template <int RT>
+__device__ void token_terms(const FewParams& p) {
+  const int lane = threadIdx.x & 31;
+  const int blocks = p.d / 128, jobs = p.T * blocks;
+  // from the last CTA on: the first ones have the logits
+  for (int job = (threadIdx.x >> 5) * gridDim.x + (gridDim.x - 1 - blockIdx.x); job < jobs; job += gridDim.x * kWarps) {
+    const int t = job / blocks, k = (job - t * blocks) * 128 + 4 * lane;
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p.x + ((int64_t)t * p.d + k) * 2));
+    const float x[4] = {ptx::bf16_lo(v.x), ptx::bf16_hi(v.x), ptx::bf16_lo(v.y), ptx::bf16_hi(v.y)};
+    if (RT == kFewE4m3)
+      store_e4m3_terms<kXTerms8>(p.x_terms, p.x_scale, t, p.d, k, x);
+    else
+      store_mxfp4_terms(p.x_terms, p.x_term_scales, t, p.d, k, x);
   }
 }
 
 // h of every row, four columns a lane and 128 a warp.
-template <int WT>
-__device__ void activations(const FewParams& p, const Lists& ls) {
+template <int RT>
+__device__ void activations(const FewParams& p) {
   const int lane = threadIdx.x & 31;
   const int warps = gridDim.x * kWarps;
   const int rows = p.T * p.k;
@@ -1176,27 +1331,20 @@ __device__ void activations(const FewParams& p, const Lists& ls) {
     const int j = shared ? job - rows * rb : job;
     const int blocks = shared ? sb : rb;
     const int row = j / blocks, block = j % blocks;
-    float f = 1.0f;
-    if (!shared && WT != kFewBf16) f = __ldcg(p.x_scale + ls.ent[row] / p.k);
     const float* buf = shared ? p.up_s : p.up_r;
     const int parts = shared ? p.split_up_s.parts : p.split_up_r.parts;
     const float4 g = sum_parts(buf + ((int64_t)(row * 2) * blocks + block) * parts * kFewCols, parts);
     const float4 u = sum_parts(buf + ((int64_t)(row * 2 + 1) * blocks + block) * parts * kFewCols, parts);
-    const float h[4] = {gated(g.x * f, u.x * f), gated(g.y * f, u.y * f), gated(g.z * f, u.z * f), gated(g.w * f, u.w * f)};
+    const float h[4] = {gated(g.x, u.x), gated(g.y, u.y), gated(g.z, u.z), gated(g.w, u.w)};
     const int k = block * kFewCols + 4 * lane;
-    if (shared) {
+    if (shared)
       store_terms(p.h_s + (int64_t)row * 3 * p.S * 2, p.S, k, h);
-    } else if constexpr (WT == kFewBf16) {
+    else if (RT == kFewBf16)
       store_terms(p.h_r + (int64_t)row * 3 * p.I * 2, p.I, k, h);
-    } else {
-      uint32_t top = max(max(finite_bits(h[0]), finite_bits(h[1])), max(finite_bits(h[2]), finite_bits(h[3])));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      float factor, inverse;
-      fp16_factor(top, factor, inverse);
-      if (lane == 0) p.h_scale[(int64_t)row * rb + block] = inverse;
-      store_terms16<WT>(p.h_r + (int64_t)row * 2 * p.I * 2, p.I, k, h, factor);
-    }
+    else if (RT == kFewE4m3)
+      store_e4m3_terms<kHTerms8>(p.h_r, p.h_scale, row, p.I, k, h);
+    else
+      store_mxfp4_terms(p.h_r, p.h_term_scales, row, p.I, k, h);
   }
 }
 
@@ -1244,36 +1392,49 @@ __global__ void __launch_bounds__(kAllThreads, 1)
   extern __shared__ uint8_t dyn[];
   __shared__ Lists ls;
   __shared__ Control ct;
+  constexpr int S = Cfg<RT>::kStages;
+  constexpr bool kCoded = Cfg<RT>::kCoded;
   Smem sm;
   sm.stages = align_1024(dyn);
-  sm.cols = sm.stages + kStages * kTileBytes;
-  sm.red = reinterpret_cast<float*>(sm.cols + 2 * kColBytes);
-  sm.c = &ct;
-  // the router's keys, and where it is done, the scales
+  sm.cols = sm.stages + S * Cfg<RT>::kStageBytes;
+  sm.red = reinterpret_cast<float*>(sm.cols + 2 * Cfg<RT>::kColBytes);
+  // the router's keys, and where it is done, scales on their way
   uint64_t* keys = reinterpret_cast<uint64_t*>(sm.red + 8 * kRedFloats);
-  sm.scales = reinterpret_cast<StageScales*>(keys);
+  sm.exchange = reinterpret_cast<uint32_t*>(keys);
+  sm.c = &ct;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < S; ++s) {
       ptx::mbar_init(&ct.full[s], 1);
+      // 8 consumer warps and the columns' warp, or, of a coded share's stage, that
+      // one for 8 and the MMAs
       ptx::mbar_init(&ct.empty[s], kWarps / 2 + 1);
       ptx::mbar_init(&ct.issued[s], 1);
-      ptx::mbar_init(&ct.issued[s + kStages], 1);
-      ptx::mbar_init(&ct.scaled[s], kRouterWarps);
+      ptx::mbar_init(&ct.issued[s + S], 1);
+      ptx::mbar_init(&ct.scaled[s], 128);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&ct.col_full[b], 1);
       ptx::mbar_init(&ct.col_empty[b], kWarps);
     }
+    for (int b = 0; b < 4; ++b) {
+      ptx::mbar_init(&ct.acc_full[b], 2);
+      ptx::mbar_init(&ct.acc_empty[b], 128);
+    }
     ptx::mbar_init(&ct.ready, 1);
-    ptx::mbar_init(&ct.started, 1);
     ptx::mbar_init(&ct.routed, 32 * kRouterWarps);
     ct.abort = 0u;
     ct.never = 0u;
     ptx::fence_barrier_init();
     ptx::fence_proxy_async();
   }
+  if (kCoded && warp == 8) {
+    ptx::tmem_alloc(&ct.tmem, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
   __syncthreads();
+  ptx::tc_fence_after();
   volatile uint32_t* abort = &ct.abort;
 
   if (warp == kWarps) {
@@ -1284,40 +1445,40 @@ __global__ void __launch_bounds__(kAllThreads, 1)
       if (p.S > 0) ptx::prefetch_tmap(&maps.shared[threadIdx.x & 31]);
     }
     bool ok = true;
-    if (p.S > 0) ok = produce<kFewBf16, true, false>(maps, p, ls, sm, ring, p.bar + 4);
+    if (p.S > 0) ok = produce<kFewBf16, RT, true, false>(maps, p, ls, sm, ring, p.bar + 4);
     if (ok && !warp_wait(&ct.routed, 0, abort)) {
       raise_status(p.status, abort, kStatusTimeout);
       ok = false;
     }
     ok = ok && __all_sync(0xffffffffu, *abort == 0);  // the router gave up: there are no lists
-    if ((threadIdx.x & 31) == 0) {
-      ct.first = ring.n;
-      ptx::mbar_arrive(&ct.started);
-    }
-    if (ok) ok = produce<RT, false, false>(maps, p, ls, sm, ring, p.bar + 5);
-    if (ok) ok = produce<RT, false, true>(maps, p, ls, sm, ring, p.bar + 6);
-    if (ok && p.S > 0) produce<kFewBf16, true, true>(maps, p, ls, sm, ring, p.bar + 7);
+    if (ok) ok = produce<RT, RT, false, false>(maps, p, ls, sm, ring, p.bar + 5);
+    if (ok) ok = produce<RT, RT, false, true>(maps, p, ls, sm, ring, p.bar + 6);
+    if (ok && p.S > 0) produce<kFewBf16, RT, true, true>(maps, p, ls, sm, ring, p.bar + 7);
     // every issued copy must land before the CTA may exit
     if ((threadIdx.x & 31) == 0)
-      for (int j = ring.n > kStages ? ring.n - kStages : 0; j < ring.n; ++j)
-        if (!ptx::wait_bounded(&ct.full[j % kStages], (j / kStages) & 1, &ct.never))
-          raise_status(p.status, abort, kStatusTimeout);
+      for (int j = ring.n > S ? ring.n - S : 0; j < ring.n; ++j)
+        if (!ptx::wait_bounded(&ct.full[j % S], (j / S) & 1, &ct.never)) raise_status(p.status, abort, kStatusTimeout);
   } else if (warp == kWarps + 1) {
     // ---------------------------------------------- columns
     Ring ring;
     bool ok = true;
     auto wait = [&](uint64_t* bar) {
       if (warp_wait(bar, 0, abort) && __all_sync(0xffffffffu, *abort == 0)) {
-        ptx::fence_proxy_async_all();  // x in fp16 and h were written by ordinary stores
+        ptx::fence_proxy_async_all();  // x's and h's terms were written by ordinary stores
         return true;
       }
       raise_status(p.status, abort, kStatusTimeout);
       return false;
     };
-    if (p.S > 0) ok = bring_columns<kFewBf16, true, false>(p, ls, sm, ring);
-    ok = ok && wait(&ct.routed) && bring_columns<RT, false, false>(p, ls, sm, ring);
-    ok = ok && wait(&ct.ready) && bring_columns<RT, false, true>(p, ls, sm, ring);
-    if (ok && p.S > 0) bring_columns<kFewBf16, true, true>(p, ls, sm, ring);
+    if (p.S > 0) ok = bring_columns<RT, true, false>(p, ls, sm, ring);
+    if constexpr (kCoded) {
+      ok = ok && wait(&ct.routed) && bring_terms<RT, false>(maps, p, ls, sm, ring);
+      ok = ok && wait(&ct.ready) && bring_terms<RT, true>(maps, p, ls, sm, ring);
+    } else {
+      ok = ok && wait(&ct.routed) && bring_columns<RT, false, false>(p, ls, sm, ring);
+      ok = ok && wait(&ct.ready) && bring_columns<RT, false, true>(p, ls, sm, ring);
+    }
+    if (ok && p.S > 0) bring_columns<RT, true, true>(p, ls, sm, ring);
     // every issued copy must land before the CTA may exit
     for (int j = ring.cols > 2 ? ring.cols - 2 : 0; j < ring.cols; ++j)
       if (!ptx::wait_bounded(&ct.col_full[j & 1], (j >> 1) & 1, &ct.never))
@@ -1328,57 +1489,64 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     router_sync();
     if (*abort == 0) route(p, ls, keys);
     ptx::mbar_arrive(&ct.routed);
-    if constexpr (RT != kFewBf16) {
-      auto wait = [&](uint64_t* bar) {
-        return warp_wait(bar, 0, abort) && __all_sync(0xffffffffu, *abort == 0);
-      };
-      // both warps are done with the keys, and the share has begun
-      Ring ring;
-      if (wait(&ct.routed) && wait(&ct.started)) {
-        ring.n = ct.first;
-        if (bring_scales<RT, false>(p, ls, sm, ring) && wait(&ct.ready)) bring_scales<RT, true>(p, ls, sm, ring);
-      }
-    }
   } else {
     // ---------------------------------------------- consumers
-    Ring ring;
+    Ring ring, coded;
     logits_share(p, reinterpret_cast<double*>(sm.red));
-    if (RT != kFewBf16) {
-      fp16_tokens<RT>(p, reinterpret_cast<uint32_t*>(sm.red));
-      ptx::fence_proxy_async_all();  // bulk copies will read them
+    if constexpr (kCoded) {
+      token_terms<RT>(p);
+      ptx::fence_proxy_async_all();  // TMA will read them
     }
     grid_arrive(p.bar + 0);
     bool ok = true;
-    if (p.S > 0) ok = consume<kFewBf16, true, false>(p, ls, sm, ring);
+    if (p.S > 0) ok = consume<RT, true, false>(p, ls, sm, ring);
     // all consumers agree on whether there are lists
     ok = ptx::named_barrier_and(9, kThreads, ok && ptx::wait_bounded(&ct.routed, 0, abort) && *abort == 0);
-    if (ok) ok = consume<RT, false, false>(p, ls, sm, ring);
+    if (ok) consume_routed<RT, false>(p, ls, sm, ring, coded);
     grid_arrive(p.bar + 1);
     if (grid_wait(p.bar + 1, p.status, abort)) {
-      activations<RT>(p, ls);
+      if (kCoded) ring.n = ct.position;
+      activations<RT>(p);
       ptx::fence_proxy_async_all();  // bulk copies will read h
       grid_arrive(p.bar + 2);
       if (grid_wait(p.bar + 2, p.status, abort)) {
         if (threadIdx.x == 0) ptx::mbar_arrive(&ct.ready);
-        if (consume<RT, false, true>(p, ls, sm, ring) && p.S > 0) consume<kFewBf16, true, true>(p, ls, sm, ring);
+        consume_routed<RT, true>(p, ls, sm, ring, coded);
+        if (p.S > 0) {
+          if (kCoded) {
+            // the ring's position is known to the warp that issued the MMAs
+            consumer_sync();
+            ring.n = ct.position;
+          }
+          if (*abort == 0) consume<RT, true, true>(p, ls, sm, ring);
+        }
         grid_arrive(p.bar + 3);
         if (grid_wait(p.bar + 3, p.status, abort)) combine(p, ls);
       }
+    }
+  }
+  if constexpr (kCoded) {
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+      ptx::tc_fence_after();
+      ptx::tmem_dealloc(ct.tmem, kTmemCols);
     }
   }
 }
 
 template <int RT>
 cudaError_t launch(const FewParams& p, const FewMaps& maps, int sms, cudaStream_t stream) {
-  // stages, the pairs' joins, the columns, a routing key and a logit per expert and router warp
-  const size_t smem = 1024 + kStages * kTileBytes + 2 * kColBytes + 8 * kRedFloats * 4 + 
-                      std::max((size_t)kRouterWarps * p.E * 12, kStages * sizeof(StageScales));
+  // stages, the columns, the pairs' joins; a routing key and a logit per expert and
+  // router warp, or two groups of 4 units' scales
+  const size_t smem = 1024 + Cfg<RT>::kStages * Cfg<RT>::kStageBytes + 2 * Cfg<RT>::kColBytes + 8 * kRedFloats * 4 +
+                      std::max<size_t>((size_t)kRouterWarps * p.E * 12, Cfg<RT>::kCoded ? 2 * 8 * (128 + 64) * 4 : 0);
   auto kernel = few_kernel<RT>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   void* args[] = {const_cast<FewParams*>(&p), const_cast<FewMaps*>(&maps)};
-  return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(sms),
-                                     dim3(kAllThreads), args, smem, stream);
+  return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(sms), dim3(kAllThreads), args, smem,
+                                     stream);
 }
 
 }  // namespace

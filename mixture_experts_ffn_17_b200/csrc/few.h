@@ -17,6 +17,9 @@ enum FewWeights : int { kFewBf16 = 0, kFewE4m3 = 1, kFewMxfp4 = 2 };
 // Steps of the contraction in a work unit: 16 KB of 128 columns' weights.
 constexpr int few_unit_steps(int weights) { return weights == kFewBf16 ? 64 : weights == kFewE4m3 ? 128 : 256; }
 
+// Rows that a row of x or h takes as terms: whole swizzle atoms of 8 rows.
+constexpr int few_term_rows(int weights) { return weights == kFewMxfp4 ? 16 : 8; }
+
 // How a segment's units are cut into chunks.
 struct FewSplit {
   int parts, units;  // chunks of a segment, units of a chunk (the last may have fewer)
@@ -57,19 +60,20 @@ struct FewParams {
   FewSplit split_up_r, split_up_s, split_dn_r, split_dn_s;
   float* logits;       // [T, E]
   float *up_r, *up_s, *dn_r, *dn_s;  // the chunks' sums, [row][segment][part][kFewCols]
-  uint8_t* h_r;        // [T * k][terms][I] terms of the routed rows' activations: three bf16 or two fp16
-  uint8_t* h_s;        // [T][3][S] bf16
-  // e4m3 and MXFP4 weights: x in fp16, and the powers of two that undo its and h's scaling
-  uint8_t* x16;        // [T, d]
-  float* x_scale;      // [T]
-  float* h_scale;      // [T * k][I / 128]
+  uint8_t* h_r;        // the routed rows' activations: [T * k][3][I] bf16 terms, or terms as x_terms
+  uint8_t* h_s;        // [T][3][S] bf16 terms
+  // coded weights: terms of x, [T][few_term_rows][d] e4m3 or [..][d / 2] MXFP4 codes
+  uint8_t* x_terms;
+  float *x_scale, *h_scale;                // e4m3: the power of two that undoes the scaling of 128 values
+  uint8_t *x_term_scales, *h_term_scales;  // MXFP4: [row][few_term_rows][K / 32]
 };
 
 // Tensor maps of W1, W3 and W2, all with the 128-byte swizzle.  bf16: [E, K, N]
 // in boxes of 64 steps by 64 columns; e4m3: [E, K, N] bytes in boxes of 128 by
-// 128; MXFP4: [E * N, K / 2] bytes in boxes of 128 columns by 256 steps.
+// 128; MXFP4: [E * N, K / 2] bytes in boxes of 128 columns by 256 steps.  Terms:
+// [rows, bytes of K] in boxes of few_term_rows by 128.
 struct FewMaps {
-  CUtensorMap routed[3], shared[3];
+  CUtensorMap routed[3], shared[3], x_terms, h_terms;
 };
 
 cudaError_t launch_few(const FewParams& p, const FewMaps& maps, int weights, int sms, cudaStream_t stream);

@@ -36,7 +36,7 @@ int few_weights(const moe_shape& s) {
 
 struct FewLayout {
   FewSplit split_up_r, split_up_s, split_dn_r, split_dn_s;
-  size_t logits, up_r, up_s, dn_r, dn_s, h_r, h_s, x16, x_scale, h_scale, total;
+  size_t logits, up_r, up_s, dn_r, dn_s, h_r, h_s, x_terms, x_scale, h_scale, x_term_scales, h_term_scales, total;
 };
 
 FewLayout few_layout(const moe_shape& s) {
@@ -60,11 +60,17 @@ FewLayout few_layout(const moe_shape& s) {
   L.up_s = take(sums(T * 2 * bs, L.split_up_s));
   L.dn_r = take(sums(rows * bd, L.split_dn_r));
   L.dn_s = take(s.shared_inter > 0 ? sums(T * bd, L.split_dn_s) : 0);
-  L.h_r = take((size_t)rows * 3 * s.inter * 2);
+  // bytes of a step in all of a row's terms
+  const int kind = few_weights(s);
+  const int64_t twice = kind == kFewBf16 ? 12 : few_term_rows(kind) * (kind == kFewE4m3 ? 2 : 1);
+  const bool coded = kind != kFewBf16;
+  L.h_r = take((size_t)(rows * s.inter * twice / 2));
   L.h_s = take((size_t)T * 3 * s.shared_inter * 2);
-  L.x16 = take((size_t)T * s.d * 2);
-  L.x_scale = take((size_t)T * 4);
-  L.h_scale = take((size_t)rows * bi * 4);
+  L.x_terms = take(coded ? (size_t)(T * s.d * twice / 2) : 0);
+  L.x_scale = take(kind == kFewE4m3 ? (size_t)T * bd * 4 : 0);
+  L.h_scale = take(kind == kFewE4m3 ? (size_t)rows * bi * 4 : 0);
+  L.x_term_scales = take(kind == kFewMxfp4 ? (size_t)T * few_term_rows(kind) * (s.d / kMxBlock) : 0);
+  L.h_term_scales = take(kind == kFewMxfp4 ? (size_t)rows * few_term_rows(kind) * (s.inter / kMxBlock) : 0);
   L.total = off;
   return L;
 }
@@ -229,9 +235,11 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.dn_s = at<float>(ws, L.dn_s);
   p.h_r = at<uint8_t>(ws, L.h_r);
   p.h_s = at<uint8_t>(ws, L.h_s);
-  p.x16 = at<uint8_t>(ws, L.x16);
+  p.x_terms = at<uint8_t>(ws, L.x_terms);
   p.x_scale = at<float>(ws, L.x_scale);
   p.h_scale = at<float>(ws, L.h_scale);
+  p.x_term_scales = at<uint8_t>(ws, L.x_term_scales);
+  p.h_term_scales = at<uint8_t>(ws, L.h_term_scales);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int weights = few_weights(s);
   FewMaps maps{};
@@ -245,6 +253,12 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
     if (!made) return MOE_ERR_CUDA;
     if (s.shared_inter > 0 && !map_bf16_tiles(&maps.shared[i], shared[i], i == 2 ? s.d : s.shared_inter,
                                               i == 2 ? s.shared_inter : s.d, 1))
+      return MOE_ERR_CUDA;
+  }
+  if (weights != kFewBf16) {
+    const int rows = few_term_rows(weights), per_byte = weights == kFewMxfp4 ? 2 : 1;
+    if (!map_bytes(&maps.x_terms, p.x_terms, s.d / per_byte, (uint64_t)s.T * rows, rows) ||
+        !map_bytes(&maps.h_terms, p.h_r, s.inter / per_byte, (uint64_t)s.T * s.k * rows, rows))
       return MOE_ERR_CUDA;
   }
   MOE_CUDA(cudaMemsetAsync(ws, 0, kAlign, st));
