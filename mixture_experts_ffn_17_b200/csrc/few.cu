@@ -96,7 +96,16 @@ constexpr int kRedFloats = 2 * kMaxCols * kRedPitch;  // of a pair of warps
 constexpr int kAccCols = 64;
 template <int RT>
 constexpr int kAccs = RT == kFewE4m3 ? 4 : 2;
+template <int RT>
+constexpr int kIssuers = RT == kFewE4m3 ? 2 : 1;  // threads that issue MMAs
 constexpr int kSfCols = 16;
+// e4m3: factors of a pass, [8 rows][32 units], for this many passes in turn.  When a
+// stage is filled the one before it in its place has been multiplied, so that the
+// accumulators up to kAccs stages before that are drained: the passes 11 before are
+// done with.
+constexpr int kFactors = 12;
+constexpr size_t kExchangeBytes = 2 * 8 * (128 + 64) * 4;  // two groups of 4 units' scales, or factors
+static_assert(kExchangeBytes >= kFactors * 256 * 4, "room for the factors");
 constexpr int kTmemCols = 256;
 
 struct Lists {  // what the routing leaves in shared memory
@@ -118,12 +127,12 @@ struct Control {
   // who has no part in a stage may still be looking at it when the stage's place
   // is filled again, but not when the place after it is
   uint64_t issued[2 * kMaxStages];
-  uint64_t scaled[kMaxStages];  // MXFP4: a stage's scales are in TMEM
+  uint64_t scaled[kFactors];    // MXFP4: a stage's scales are in TMEM; e4m3: a pass's factors are there
   uint64_t acc_full[4], acc_empty[4];
   uint64_t ready;   // h is there, in all CTAs
   uint64_t routed;  // the lists are there
   int chunk[2 * kMaxStages];  // which chunk a stage belongs to; -1: the share is done
-  int acc_chunk[4], acc_pass[4], acc_step[4];  // what an accumulator holds
+  int acc_chunk[4], acc_pass[4], acc_step[4];  // what an accumulator holds; a pass's first: step -1
   int position;  // stages handed over when a coded share ended
   uint32_t tmem, abort, never;
 };
@@ -354,7 +363,7 @@ struct Smem {
   uint8_t* stages;
   uint8_t* cols;
   float* red;
-  uint32_t* exchange;  // MXFP4: two groups of scales on their way from rows to lanes
+  uint32_t* exchange;  // MXFP4: two groups of scales on their way from rows to lanes; e4m3: factors
   Control* c;
 };
 
@@ -665,32 +674,34 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
-// Issues a share's MMAs (one warp; one lane issues).
+// Issues a share's MMAs.  A thread does all of it, since with a warp's other lanes
+// waiting beside each issue a stage took half as long again.  An MMA takes its
+// thread some 70 cycles, so e4m3's units, which have accumulators of their own,
+// are issued by two threads in turn.
 template <int RT, bool DOWN>
-__device__ bool issue_mmas(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
-  constexpr int S = Cfg<RT>::kStages, kA = kAccs<RT>;
-  const int lane = threadIdx.x & 31;
+__device__ bool issue_mmas(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring, int who) {
+  constexpr int S = Cfg<RT>::kStages, kA = kAccs<RT>, kI = kIssuers<RT>;
+  // the stage that was in a stage's place was this thread's too, so its barrier is
+  // never waited for a turn early
+  static_assert(S % kI == 0 && kA % kI == 0, "stages and accumulators of its own");
   Control& c = *sm.c;
   const uint32_t base = ptx::smem_u32(sm.stages);
   const uint64_t a_desc = ptx::sdesc_sw128(base, 16, 1024), b_desc = ptx::sdesc_sw128(base + kTileBytes, 16, 1024);
   const int K = DOWN ? p.I : p.d;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (warp_wait(bar, parity, &c.abort)) return true;
-    if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
+    if (ptx::wait_bounded(bar, parity, &c.abort)) return true;
+    raise_status(p.status, &c.abort, kStatusTimeout);
     return false;
   };
   // an accumulator is handed over when its MMAs are done and its labels are there
   auto take = [&] { return wait(&c.acc_empty[ring.accs % kA], ((ring.accs / kA) & 1) ^ 1); };
   auto hand_over = [&](int id, int pass, int step) {
-    if (lane == 0) {
-      const int b = ring.accs % kA;
-      ptx::mma_commit(&c.acc_full[b]);
-      c.acc_chunk[b] = id;
-      c.acc_pass[b] = pass;
-      c.acc_step[b] = step;
-      ptx::mbar_arrive(&c.acc_full[b]);
-    }
-    __syncwarp();
+    const int b = ring.accs % kA;
+    ptx::mma_commit(&c.acc_full[b]);
+    c.acc_chunk[b] = id;
+    c.acc_pass[b] = pass;
+    c.acc_step[b] = step;
+    ptx::mbar_arrive(&c.acc_full[b]);
     ++ring.accs;
   };
   const Share<RT, false, DOWN> share(p, ls);
@@ -704,6 +715,10 @@ __device__ bool issue_mmas(const FewParams& p, const Lists& ls, const Smem& sm, 
       const uint32_t id0 = RT == kFewE4m3 ? idesc_e4m3(N) : idesc_mxf4(N, 0), id1 = idesc_mxf4(N, 1);
       for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
         const int s = ring.n % S;
+        if (kI > 1 && ring.accs % kI != who) {
+          ++ring.accs;
+          continue;
+        }
         if ((RT == kFewE4m3 || step == q.step0) && !take()) return false;
         if (!wait(&c.full[s], (ring.n / S) & 1)) return false;
         if (RT == kFewMxfp4) {
@@ -712,44 +727,41 @@ __device__ bool issue_mmas(const FewParams& p, const Lists& ls, const Smem& sm, 
           ring.cols ^= 1 << s;
         }
         ptx::tc_fence_after();
-        if (lane == 0) {
-          const uint32_t off = s * (Cfg<RT>::kStageBytes >> 4);
-          const uint64_t a = a_desc + off, b = b_desc + off;
-          const uint32_t d = c.tmem + (ring.accs % kA) * kAccCols;
-          if (RT == kFewE4m3) {
-            // 32 steps: 32 rows of the tile, 32 bytes of a term's row
-            mma_e4m3(d, a, b, id0, 0u);
-            mma_e4m3(d, a + (4096 >> 4), b + 2, id0, 1u);
-            mma_e4m3(d, a + (8192 >> 4), b + 4, id0, 1u);
-            mma_e4m3(d, a + (12288 >> 4), b + 6, id0, 1u);
-          } else {
-            const uint32_t sf = c.tmem + kA * kAccCols + s * kSfCols;
-            mma_mxf4(d, a, b, id0, sf, sf + 8, step != q.step0 ? 1u : 0u);
-            mma_mxf4(d, a + 2, b + 2, id1, sf, sf + 8, 1u);
-            if (K - step * 256 > 128) {  // else the last unit is half of one
-              mma_mxf4(d, a + 4, b + 4, id0, sf + 4, sf + 12, 1u);
-              mma_mxf4(d, a + 6, b + 6, id1, sf + 4, sf + 12, 1u);
-            }
+        const uint32_t off = s * (Cfg<RT>::kStageBytes >> 4);
+        const uint64_t a = a_desc + off, b = b_desc + off;
+        const uint32_t d = c.tmem + (ring.accs % kA) * kAccCols;
+        if (RT == kFewE4m3) {
+          // 32 steps: 32 rows of the tile, 32 bytes of a term's row
+          mma_e4m3(d, a, b, id0, 0u);
+          mma_e4m3(d, a + (4096 >> 4), b + 2, id0, 1u);
+          mma_e4m3(d, a + (8192 >> 4), b + 4, id0, 1u);
+          mma_e4m3(d, a + (12288 >> 4), b + 6, id0, 1u);
+        } else {
+          const uint32_t sf = c.tmem + kA * kAccCols + s * kSfCols;
+          mma_mxf4(d, a, b, id0, sf, sf + 8, step != q.step0 ? 1u : 0u);
+          mma_mxf4(d, a + 2, b + 2, id1, sf, sf + 8, 1u);
+          if (K - step * 256 > 128) {  // else the last unit is half of one
+            mma_mxf4(d, a + 4, b + 4, id0, sf + 4, sf + 12, 1u);
+            mma_mxf4(d, a + 6, b + 6, id1, sf + 4, sf + 12, 1u);
           }
-          ptx::mma_commit(&c.empty[s]);
         }
-        __syncwarp();
-        if (RT == kFewE4m3) hand_over(id, pass, step);
+        ptx::mma_commit(&c.empty[s]);
+        if (RT == kFewE4m3) hand_over(id, pass, step == q.step0 ? -1 : step - q.step0);
       }
-      if (RT == kFewMxfp4) hand_over(id, pass, q.step1 - 1);
+      if (RT == kFewMxfp4) hand_over(id, pass, -1);
       ++pass;
       return true;
     });
     if (!ok) return false;
   }
+  if (kI > 1 && ring.accs % kI != who) {
+    ++ring.accs;
+    return true;
+  }
   if (!take()) return false;
   hand_over(-1, 0, 0);
-  if (lane == 0) {
-    ptx::mbar_arrive(&c.empty[ring.n % S]);
-    c.position = ring.n + 1;
-  }
-  __syncwarp();
-  ++ring.n;
+  ptx::mbar_arrive(&c.empty[ring.n % S]);
+  c.position = ring.n + 1;
   return true;
 }
 
@@ -770,16 +782,18 @@ __device__ bool drain(const FewParams& p, const Lists& ls, const Smem& sm, Ring&
   const int col = threadIdx.x & 127;
   Control& c = *sm.c;
   const Share<RT, false, DOWN> share(p, ls);
-  float sums[8];     // e4m3: of each row
-  float factor[8];   // e4m3: lane l has unit l's, for each row, of the chunk
+  float sums[8];  // e4m3: of each row
+  Piece q = {};
   while (true) {
     const int b = ring.accs % kA;
-    if (!warp_wait(&c.acc_full[b], (ring.accs / kA) & 1, &c.abort)) {
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (warp_wait(bar, parity, &c.abort)) return true;
       if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
       return false;
-    }
+    };
+    if (!wait(&c.acc_full[b], (ring.accs / kA) & 1)) return false;
     ptx::tc_fence_after();
-    const int id = c.acc_chunk[b], pass = c.acc_pass[b], step = c.acc_step[b];
+    const int id = c.acc_chunk[b], step = c.acc_step[b];
     auto release = [&] {
       ptx::tc_fence_before();
       ptx::mbar_arrive(&c.acc_empty[b]);
@@ -789,8 +803,10 @@ __device__ bool drain(const FewParams& p, const Lists& ls, const Smem& sm, Ring&
       release();
       return true;
     }
-    Piece q = share.chunk(p, ls, id);
-    share.cut(q, q.rows, pass * share.kPass);
+    if (step < 0) {  // the pass's first
+      q = share.chunk(p, ls, id);
+      share.cut(q, q.rows, c.acc_pass[b] * share.kPass);
+    }
     const uint32_t acc = c.tmem + ((uint32_t)((warp & 3) * 32) << 16) + b * kAccCols;
     if constexpr (RT == kFewMxfp4) {
       for (int r = 0; r < q.rows; ++r) {
@@ -804,21 +820,14 @@ __device__ bool drain(const FewParams& p, const Lists& ls, const Smem& sm, Ring&
       }
       release();
     } else {
-      if (step == q.step0) {
-        // the block's scale times the row's factor, unit step0 + lane's
-        const int unit = min(step + lane, share.steps - 1);
-        const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
-        const float f = __ldg(reinterpret_cast<const float*>(scales) +
-                              ((int64_t)q.expert * share.steps + unit) * share.blocks + q.col0 / 128);
+      const int slot = ring.cols % kFactors;
+      const float* factors = reinterpret_cast<const float*>(sm.exchange) + slot * 256;
+      int unit = step;
+      if (step < 0) {
+        if (!wait(&c.scaled[slot], (ring.cols / kFactors) & 1)) return false;
+        unit = 0;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          sums[r] = 0.0f;
-          factor[r] = 0.0f;
-          if (r < q.rows) {
-            const int row = DOWN ? q.first + r : ls.ent[q.first + r] / p.k;
-            factor[r] = f * __ldcg((DOWN ? p.h_scale : p.x_scale) + (int64_t)row * share.steps + unit);
-          }
-        }
+        for (int r = 0; r < 8; ++r) sums[r] = 0.0f;
       }
 #pragma unroll
       for (int r = 0; r < 8; r += 2) {
@@ -831,18 +840,63 @@ __device__ bool drain(const FewParams& p, const Lists& ls, const Smem& sm, Ring&
             float a = 0.0f;
 #pragma unroll
             for (int t = kT - 1; t >= 0; --t) a = fmaf(a, 0.0625f, v[8 * i + t]);
-            sums[r + i] = fmaf(a, __shfl_sync(0xffffffffu, factor[r + i], step - q.step0), sums[r + i]);
+            sums[r + i] = fmaf(a, factors[(r + i) * 32 + unit], sums[r + i]);
           }
         }
       }
       release();
-      if (step == q.step1 - 1) {
+      if (unit == q.step1 - q.step0 - 1) {
 #pragma unroll
         for (int r = 0; r < 8; ++r)
           if (r < q.rows) q.out[r * q.ld + col] = sums[r];
+        ++ring.cols;
       }
     }
   }
+}
+
+// e4m3: the factors of a share's passes (one warp, a lane per unit): the scale of a
+// block of weights times the power of two that undoes the scaling of a row's terms.
+template <bool DOWN>
+__device__ bool bring_factors(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
+  constexpr int RT = kFewE4m3;
+  const int lane = threadIdx.x & 31;
+  Control& c = *sm.c;
+  const Share<RT, false, DOWN> share(p, ls);
+  auto issued = [&] {
+    if (wait_issued<RT>(c, ring.n)) return true;
+    if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
+    return false;
+  };
+  const bool ok = follow_chunks<RT, RT, false, DOWN>(p, ls, sm, ring, [&](const Piece& q) {
+    const int unit = min(q.step0 + lane, share.steps - 1);
+    const uint8_t* scales = q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2;
+    const float f = __ldg(reinterpret_cast<const float*>(scales) +
+                          ((int64_t)q.expert * share.steps + unit) * share.blocks + q.col0 / 128);
+    float v[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      v[r] = 0.0f;
+      if (r < q.rows) {
+        const int row = DOWN ? q.first + r : ls.ent[q.first + r] / p.k;
+        v[r] = __ldcg((DOWN ? p.h_scale : p.x_scale) + (int64_t)row * share.steps + unit);
+      }
+    }
+    if (!issued()) return false;  // the place is free once the pass's first stage is on its way
+    const int slot = ring.cols % kFactors;
+    float* to = reinterpret_cast<float*>(sm.exchange) + slot * 256 + lane;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) to[r * 32] = f * v[r];
+    ptx::mbar_arrive(&c.scaled[slot]);
+    ++ring.cols;
+    // every stage is waited for: a barrier can be read one turn of the ring late
+    // or early, not two
+    for (int step = q.step0; step < q.step1; ++step, ++ring.n)
+      if (!issued()) return false;
+    return true;
+  });
+  ++ring.n;  // the mark of the end
+  return ok;
 }
 
 // MXFP4: a share's scales to TMEM (four warps), row r of 128 in lane r % 32 of
@@ -877,21 +931,38 @@ __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm
       const int row = DOWN ? q.first + r / kTermRows4 : ls.ent[q.first + r / kTermRows4] / p.k;
       x = reinterpret_cast<const uint32_t*>(terms) + ((int64_t)row * kTermRows4 + r % kTermRows4) * words;
     }
-    for (int step0 = q.step0; step0 < q.step1; step0 += kGroup) {
-      uint32_t a[2 * kGroup], t[2 * kGroup];
+    uint32_t a[2 * kGroup], t[2 * kGroup];
+    const bool wide = words % 4 == 0 && q.step0 % 2 == 0;
+    auto load = [&](int step0) {
+      if (wide) {
+#pragma unroll
+        for (int i = 0; i < 2 * kGroup; i += 4) {
+          const bool have = 2 * step0 + i < words && step0 < q.step1;
+          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+          const uint4 y = have ? __ldg(reinterpret_cast<const uint4*>(w + 2 * step0 + i)) : zero;
+          const uint4 z = have && x ? __ldcg(reinterpret_cast<const uint4*>(x + 2 * step0 + i)) : zero;
+          a[i] = y.x, a[i + 1] = y.y, a[i + 2] = y.z, a[i + 3] = y.w;
+          t[i] = z.x, t[i + 1] = z.y, t[i + 2] = z.z, t[i + 3] = z.w;
+        }
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < 2 * kGroup; ++i) {
         const int at = 2 * step0 + i;
-        const bool have = at < words && step0 + i / 2 < q.step1;
+        const bool have = at < words && step0 < q.step1;
         a[i] = have ? __ldg(w + at) : 0u;
         t[i] = have && x ? __ldcg(x + at) : 0u;
       }
+    };
+    load(q.step0);
+    for (int step0 = q.step0; step0 < q.step1; step0 += kGroup) {
       uint32_t* ex = sm.exchange + buf * (2 * kGroup * kRows);
 #pragma unroll
       for (int i = 0; i < 2 * kGroup; ++i) {
         ex[i * kRows + r] = a[i];
         if (r < 64) ex[i * kRows + 128 + r] = t[i];
       }
+      load(step0 + kGroup);  // the next group's are on their way meanwhile
       ptx::named_barrier(11, 128);
       for (int u = 0; u < kGroup && step0 + u < q.step1; ++u, ++ring.n) {
         uint32_t v[16];
@@ -945,10 +1016,14 @@ __device__ bool consume_routed(const FewParams& p, const Lists& ls, const Smem& 
       if (RT == kFewMxfp4) {
         coded.n = ring.n;
         ok = bring_scales<DOWN>(p, ls, sm, coded);
+      } else if (warp == 4) {
+        coded.n = ring.n;
+        ok = bring_factors<DOWN>(p, ls, sm, coded);
       }
-    } else if (warp == 8) {
+    } else if (warp < 8 + kIssuers<RT>) {
       coded.n = ring.n;
-      ok = issue_mmas<RT, DOWN>(p, ls, sm, coded);
+      if ((threadIdx.x & 31) == 0) ok = issue_mmas<RT, DOWN>(p, ls, sm, coded, warp - 8);
+      __syncwarp();
     }
     return ok;
   }
@@ -1404,6 +1479,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
   sm.c = &ct;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
+    for (int s = 0; s < kFactors; ++s) ptx::mbar_init(&ct.scaled[s], RT == kFewE4m3 ? 32 : 128);
     for (int s = 0; s < S; ++s) {
       ptx::mbar_init(&ct.full[s], 1);
       // 8 consumer warps and the columns' warp, or, of a coded share's stage, that
@@ -1411,7 +1487,6 @@ __global__ void __launch_bounds__(kAllThreads, 1)
       ptx::mbar_init(&ct.empty[s], kWarps / 2 + 1);
       ptx::mbar_init(&ct.issued[s], 1);
       ptx::mbar_init(&ct.issued[s + S], 1);
-      ptx::mbar_init(&ct.scaled[s], 128);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&ct.col_full[b], 1);
@@ -1538,9 +1613,9 @@ __global__ void __launch_bounds__(kAllThreads, 1)
 template <int RT>
 cudaError_t launch(const FewParams& p, const FewMaps& maps, int sms, cudaStream_t stream) {
   // stages, the columns, the pairs' joins; a routing key and a logit per expert and
-  // router warp, or two groups of 4 units' scales
+  // router warp, or the scales' exchange
   const size_t smem = 1024 + Cfg<RT>::kStages * Cfg<RT>::kStageBytes + 2 * Cfg<RT>::kColBytes + 8 * kRedFloats * 4 +
-                      std::max<size_t>((size_t)kRouterWarps * p.E * 12, Cfg<RT>::kCoded ? 2 * 8 * (128 + 64) * 4 : 0);
+                      std::max<size_t>((size_t)kRouterWarps * p.E * 12, Cfg<RT>::kCoded ? kExchangeBytes : 0);
   auto kernel = few_kernel<RT>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;

@@ -29,7 +29,8 @@ struct FewSplit {
 // so that CTAs that are ahead take more of them, of 8 to 32 units (a chunk's end
 // costs about one unit's time), and a chunk a CTA where there is less work.
 // Made for 148 CTAs whatever the device, so that results do not depend on it.
-inline FewSplit few_split(int64_t segs, int steps) {
+// Chunks start at multiples of `whole` units.
+inline FewSplit few_split(int64_t segs, int steps, int whole) {
   constexpr int64_t kCtas = 148;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
   if (segs < 1 || steps < 1) return FewSplit{1, 1};  // nothing to cut
@@ -38,8 +39,8 @@ inline FewSplit few_split(int64_t segs, int steps) {
   if (units < 8) units = least < 8 ? least : 8;
   if (units > 32) units = 32;
   if (units > steps) units = steps;
-  const int64_t parts = up(steps, units);
-  return FewSplit{(int)parts, (int)up(steps, parts)};
+  units = up(up(steps, up(steps, units)), whole) * whole;
+  return FewSplit{(int)up(steps, units), (int)units};
 }
 
 struct FewParams {

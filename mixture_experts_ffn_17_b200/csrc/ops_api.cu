@@ -44,10 +44,11 @@ FewLayout few_layout(const moe_shape& s) {
   const int64_t T = s.T, rows = T * s.k, experts = std::min<int64_t>(s.E, rows);
   const int unit = few_unit_steps(few_weights(s)), unit_s = few_unit_steps(kFewBf16);
   const int64_t bi = s.inter / kFewCols, bs = s.shared_inter / kFewCols, bd = s.d / kFewCols;
-  L.split_up_r = few_split(experts * 2 * bi, (s.d + unit - 1) / unit);
-  L.split_up_s = few_split(2 * bs, s.d / unit_s);
-  L.split_dn_r = few_split(experts * bd, (s.inter + unit - 1) / unit);
-  L.split_dn_s = few_split(bd, s.shared_inter / unit_s);
+  const int whole = few_weights(s) == kFewMxfp4 ? 2 : 1;  // chunks' scales on 16-byte boundaries
+  L.split_up_r = few_split(experts * 2 * bi, (s.d + unit - 1) / unit, whole);
+  L.split_up_s = few_split(2 * bs, s.d / unit_s, 1);
+  L.split_dn_r = few_split(experts * bd, (s.inter + unit - 1) / unit, whole);
+  L.split_dn_s = few_split(bd, s.shared_inter / unit_s, 1);
   size_t off = kAlign;  // the status word and the counters
   auto take = [&](size_t bytes) {
     const size_t here = off;
