@@ -115,7 +115,6 @@ struct Lists {  // what the routing leaves in shared memory
   int16_t row_of[kMaxRows];   // the inverse
   int16_t expert[kMaxRows];   // distinct experts, ascending
   int16_t start[kMaxRows + 1];
-  int16_t place[kMaxExperts];  // of an expert among the distinct ones
   int32_t counts[kMaxExperts];
   int n;                      // distinct experts
 };
@@ -150,13 +149,14 @@ __device__ __forceinline__ void grid_arrive(uint32_t* bar) {
   }
 }
 
-// One thread's wait for all CTAs' arrivals.
-__device__ __forceinline__ bool grid_poll(const uint32_t* bar, uint32_t* status, volatile uint32_t* abort) {
+// One thread's wait for `count` CTAs' arrivals.
+__device__ __forceinline__ bool grid_poll(const uint32_t* bar, uint32_t count, uint32_t* status,
+                                          volatile uint32_t* abort) {
   const uint64_t t0 = ptx::globaltimer();
   uint32_t n = 0, seen;
   while (true) {
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(bar) : "memory");
-    if (seen >= gridDim.x) break;
+    if (seen >= count) break;
     if ((++n & 63u) == 0) {
       if (*abort) return false;
       if (ptx::globaltimer() - t0 > kWaitLimitNs) {
@@ -169,32 +169,19 @@ __device__ __forceinline__ bool grid_poll(const uint32_t* bar, uint32_t* status,
   return true;
 }
 
+// All consumers' wait: they go on, or none of them.
 __device__ bool grid_wait(const uint32_t* bar, uint32_t* status, volatile uint32_t* abort) {
-  if (threadIdx.x == 0) grid_poll(bar, status, abort);
-  consumer_sync();
-  return *abort == 0;
+  if (threadIdx.x == 0) grid_poll(bar, gridDim.x, status, abort);
+  return ptx::named_barrier_and(9, kThreads, *abort == 0);
 }
 
-// Sum of a segment's chunks in order, four columns a lane, eight loads at a time.
-__device__ __forceinline__ float4 sum_parts(const float* at, int parts) {
-  const float4* v = reinterpret_cast<const float4*>(at) + (threadIdx.x & 31);
-  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int i = 0; i < parts; i += 8) {
-    float4 b[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (i + j < parts) b[j] = __ldcg(v + (i + j) * (kFewCols / 4));
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (i + j < parts) {
-        a.x += b[j].x;
-        a.y += b[j].y;
-        a.z += b[j].z;
-        a.w += b[j].w;
-      }
-    }
-  }
-  return a;
+// The code between the products runs once or twice a call and is not in any cache
+// then: it is kept short, and its loads in batches.
+__device__ __forceinline__ void add(float4& a, const float4& b) {
+  a.x += b.x;
+  a.y += b.y;
+  a.z += b.z;
+  a.w += b.w;
 }
 
 // ------------------------------------------------------------ tiles and columns
@@ -1194,16 +1181,40 @@ __device__ void choose(const FewParams& p, Lists& ls, int t, uint64_t* key, floa
 }
 
 // Routing of all tokens and the lists of chosen experts and their rows, by the
-// router's warps.
-__device__ void route(const FewParams& p, Lists& ls, uint64_t* keys) {
+// router's warps.  With more tokens than these the first CTAs choose, two tokens
+// each, and tell the others: a token takes a warp some 2.5 us, a barrier 2.
+__device__ void route(const FewParams& p, Lists& ls, uint64_t* keys, volatile uint32_t* abort) {
   constexpr int kThreads = 32 * kRouterWarps;
   const int tid = threadIdx.x - kAllThreads + kThreads;
   const int warp = tid >> 5, lane = tid & 31;
   for (int e = tid; e < p.E; e += kThreads) ls.counts[e] = 0;
-  for (int t = warp; t < p.T; t += kRouterWarps)
-    choose(p, ls, t, keys + warp * p.E, reinterpret_cast<float*>(keys + kRouterWarps * p.E) + warp * p.E);
-  router_sync();
   const int n = p.T * p.k;
+  const bool apart = p.T > kRouterWarps;
+  const int choosers = min((int)gridDim.x, (p.T + kRouterWarps - 1) / kRouterWarps);
+  const int end = apart && blockIdx.x >= choosers ? 0 : p.T;
+  for (int t = (apart ? blockIdx.x * kRouterWarps : 0) + warp; t < end; t += (apart ? choosers : 1) * kRouterWarps) {
+    choose(p, ls, t, keys + warp * p.E, reinterpret_cast<float*>(keys + kRouterWarps * p.E) + warp * p.E);
+    if (apart && lane < p.k) {
+      p.chosen[t * p.k + lane] = ls.idx[t * p.k + lane];
+      p.chosen_w[t * p.k + lane] = ls.w[t * p.k + lane];
+    }
+  }
+  router_sync();
+  if (apart) {
+    if (tid == 0) {
+      if (blockIdx.x < choosers) {
+        __threadfence();
+        atomicAdd(p.bar + 9, 1u);
+      }
+      grid_poll(p.bar + 9, choosers, p.status, abort);
+    }
+    if (!ptx::named_barrier_and(10, kThreads, *abort == 0)) return;
+    for (int i = tid; i < n; i += kThreads) {
+      ls.idx[i] = __ldcg(p.chosen + i);
+      ls.w[i] = __ldcg(p.chosen_w + i);
+    }
+    router_sync();
+  }
   for (int i = tid; i < n; i += kThreads) atomicAdd(&ls.counts[ls.idx[i]], 1);
   router_sync();
   if (warp == 0) {
@@ -1218,11 +1229,12 @@ __device__ void route(const FewParams& p, Lists& ls, uint64_t* keys) {
         if (lane >= o) before += v;
       }
       const int total = __shfl_sync(0xffffffffu, before, 31);
+      uint32_t* filled = reinterpret_cast<uint32_t*>(keys);  // the keys are done with
       if (cnt > 0) {
+        filled[e0 + lane] = rows + before - cnt;
         const int at = chosen + __popc(any & ((1u << lane) - 1u));
         ls.expert[at] = (int16_t)(e0 + lane);
         ls.start[at] = (int16_t)(rows + before - cnt);
-        ls.place[e0 + lane] = (int16_t)at;
       }
       chosen += __popc(any);
       rows += total;
@@ -1232,13 +1244,22 @@ __device__ void route(const FewParams& p, Lists& ls, uint64_t* keys) {
       ls.n = chosen;
     }
   }
-  router_sync();
-  for (int i = tid; i < n; i += kThreads) {
-    const int e = ls.idx[i];
-    int at = ls.start[ls.place[e]];
-    for (int q = 0; q < i; ++q) at += ls.idx[q] == e ? 1 : 0;
-    ls.ent[at] = (int16_t)i;
-    ls.row_of[i] = (int16_t)at;
+  if (warp == 0) {
+    // rows of an expert in the entries' order
+    volatile uint32_t* filled = reinterpret_cast<uint32_t*>(keys);
+    __syncwarp();
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane, e = i < n ? ls.idx[i] : -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, e);
+      if (e >= 0) {
+        const int at = filled[e] + __popc(same & ((1u << lane) - 1u));
+        ls.ent[at] = (int16_t)i;
+        ls.row_of[i] = (int16_t)at;
+      }
+      __syncwarp();
+      if (e >= 0 && (same >> lane) == 1u) filled[e] += __popc(same);
+      __syncwarp();
+    }
   }
   if (blockIdx.x == 0) {
     for (int i = tid; i < n; i += kThreads) {
@@ -1322,7 +1343,7 @@ __device__ __forceinline__ void store_e4m3_terms(uint8_t* terms, float* scale, i
     v[i] = finite ? value[i] * factor : __uint_as_float(0x7fffffffu);
   }
   uint8_t* to = terms + row * kTermRows8 * K + k;
-#pragma unroll
+#pragma unroll 1  // code that runs once a call costs its fetch: unrolled, h took twice as long
   for (int t = 0; t < N; ++t) {
     const uint32_t q0 = e4m3_pair(v[0], v[1]), q1 = e4m3_pair(v[2], v[3]);
     *reinterpret_cast<uint32_t*>(to + (int64_t)t * K) = q0 | (q1 << 16);
@@ -1342,7 +1363,7 @@ __device__ __forceinline__ void store_mxfp4_terms(uint8_t* terms, uint8_t* scale
   float v[4] = {value[0], value[1], value[2], value[3]};
   uint8_t* codes = terms + row * kTermRows4 * (K / 2) + k / 2;
   uint8_t* bytes = scales + row * kTermRows4 * (K / 32) + k / 32;
-#pragma unroll
+#pragma unroll 1
   for (int t = 0; t < kTerms4; ++t) {
     uint32_t top = 0;
 #pragma unroll
@@ -1376,13 +1397,13 @@ __device__ __forceinline__ void store_mxfp4_terms(uint8_t* terms, uint8_t* scale
   }
 }
 
-// The terms of x, 128 values a warp.
+// The terms of x, 128 values a warp, by the routers' warps of all CTAs.
 template <int RT>
 __device__ void token_terms(const FewParams& p) {
   const int lane = threadIdx.x & 31;
   const int blocks = p.d / 128, jobs = p.T * blocks;
-  // from the last CTA on: the first ones have the logits
-  for (int job = (threadIdx.x >> 5) * gridDim.x + (gridDim.x - 1 - blockIdx.x); job < jobs; job += gridDim.x * kWarps) {
+  const int warp = (threadIdx.x >> 5) - (kAllThreads / 32 - kRouterWarps);
+  for (int job = warp * gridDim.x + blockIdx.x; job < jobs; job += gridDim.x * kRouterWarps) {
     const int t = job / blocks, k = (job - t * blocks) * 128 + 4 * lane;
     const uint2 v = __ldg(reinterpret_cast<const uint2*>(p.x + ((int64_t)t * p.d + k) * 2));
     const float x[4] = {ptx::bf16_lo(v.x), ptx::bf16_hi(v.x), ptx::bf16_lo(v.y), ptx::bf16_hi(v.y)};
@@ -1408,8 +1429,15 @@ __device__ void activations(const FewParams& p) {
     const int row = j / blocks, block = j % blocks;
     const float* buf = shared ? p.up_s : p.up_r;
     const int parts = shared ? p.split_up_s.parts : p.split_up_r.parts;
-    const float4 g = sum_parts(buf + ((int64_t)(row * 2) * blocks + block) * parts * kFewCols, parts);
-    const float4 u = sum_parts(buf + ((int64_t)(row * 2 + 1) * blocks + block) * parts * kFewCols, parts);
+    // sums of the segments' chunks in order, four columns a lane
+    float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = g;
+    const float* from = buf + ((int64_t)(row * 2) * blocks + block) * parts * kFewCols + 4 * lane;
+    const int64_t second = (int64_t)blocks * parts * kFewCols;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i, from += kFewCols) {
+      add(g, __ldcg(reinterpret_cast<const float4*>(from)));
+      add(u, __ldcg(reinterpret_cast<const float4*>(from + second)));
+    }
     const float h[4] = {gated(g.x, u.x), gated(g.y, u.y), gated(g.z, u.z), gated(g.w, u.w)};
     const int k = block * kFewCols + 4 * lane;
     if (shared)
@@ -1423,7 +1451,7 @@ __device__ void activations(const FewParams& p) {
   }
 }
 
-// y: routed rows in slot order, then the shared expert's.
+// y: routed rows' chunks in order, slots inside, then the shared expert's.
 __device__ void combine(const FewParams& p, const Lists& ls) {
   const int lane = threadIdx.x & 31;
   const int warps = gridDim.x * kWarps;
@@ -1432,24 +1460,42 @@ __device__ void combine(const FewParams& p, const Lists& ls) {
   for (int job = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; job < jobs; job += warps) {
     const int t = job / blocks, block = job % blocks;
     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int j = 0; j < p.k; ++j) {
-      const int i = t * p.k + j;
-      const float w = ls.w[i];
-      const int parts = p.split_dn_r.parts;
-      const float4 o = sum_parts(p.dn_r + ((int64_t)ls.row_of[i] * blocks + block) * parts * kFewCols, parts);
-      y.x = fmaf(w, o.x, y.x);
-      y.y = fmaf(w, o.y, y.y);
-      y.z = fmaf(w, o.z, y.z);
-      y.w = fmaf(w, o.w, y.w);
+    const int parts = p.split_dn_r.parts;
+#pragma unroll 1
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+      const float* from[8];
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = t * p.k + min(j0 + j, p.k - 1);
+        from[j] = p.dn_r + ((int64_t)ls.row_of[i] * blocks + block) * parts * kFewCols + 4 * lane;
+        w[j] = ls.w[i];
+      }
+      const int n = p.k - j0;
+#pragma unroll 1
+      for (int i = 0; i < parts; ++i) {
+        float4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < n) v[j] = __ldcg(reinterpret_cast<const float4*>(from[j] + i * kFewCols));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j < n) {
+            y.x = fmaf(w[j], v[j].x, y.x);
+            y.y = fmaf(w[j], v[j].y, y.y);
+            y.z = fmaf(w[j], v[j].z, y.z);
+            y.w = fmaf(w[j], v[j].w, y.w);
+          }
+        }
+      }
     }
     if (p.S > 0) {
-      const int parts = p.split_dn_s.parts;
-      const float4 o = sum_parts(p.dn_s + ((int64_t)t * blocks + block) * parts * kFewCols, parts);
-      y.x += o.x;
-      y.y += o.y;
-      y.z += o.z;
-      y.w += o.w;
+      const int own = p.split_dn_s.parts;
+      const float* from = p.dn_s + ((int64_t)t * blocks + block) * own * kFewCols + 4 * lane;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int i = 0; i < own; ++i) add(o, __ldcg(reinterpret_cast<const float4*>(from + i * kFewCols)));
+      add(y, o);
     }
     const int64_t at = (int64_t)t * p.d + block * kFewCols + 4 * lane;
     if (p.y_bf16)
@@ -1560,18 +1606,25 @@ __global__ void __launch_bounds__(kAllThreads, 1)
         raise_status(p.status, abort, kStatusTimeout);
   } else if (warp > kWarps) {
     // ---------------------------------------------- router
-    if (threadIdx.x == kThreads + 64) grid_poll(p.bar + 0, p.status, abort);
-    router_sync();
-    if (*abort == 0) route(p, ls, keys);
+    if constexpr (kCoded) {
+      token_terms<RT>(p);
+      ptx::fence_proxy_async_all();  // TMA will read them
+      router_sync();
+    }
+    if (threadIdx.x == kThreads + 64) {
+      if (kCoded) {
+        __threadfence();
+        atomicAdd(p.bar + 8, 1u);
+      }
+      grid_poll(p.bar + 0, gridDim.x, p.status, abort);
+      if (kCoded) grid_poll(p.bar + 8, gridDim.x, p.status, abort);
+    }
+    if (ptx::named_barrier_and(10, 32 * kRouterWarps, *abort == 0)) route(p, ls, keys, abort);
     ptx::mbar_arrive(&ct.routed);
   } else {
     // ---------------------------------------------- consumers
     Ring ring, coded;
     logits_share(p, reinterpret_cast<double*>(sm.red));
-    if constexpr (kCoded) {
-      token_terms<RT>(p);
-      ptx::fence_proxy_async_all();  // TMA will read them
-    }
     grid_arrive(p.bar + 0);
     bool ok = true;
     if (p.S > 0) ok = consume<RT, true, false>(p, ls, sm, ring);
@@ -1593,7 +1646,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
             consumer_sync();
             ring.n = ct.position;
           }
-          if (*abort == 0) consume<RT, true, true>(p, ls, sm, ring);
+          consume<RT, true, true>(p, ls, sm, ring);
         }
         grid_arrive(p.bar + 3);
         if (grid_wait(p.bar + 3, p.status, abort)) combine(p, ls);

@@ -57,7 +57,10 @@ struct FewParams {
   float* w_out;        // may be null
   int32_t* counts_out; // may be null
   uint32_t* status;
-  uint32_t* bar;       // arrivals at the grid's barriers, claimed chunks (4 each); zero before the launch
+  // arrivals at the grid's barriers, claimed chunks (4 each), x's terms, choosers; zero before the launch
+  uint32_t* bar;
+  int32_t* chosen;     // [T, k] experts and weights, on their way between CTAs
+  float* chosen_w;
   FewSplit split_up_r, split_up_s, split_dn_r, split_dn_s;
   float* logits;       // [T, E]
   float *up_r, *up_s, *dn_r, *dn_s;  // the chunks' sums, [row][segment][part][kFewCols]

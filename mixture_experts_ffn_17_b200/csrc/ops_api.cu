@@ -36,7 +36,7 @@ int few_weights(const moe_shape& s) {
 
 struct FewLayout {
   FewSplit split_up_r, split_up_s, split_dn_r, split_dn_s;
-  size_t logits, up_r, up_s, dn_r, dn_s, h_r, h_s, x_terms, x_scale, h_scale, x_term_scales, h_term_scales, total;
+  size_t logits, up_r, up_s, dn_r, dn_s, h_r, h_s, x_terms, x_scale, h_scale, x_term_scales, h_term_scales, chosen, chosen_w, total;
 };
 
 FewLayout few_layout(const moe_shape& s) {
@@ -72,6 +72,8 @@ FewLayout few_layout(const moe_shape& s) {
   L.h_scale = take(kind == kFewE4m3 ? (size_t)rows * bi * 4 : 0);
   L.x_term_scales = take(kind == kFewMxfp4 ? (size_t)T * few_term_rows(kind) * (s.d / kMxBlock) : 0);
   L.h_term_scales = take(kind == kFewMxfp4 ? (size_t)rows * few_term_rows(kind) * (s.inter / kMxBlock) : 0);
+  L.chosen = take((size_t)rows * 4);
+  L.chosen_w = take((size_t)rows * 4);
   L.total = off;
   return L;
 }
@@ -236,6 +238,8 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.dn_s = at<float>(ws, L.dn_s);
   p.h_r = at<uint8_t>(ws, L.h_r);
   p.h_s = at<uint8_t>(ws, L.h_s);
+  p.chosen = at<int32_t>(ws, L.chosen);
+  p.chosen_w = at<float>(ws, L.chosen_w);
   p.x_terms = at<uint8_t>(ws, L.x_terms);
   p.x_scale = at<float>(ws, L.x_scale);
   p.h_scale = at<float>(ws, L.h_scale);
