@@ -90,14 +90,11 @@ constexpr int kXTerms8 = 3, kHTerms8 = 6, kTerms4 = 12;
 constexpr int kRedPitch = 17;  // floats of one B column of a warp pair's 16 output columns
 constexpr int kRedFloats = 2 * kMaxCols * kRedPitch;  // of a pair of warps
 
-// TMEM of coded calls: accumulators (MXFP4: one for a pass, two in turn; e4m3: one
-// for a unit, whose sums get their scales in registers, four in turn), then MXFP4's
-// scales, 8 columns of the weights' and 8 of the terms' for each stage.
-constexpr int kAccCols = 64;
-template <int RT>
-constexpr int kAccs = RT == kFewE4m3 ? 4 : 2;
-template <int RT>
-constexpr int kIssuers = RT == kFewE4m3 ? 2 : 1;  // threads that issue MMAs
+// TMEM of coded calls: four accumulators (e4m3: each of a unit, whose sums get their
+// scales in registers; MXFP4: in pairs, each of a pass's every second unit), then
+// MXFP4's scales, 8 columns of the weights' and 8 of the terms' for each stage.
+constexpr int kAccCols = 64, kAccs = 4;
+constexpr int kIssuers = 2;  // threads that issue MMAs
 constexpr int kSfCols = 16;
 // e4m3: factors of a pass, [8 rows][32 units], for this many passes in turn.  When a
 // stage is filled the one before it in its place has been multiplied, so that the
@@ -106,7 +103,8 @@ constexpr int kSfCols = 16;
 constexpr int kFactors = 12;
 constexpr size_t kExchangeBytes = 2 * 8 * (128 + 64) * 4;  // two groups of 4 units' scales, or factors
 static_assert(kExchangeBytes >= kFactors * 256 * 4, "room for the factors");
-constexpr int kTmemCols = 256;
+template <int RT>
+constexpr int kTmemCols = RT == kFewE4m3 ? 256 : 512;
 
 struct Lists {  // what the routing leaves in shared memory
   int32_t idx[kMaxRows];      // [T][k]
@@ -127,11 +125,13 @@ struct Control {
   // is filled again, but not when the place after it is
   uint64_t issued[2 * kMaxStages];
   uint64_t scaled[kFactors];    // MXFP4: a stage's scales are in TMEM; e4m3: a pass's factors are there
-  uint64_t acc_full[4], acc_empty[4];
+  uint64_t acc_full[kAccs], acc_empty[kAccs];
   uint64_t ready;   // h is there, in all CTAs
   uint64_t routed;  // the lists are there
   int chunk[2 * kMaxStages];  // which chunk a stage belongs to; -1: the share is done
-  int acc_chunk[4], acc_pass[4], acc_step[4];  // what an accumulator holds; a pass's first: step -1
+  // what an accumulator holds: of e4m3 a pass's first unit (-1) or the one of this
+  // number, of MXFP4 nothing (0) or sums
+  int acc_chunk[kAccs], acc_pass[kAccs], acc_what[kAccs];
   int position;  // stages handed over when a coded share ended
   uint32_t tmem, abort, never;
 };
@@ -662,15 +662,15 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
 }
 
 // Issues a share's MMAs.  A thread does all of it, since with a warp's other lanes
-// waiting beside each issue a stage took half as long again.  An MMA takes its
-// thread some 70 cycles, so e4m3's units, which have accumulators of their own,
-// are issued by two threads in turn.
+// waiting beside each issue a stage took half as long again; and an MMA takes its
+// thread some 70 cycles, so two threads have every second stage each, with
+// accumulators of their own.
 template <int RT, bool DOWN>
 __device__ bool issue_mmas(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring, int who) {
-  constexpr int S = Cfg<RT>::kStages, kA = kAccs<RT>, kI = kIssuers<RT>;
+  constexpr int S = Cfg<RT>::kStages;
   // the stage that was in a stage's place was this thread's too, so its barrier is
   // never waited for a turn early
-  static_assert(S % kI == 0 && kA % kI == 0, "stages and accumulators of its own");
+  static_assert(S % kIssuers == 0 && kAccs % kIssuers == 0, "stages and accumulators of its own");
   Control& c = *sm.c;
   const uint32_t base = ptx::smem_u32(sm.stages);
   const uint64_t a_desc = ptx::sdesc_sw128(base, 16, 1024), b_desc = ptx::sdesc_sw128(base + kTileBytes, 16, 1024);
@@ -681,15 +681,14 @@ __device__ bool issue_mmas(const FewParams& p, const Lists& ls, const Smem& sm, 
     return false;
   };
   // an accumulator is handed over when its MMAs are done and its labels are there
-  auto take = [&] { return wait(&c.acc_empty[ring.accs % kA], ((ring.accs / kA) & 1) ^ 1); };
-  auto hand_over = [&](int id, int pass, int step) {
-    const int b = ring.accs % kA;
+  auto take = [&](int acc) { return wait(&c.acc_empty[acc % kAccs], ((acc / kAccs) & 1) ^ 1); };
+  auto hand_over = [&](int acc, int id, int pass, int what) {
+    const int b = acc % kAccs;
     ptx::mma_commit(&c.acc_full[b]);
     c.acc_chunk[b] = id;
     c.acc_pass[b] = pass;
-    c.acc_step[b] = step;
+    c.acc_what[b] = what;
     ptx::mbar_arrive(&c.acc_full[b]);
-    ++ring.accs;
   };
   const Share<RT, false, DOWN> share(p, ls);
   while (true) {
@@ -699,56 +698,69 @@ __device__ bool issue_mmas(const FewParams& p, const Lists& ls, const Smem& sm, 
     int pass = 0;
     const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
       const int N = (q.rows * few_term_rows(RT) + 15) & ~15;
-      const uint32_t id0 = RT == kFewE4m3 ? idesc_e4m3(N) : idesc_mxf4(N, 0), id1 = idesc_mxf4(N, 1);
-      for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
-        const int s = ring.n % S;
-        if (kI > 1 && ring.accs % kI != who) {
-          ++ring.accs;
-          continue;
-        }
-        if ((RT == kFewE4m3 || step == q.step0) && !take()) return false;
-        if (!wait(&c.full[s], (ring.n / S) & 1)) return false;
-        if (RT == kFewMxfp4) {
-          // every stage of a coded share has scales: its own count of them
-          if (!wait(&c.scaled[s], (ring.cols >> s) & 1)) return false;
-          ring.cols ^= 1 << s;
-        }
-        ptx::tc_fence_after();
-        const uint32_t off = s * (Cfg<RT>::kStageBytes >> 4);
-        const uint64_t a = a_desc + off, b = b_desc + off;
-        const uint32_t d = c.tmem + (ring.accs % kA) * kAccCols;
-        if (RT == kFewE4m3) {
+      if constexpr (RT == kFewE4m3) {
+        const uint32_t idesc = idesc_e4m3(N);
+        for (int step = q.step0; step < q.step1; ++step, ++ring.n, ++ring.accs) {
+          if (ring.accs % kIssuers != who) continue;
+          const int s = ring.n % S;
+          if (!take(ring.accs) || !wait(&c.full[s], (ring.n / S) & 1)) return false;
+          ptx::tc_fence_after();
+          const uint32_t off = s * (Cfg<RT>::kStageBytes >> 4);
+          const uint64_t a = a_desc + off, b = b_desc + off;
+          const uint32_t d = c.tmem + (ring.accs % kAccs) * kAccCols;
           // 32 steps: 32 rows of the tile, 32 bytes of a term's row
-          mma_e4m3(d, a, b, id0, 0u);
-          mma_e4m3(d, a + (4096 >> 4), b + 2, id0, 1u);
-          mma_e4m3(d, a + (8192 >> 4), b + 4, id0, 1u);
-          mma_e4m3(d, a + (12288 >> 4), b + 6, id0, 1u);
-        } else {
-          const uint32_t sf = c.tmem + kA * kAccCols + s * kSfCols;
-          mma_mxf4(d, a, b, id0, sf, sf + 8, step != q.step0 ? 1u : 0u);
+          mma_e4m3(d, a, b, idesc, 0u);
+          mma_e4m3(d, a + (4096 >> 4), b + 2, idesc, 1u);
+          mma_e4m3(d, a + (8192 >> 4), b + 4, idesc, 1u);
+          mma_e4m3(d, a + (12288 >> 4), b + 6, idesc, 1u);
+          ptx::mma_commit(&c.empty[s]);
+          hand_over(ring.accs, id, pass, step == q.step0 ? -1 : step - q.step0);
+        }
+      } else {
+        const uint32_t id0 = idesc_mxf4(N, 0), id1 = idesc_mxf4(N, 1);
+        const int acc = ring.accs + who;
+        const uint32_t d = c.tmem + (acc % kAccs) * kAccCols;
+        if (!take(acc)) return false;
+        uint32_t more = 0;
+        for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
+          if (ring.n % kIssuers != who) continue;
+          const int s = ring.n % S;
+          // every stage of a coded share has scales: its own count of them
+          if (!wait(&c.full[s], (ring.n / S) & 1) || !wait(&c.scaled[s], (ring.cols >> s) & 1)) return false;
+          ring.cols ^= 1 << s;
+          ptx::tc_fence_after();
+          const uint32_t off = s * (Cfg<RT>::kStageBytes >> 4);
+          const uint64_t a = a_desc + off, b = b_desc + off;
+          const uint32_t sf = c.tmem + kAccs * kAccCols + s * kSfCols;
+          mma_mxf4(d, a, b, id0, sf, sf + 8, more);
           mma_mxf4(d, a + 2, b + 2, id1, sf, sf + 8, 1u);
           if (K - step * 256 > 128) {  // else the last unit is half of one
             mma_mxf4(d, a + 4, b + 4, id0, sf + 4, sf + 12, 1u);
             mma_mxf4(d, a + 6, b + 6, id1, sf + 4, sf + 12, 1u);
           }
+          ptx::mma_commit(&c.empty[s]);
+          more = 1;
         }
-        ptx::mma_commit(&c.empty[s]);
-        if (RT == kFewE4m3) hand_over(id, pass, step == q.step0 ? -1 : step - q.step0);
+        hand_over(acc, id, pass, more);
+        ring.accs += kIssuers;
       }
-      if (RT == kFewMxfp4) hand_over(id, pass, -1);
       ++pass;
       return true;
     });
     if (!ok) return false;
   }
-  if (kI > 1 && ring.accs % kI != who) {
-    ++ring.accs;
-    return true;
+  // the end is told once, or by MXFP4's accumulators, which go in pairs, both
+  const bool mine = ring.accs % kIssuers == who;
+  const int acc = RT == kFewE4m3 ? ring.accs : ring.accs + who;
+  if (RT == kFewMxfp4 || mine) {
+    if (!take(acc)) return false;
+    hand_over(acc, -1, 0, 0);
   }
-  if (!take()) return false;
-  hand_over(-1, 0, 0);
-  ptx::mbar_arrive(&c.empty[ring.n % S]);
-  c.position = ring.n + 1;
+  if (mine) {
+    ptx::mbar_arrive(&c.empty[ring.n % S]);
+    c.position = ring.n + 1;
+  }
+  ring.accs += RT == kFewE4m3 ? 1 : kIssuers;
   return true;
 }
 
@@ -764,23 +776,24 @@ __device__ __forceinline__ void load_sums(uint32_t tmem, float (&v)[16]) {
 // Drains a share's accumulators (four warps; a thread has one output column).
 template <int RT, bool DOWN>
 __device__ bool drain(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
-  constexpr int kA = kAccs<RT>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = threadIdx.x & 127;
   Control& c = *sm.c;
   const Share<RT, false, DOWN> share(p, ls);
-  float sums[8];  // e4m3: of each row
+  float sums[RT == kFewE4m3 ? 8 : 4];  // of each row
   Piece q = {};
   while (true) {
-    const int b = ring.accs % kA;
+    const int b = ring.accs % kAccs;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (warp_wait(bar, parity, &c.abort)) return true;
       if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
       return false;
     };
-    if (!wait(&c.acc_full[b], (ring.accs / kA) & 1)) return false;
+    if (!wait(&c.acc_full[b], (ring.accs / kAccs) & 1)) return false;
     ptx::tc_fence_after();
-    const int id = c.acc_chunk[b], step = c.acc_step[b];
+    const int id = c.acc_chunk[b], what = c.acc_what[b];
+    const bool second = RT == kFewMxfp4 && (ring.accs & 1) != 0;  // of a pair
+    const uint32_t acc = c.tmem + ((uint32_t)((warp & 3) * 32) << 16) + b * kAccCols;
     auto release = [&] {
       ptx::tc_fence_before();
       ptx::mbar_arrive(&c.acc_empty[b]);
@@ -788,34 +801,39 @@ __device__ bool drain(const FewParams& p, const Lists& ls, const Smem& sm, Ring&
     };
     if (id < 0) {
       release();
+      if (RT == kFewMxfp4 && !second) continue;
       return true;
     }
-    if (step < 0) {  // the pass's first
+    if (RT == kFewMxfp4 ? !second : what < 0) {  // the pass's first
       q = share.chunk(p, ls, id);
       share.cut(q, q.rows, c.acc_pass[b] * share.kPass);
-    }
-    const uint32_t acc = c.tmem + ((uint32_t)((warp & 3) * 32) << 16) + b * kAccCols;
-    if constexpr (RT == kFewMxfp4) {
-      for (int r = 0; r < q.rows; ++r) {
-        float v[16];
-        load_sums(acc + r * 16, v);
-        // the last terms, the smallest, first
-        float a = 0.0f;
 #pragma unroll
-        for (int t = kTerms4 - 1; t >= 0; --t) a += v[t];
-        q.out[r * q.ld + col] = a;
+      for (int r = 0; r < share.kPass; ++r) sums[r] = 0.0f;
+    }
+    if constexpr (RT == kFewMxfp4) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (r < q.rows && what) {
+          float v[16];
+          load_sums(acc + r * 16, v);
+          // the last terms, the smallest, first
+          float a = 0.0f;
+#pragma unroll
+          for (int t = kTerms4 - 1; t >= 0; --t) a += v[t];
+          sums[r] += a;
+        }
       }
       release();
+      if (second) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (r < q.rows) q.out[r * q.ld + col] = sums[r];
+      }
     } else {
       const int slot = ring.cols % kFactors;
       const float* factors = reinterpret_cast<const float*>(sm.exchange) + slot * 256;
-      int unit = step;
-      if (step < 0) {
-        if (!wait(&c.scaled[slot], (ring.cols / kFactors) & 1)) return false;
-        unit = 0;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) sums[r] = 0.0f;
-      }
+      if (what < 0 && !wait(&c.scaled[slot], (ring.cols / kFactors) & 1)) return false;
+      const int unit = max(what, 0);
 #pragma unroll
       for (int r = 0; r < 8; r += 2) {
         if (r < q.rows) {
@@ -963,7 +981,7 @@ __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm
         }
         if (!issued()) continue;
         ptx::tc_fence_after();
-        const uint32_t to = c.tmem + ((uint32_t)((warp & 3) * 32) << 16) + kAccs<RT> * kAccCols + (ring.n % S) * kSfCols;
+        const uint32_t to = c.tmem + ((uint32_t)((warp & 3) * 32) << 16) + kAccs * kAccCols + (ring.n % S) * kSfCols;
         asm volatile(
             "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
             "%15, %16};" ::"r"(to),
@@ -1007,7 +1025,7 @@ __device__ bool consume_routed(const FewParams& p, const Lists& ls, const Smem& 
         coded.n = ring.n;
         ok = bring_factors<DOWN>(p, ls, sm, coded);
       }
-    } else if (warp < 8 + kIssuers<RT>) {
+    } else if (warp < 8 + kIssuers) {
       coded.n = ring.n;
       if ((threadIdx.x & 31) == 0) ok = issue_mmas<RT, DOWN>(p, ls, sm, coded, warp - 8);
       __syncwarp();
@@ -1538,7 +1556,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
       ptx::mbar_init(&ct.col_full[b], 1);
       ptx::mbar_init(&ct.col_empty[b], kWarps);
     }
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < kAccs; ++b) {
       ptx::mbar_init(&ct.acc_full[b], 2);
       ptx::mbar_init(&ct.acc_empty[b], 128);
     }
@@ -1550,7 +1568,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     ptx::fence_proxy_async();
   }
   if (kCoded && warp == 8) {
-    ptx::tmem_alloc(&ct.tmem, kTmemCols);
+    ptx::tmem_alloc(&ct.tmem, kTmemCols<RT>);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -1658,7 +1676,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     __syncthreads();
     if (warp == 8) {
       ptx::tc_fence_after();
-      ptx::tmem_dealloc(ct.tmem, kTmemCols);
+      ptx::tmem_dealloc(ct.tmem, kTmemCols<RT>);
     }
   }
 }
