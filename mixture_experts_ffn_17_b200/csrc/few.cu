@@ -101,7 +101,7 @@ constexpr int kSfCols = 16;
 // accumulators up to kAccs stages before that are drained: the passes 11 before are
 // done with.
 constexpr int kFactors = 12;
-constexpr size_t kExchangeBytes = 2 * 8 * (128 + 64) * 4;  // two groups of 4 units' scales, or factors
+constexpr size_t kExchangeBytes = 4 * 8 * (128 + 64) * 4;  // two groups of 4 units' scales for each team, or factors
 static_assert(kExchangeBytes >= kFactors * 256 * 4, "room for the factors");
 template <int RT>
 constexpr int kTmemCols = RT == kFewE4m3 ? 256 : 512;
@@ -350,7 +350,7 @@ struct Smem {
   uint8_t* stages;
   uint8_t* cols;
   float* red;
-  uint32_t* exchange;  // MXFP4: two groups of scales on their way from rows to lanes; e4m3: factors
+  uint32_t* exchange;  // MXFP4: groups of scales on their way from rows to lanes; e4m3: factors
   Control* c;
 };
 
@@ -904,12 +904,12 @@ __device__ bool bring_factors(const FewParams& p, const Lists& ls, const Smem& s
   return ok;
 }
 
-// MXFP4: a share's scales to TMEM (four warps), row r of 128 in lane r % 32 of
+// MXFP4: a share's scales to TMEM (two teams of four warps, which take groups of
+// units in turn), row r of 128 in lane r % 32 of
 // column r / 32 in all lane quarters, four blocks of 32 steps to a word.  Thread r
-// reads row r of the weights and of the terms, a group of units at a time, and the
-// rows go through shared memory to the lanes that store them.
+// reads row r of the weights and of the terms, and the rows go through shared memory to the lanes that store them.
 template <bool DOWN>
-__device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
+__device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring, int team) {
   constexpr int RT = kFewMxfp4, S = Cfg<RT>::kStages, kGroup = 4, kRows = 128 + 64;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = threadIdx.x & 127;
@@ -917,7 +917,7 @@ __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm
   const Share<RT, false, DOWN> share(p, ls);
   const int words = share.K / 128;  // of a row, four scales each
   const uint8_t* terms = DOWN ? p.h_term_scales : p.x_term_scales;
-  int buf = 0;
+  int buf = 2 * team, group = 0;
   bool ok = true;
   // A warp whose wait failed goes on without: the others need it at the barriers.
   // They leave together at the end of a chunk.
@@ -959,16 +959,20 @@ __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm
         t[i] = have && x ? __ldcg(x + at) : 0u;
       }
     };
-    load(q.step0);
+    load((group & 1) == team ? q.step0 : q.step0 + kGroup);
     for (int step0 = q.step0; step0 < q.step1; step0 += kGroup) {
+      if ((group++ & 1) != team) {
+        ring.n += min(kGroup, q.step1 - step0);
+        continue;
+      }
       uint32_t* ex = sm.exchange + buf * (2 * kGroup * kRows);
 #pragma unroll
       for (int i = 0; i < 2 * kGroup; ++i) {
         ex[i * kRows + r] = a[i];
         if (r < 64) ex[i * kRows + 128 + r] = t[i];
       }
-      load(step0 + kGroup);  // the next group's are on their way meanwhile
-      ptx::named_barrier(11, 128);
+      load(step0 + 2 * kGroup);  // the next ones are on their way meanwhile
+      ptx::named_barrier(11 + team, 128);
       for (int u = 0; u < kGroup && step0 + u < q.step1; ++u, ++ring.n) {
         uint32_t v[16];
 #pragma unroll
@@ -999,7 +1003,7 @@ __device__ bool bring_scales(const FewParams& p, const Lists& ls, const Smem& sm
   int id = blockIdx.x < share.total ? (int)blockIdx.x : -1;
   while (id >= 0) {
     share.passes(share.chunk(p, ls, id), pass);
-    if (!ptx::named_barrier_and(11, 128, issued())) return false;
+    if (!ptx::named_barrier_and(11 + team, 128, issued())) return false;
     id = c.chunk[ring.n % (2 * S)];
   }
   ++ring.n;  // the mark of the end
@@ -1017,11 +1021,11 @@ __device__ bool consume_routed(const FewParams& p, const Lists& ls, const Smem& 
     bool ok = true;
     if (warp < 4) {
       ok = drain<RT, DOWN>(p, ls, sm, coded);
+    } else if (RT == kFewMxfp4 && (warp < 8 || warp >= 12)) {
+      coded.n = ring.n;
+      ok = bring_scales<DOWN>(p, ls, sm, coded, warp >= 12);
     } else if (warp < 8) {
-      if (RT == kFewMxfp4) {
-        coded.n = ring.n;
-        ok = bring_scales<DOWN>(p, ls, sm, coded);
-      } else if (warp == 4) {
+      if (RT == kFewE4m3 && warp == 4) {
         coded.n = ring.n;
         ok = bring_factors<DOWN>(p, ls, sm, coded);
       }
