@@ -94,8 +94,8 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) 
 }
 
 // silu(g) * u: the exponential is good to one step of fp32, the reciprocal and the
-// products add four halves.
-__device__ __forceinline__ float gated(float g, float u) { return g * u * __fdividef(1.0f, 1.0f + expf(-g)); }
+// products add four halves.  silu(g) first: g * u may overflow where it does not.
+__device__ __forceinline__ float gated(float g, float u) { return g * __fdividef(1.0f, 1.0f + expf(-g)) * u; }
 
 // Groups of 8 values in flight per thread: 2048 threads of an SM with 16 bytes each
 // do not cover HBM's latency (58% of its rate, with 64 bytes 84%).

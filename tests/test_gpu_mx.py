@@ -104,6 +104,18 @@ def test_gated_rows(dtype):
     assert np.mean(got == sides[1]) > 0.999
 
 
+def test_gated_rows_whose_product_alone_overflows():
+    # g u is -infinite in fp32.  silu(-120) = -120 e^-120 = -9e-51 is 0 in fp32;
+    # silu(-80) 3e38 = -433164 is 6 of 2^16 (the border to the next code down, 5 of
+    # 2^16, lies 24% away)
+    g = torch.full((2, 32), -120.0)
+    g[1, 3] = -80.0
+    codes, scales = quantised(g.cuda(), torch.full((2, 32), 3e38).cuda())
+    want = np.zeros((2, 32))
+    want[1, 3] = -6 * 2.0 ** 16
+    assert np.array_equal(mx_ref.values(codes.cpu().numpy(), scales.cpu().numpy()), want)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("E,K,N", [(1, 32, 1), (2, 96, 7), (1, 256, 64), (3, 288, 66), (2, 1024, 129), (1, 7168, 10)])
 def test_weights(E, K, N, dtype):
