@@ -331,13 +331,16 @@ def _on(device, stream, call):
     if device.type != "cuda":
         raise ValueError(f"libmoe works on CUDA tensors, got one on {device}")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if stream.device != device:
+        # the handle alone: a Stream object costs 2 us, a quarter of a small call
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device != device:
         raise ValueError(f"stream on {stream.device} for tensors on {device}")
+    else:
+        raw = stream.cuda_stream
     if device.index == torch.cuda.current_device():
-        return call(stream.cuda_stream)
+        return call(raw)
     with torch.cuda.device(device):
-        return call(stream.cuda_stream)
+        return call(raw)
 
 
 def _adr(t, device):
@@ -409,10 +412,10 @@ def mx_quantise(src, codes, scales, up=None, stream=None):
 
 def _row_stride(t):
     """Elements between neighbouring rows of a tensor whose rows are evenly spaced."""
+    if t.dim() > 0 and t.is_contiguous():
+        return t.shape[-1]
     if t.dim() == 0 or (t.shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError("rows must be contiguous")
-    if t.is_contiguous():
-        return t.shape[-1]
     if t.dim() == 2:
         ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
         if ld >= t.shape[1]:
