@@ -380,7 +380,10 @@ moe_status moe_forward_profiled(const moe_shape* shape, const void* x, const voi
  *     sigmoid, the selection scores and the group scores are fp64 values of the
  *     fp32 logits (a NaN score ranks last, the lowest index first among equals);
  *   - h = silu(x W1) * (x W3) and every expert's output stay fp32 (moe_forward
- *     rounds both to bf16); y is rounded once, to shape->y_dtype.
+ *     rounds both to bf16); y is rounded once, to shape->y_dtype;
+ *   - with e4m3 and MXFP4 experts x and h enter the products as sums of terms of
+ *     the weights' own type, together good to 2^-24 of the largest value of 128
+ *     (e4m3) or 32 (MXFP4) neighbouring ones; an infinity enters as NaN.
  *   shape: as moe_forward; w_dtype may also be MOE_MXFP4.
  *   W1, W3, W2, s1, s3, s2: bf16 and e4m3 weights (with fp32 block scales) as
  *     moe_grouped_swiglu; MOE_MXFP4 weights with the contraction innermost, as

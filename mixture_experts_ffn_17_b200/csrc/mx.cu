@@ -358,7 +358,9 @@ cudaError_t launch_mx_dequantise(const uint8_t* codes, const uint8_t* scales, in
                                  bool bf16, int sms, cudaStream_t stream) {
   const int64_t groups = rows * (cols / 8);
   const uint32_t* c = reinterpret_cast<const uint32_t*>(codes);
-  return launch_chained(bf16 ? mx_dequantise_kernel<true> : mx_dequantise_kernel<false>, dim3(grid_for((groups + kReads - 1) / kReads, sms)), dim3(256), 0, stream, c, scales, groups, dst);
+  return launch_chained(bf16 ? mx_dequantise_kernel<true> : mx_dequantise_kernel<false>,
+                        dim3(grid_for((groups + kReads - 1) / kReads, sms)), dim3(256), 0, stream, c, scales, groups,
+                        dst);
 }
 
 }  // namespace moe

@@ -36,7 +36,8 @@ int few_weights(const moe_shape& s) {
 
 struct FewLayout {
   FewSplit split_up_r, split_up_s, split_dn_r, split_dn_s;
-  size_t logits, up_r, up_s, dn_r, dn_s, h_r, h_s, x_terms, x_scale, h_scale, x_term_scales, h_term_scales, chosen, chosen_w, total;
+  size_t logits, up_r, up_s, dn_r, dn_s, h_r, h_s, x_terms, x_scale, h_scale, x_term_scales, h_term_scales;
+  size_t chosen, chosen_w, total;
 };
 
 FewLayout few_layout(const moe_shape& s) {

@@ -278,3 +278,31 @@ def test_two_streams_with_workspaces_of_their_own():
                           ws, stream=st)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, ys))
+
+
+def test_long_sums_keep_their_bits():
+    """The tensor core cuts off (2^-24 of its accumulator on average) at every MMA.
+    Four MMAs of a tile, whose sum is 1/sqrt(d/64) of the whole, cut 4 2^-24 of it in
+    norm over all d/64 tiles: 2.4e-7 in each of g, u and the down product.  Adding the
+    tiles up to nearest, h and the joins add some 4 roundings of 2^-24 at random
+    signs, 1.2e-7.  Together sqrt(3) (2.4e-7 + 1.2e-7) = 6.2e-7; cutting in one
+    accumulator over 64 MMAs would cost about 64^(1/2) / 2 as much."""
+    d, inter, E, k, T = 7168, 2048, 32, 2, 16
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x, Wg = r(T, d).bfloat16(), (r(E, d) * d ** -0.5).bfloat16()
+    W = [(r(E, K, N) * K ** -0.5).bfloat16() for K, N in ((d, inter), (d, inter), (inter, d))]
+    shape = B.make_shape(T, d, E, k, inter, 0, 0, 1, 1, 2, 1.0, B.MOE_BF16, B.MOE_F32)
+    y, ws = torch.empty(T, d, device="cuda"), B.alloc_few_workspace(shape)
+    idx, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    B.forward_few(shape, x, Wg, None, *W, None, None, None, None, None, None, y, ws, idx, w)
+    assert B.check_device_status(ws) == (0, 0)
+    want = torch.zeros(T, d, dtype=torch.float64, device="cuda")
+    for e in range(E):
+        t, j = torch.where(idx == e)
+        if len(t):
+            v = x[t].double()
+            h = torch.nn.functional.silu(v @ W[0][e].double()) * (v @ W[1][e].double())
+            want.index_add_(0, t, w[t, j].double()[:, None] * (h @ W[2][e].double()))
+    error = ((y.double() - want).norm() / want.norm()).item()
+    assert error < 6.2e-7, error
