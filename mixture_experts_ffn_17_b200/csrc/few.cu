@@ -58,7 +58,7 @@
 //   (e4m3) the factors of the sums.
 //
 // Measured, d = 7168, inner 2048, top-8 of 32 with a shared expert, T = 8 (28
-// experts): bf16 395 us, 6.5 TB/s and the measured copy rate of HBM; e4m3 262 us,
+// experts): bf16 387 us, 6.6 TB/s and the measured copy rate of HBM; e4m3 262 us,
 // 5.0 TB/s, where its tiles' rows of 128 bytes alone allow no more (with the MMAs,
 // scales and terms left out it takes as long); MXFP4 190 us, 3.9 TB/s (160 us
 // without them).  T = 1: 146, 114 and 90 us, of which the phases outside the
