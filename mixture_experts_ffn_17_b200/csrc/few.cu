@@ -60,7 +60,7 @@
 // Measured, d = 7168, inner 2048, top-8 of 32 with a shared expert, T = 8 (28
 // experts): bf16 387 us, 6.6 TB/s and the measured copy rate of HBM; e4m3 262 us,
 // 5.0 TB/s, where its tiles' rows of 128 bytes alone allow no more (with the MMAs,
-// scales and terms left out it takes as long); MXFP4 190 us, 3.9 TB/s (160 us
+// scales and terms left out it takes as long); MXFP4 184 us, 4.0 TB/s (160 us
 // without them).  T = 1: 146, 114 and 90 us, of which the phases outside the
 // streams (router, four barriers of 2 us, activations, combine) take some 25.
 #include <algorithm>
@@ -402,10 +402,25 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
     if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
     return false;
   };
+  // MXFP4: the next chunk's scale bytes to L2, a line or two of each of its 128 rows.
+  // Read when they are needed, in pieces of 32 bytes, they held the stages up: 54
+  // experts at T = 16 took 311 instead of 293 us.  (Bulk prefetches of whole rows
+  // went through the unit that has the tiles to load: 397 us.)
+  auto fetch_scales = [&](int id) {
+    if (WT != kFewMxfp4 || id >= share.total) return;
+    const Piece q = share.chunk(p, ls, id);
+    const int pitch = share.K / 32, from = q.step0 * 8, end = min(q.step1 * 8, pitch);
+    const uint8_t* scales = (q.mat == 0 ? p.s1 : q.mat == 1 ? p.s3 : p.s2) +
+                            ((int64_t)q.expert * share.N + q.col0 + lane) * pitch;
+    for (int i = 0; i < 4; ++i)  // rows lane + 32 i
+      for (int o = from; o < end; o += 64)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(scales + (int64_t)(32 * i) * pitch + o) : "memory");
+  };
   int id = blockIdx.x;
   while (id < share.total) {
     int claimed = 0;
     if (lane == 0) claimed = (int)atomicAdd(counter, 1u) + gridDim.x;  // used after this chunk
+    bool fetched = WT != kFewMxfp4;
     const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
       // the columns' warp adds the terms to a stage of codes
       const uint32_t bytes = kTileBytes + (WT == kFewBf16 ? 0 : q.rows * few_term_rows(WT) * 128);
@@ -419,6 +434,10 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
           load_tile<WT, SHARED>(m, p, q, step, sm.stages + s * Cfg<RT>::kStageBytes, &c.full[s], q.again ? more : once);
         }
         __syncwarp();
+        if (!fetched && (step == q.step0 + 1 || step == q.step1 - 1)) {
+          fetch_scales(__shfl_sync(0xffffffffu, claimed, 0));
+          fetched = true;
+        }
       }
       return true;
     });
