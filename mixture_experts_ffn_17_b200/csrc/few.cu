@@ -534,11 +534,12 @@ __device__ bool bring_terms(const FewMaps& m, const FewParams& p, const Lists& l
     if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
     return false;
   };
-  // this warp's release of a stage, and the seven of the consumer warps that have
-  // no part in coded shares (the MMAs' completion is the last)
+  // this warp's release of a stage, and those of the consumer warps that have no part
+  // in coded shares (the MMAs' completion is the last, and e4m3's factors have one of
+  // their own)
   auto next_stage = [&] {
     __syncwarp();
-    if (lane == 0) mbar_arrive_many(&c.empty[ring.n % S], 8);
+    if (lane == 0) mbar_arrive_many(&c.empty[ring.n % S], RT == kFewE4m3 ? 7 : 8);
     ++ring.n;
   };
   const bool ok = follow_chunks<RT, RT, false, DOWN>(p, ls, sm, ring, [&](const Piece& q) {
@@ -902,6 +903,8 @@ __device__ bool drain(const FewParams& p, const Lists& ls, const Smem& sm, Ring&
 
 // e4m3: the factors of a share's passes (one warp, a lane per unit): the scale of a
 // block of weights times the power of two that undoes the scaling of a row's terms.
+// It reads no stage, but releases each: who waits for `issued` and holds no stage back
+// can fall two turns of the ring behind and wait for a phase that is gone.
 template <bool DOWN>
 __device__ bool bring_factors(const FewParams& p, const Lists& ls, const Smem& sm, Ring& ring) {
   constexpr int RT = kFewE4m3;
@@ -909,9 +912,17 @@ __device__ bool bring_factors(const FewParams& p, const Lists& ls, const Smem& s
   Control& c = *sm.c;
   const Share<RT, false, DOWN> share(p, ls);
   auto issued = [&] {
+    if (p.late_factors) __nanosleep(20000);  // a test's: more than a pass takes
     if (wait_issued<RT>(c, ring.n)) return true;
     if (lane == 0) raise_status(p.status, &c.abort, kStatusTimeout);
     return false;
+  };
+  auto next_stage = [&] {
+    if (!issued()) return false;
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&c.empty[ring.n % Cfg<RT>::kStages]);
+    ++ring.n;
+    return true;
   };
   const bool ok = follow_chunks<RT, RT, false, DOWN>(p, ls, sm, ring, [&](const Piece& q) {
     const int unit = min(q.step0 + lane, share.steps - 1);
@@ -934,14 +945,11 @@ __device__ bool bring_factors(const FewParams& p, const Lists& ls, const Smem& s
     for (int r = 0; r < 8; ++r) to[r * 32] = f * v[r];
     ptx::mbar_arrive(&c.scaled[slot]);
     ++ring.cols;
-    // every stage is waited for: a barrier can be read one turn of the ring late
-    // or early, not two
-    for (int step = q.step0; step < q.step1; ++step, ++ring.n)
-      if (!issued()) return false;
+    for (int step = q.step0; step < q.step1; ++step)
+      if (!next_stage()) return false;
     return true;
   });
-  ++ring.n;  // the mark of the end
-  return ok;
+  return ok && next_stage();  // the mark of the end
 }
 
 // MXFP4: a share's scales to TMEM (two teams of four warps, which take groups of
@@ -1591,7 +1599,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     for (int s = 0; s < S; ++s) {
       ptx::mbar_init(&ct.full[s], 1);
       // 8 consumer warps and the columns' warp, or, of a coded share's stage, that
-      // one for 8 and the MMAs
+      // one for 7 or 8 (with e4m3 the factors' warp has its own) and the MMAs
       ptx::mbar_init(&ct.empty[s], kWarps / 2 + 1);
       ptx::mbar_init(&ct.issued[s], 1);
       ptx::mbar_init(&ct.issued[s + S], 1);

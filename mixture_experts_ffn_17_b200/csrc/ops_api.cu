@@ -2,6 +2,7 @@
 // gradient norm: argument checks, workspace layouts and launch sequences.
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 
 #include "api_internal.h"
 #include "few.h"
@@ -77,6 +78,13 @@ FewLayout few_layout(const moe_shape& s) {
   L.chosen_w = take((size_t)rows * 4);
   L.total = off;
   return L;
+}
+
+// MOE_DEBUG_LATE_FACTORS=1 in the environment holds up the warp that brings the
+// e4m3 factors (tests of the ring: the others must wait for it).
+bool debug_late_factors() {
+  const char* v = std::getenv("MOE_DEBUG_LATE_FACTORS");
+  return v && v[0] == '1';
 }
 
 moe_status check_few(const moe_shape* shape) {
@@ -246,6 +254,7 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.h_scale = at<float>(ws, L.h_scale);
   p.x_term_scales = at<uint8_t>(ws, L.x_term_scales);
   p.h_term_scales = at<uint8_t>(ws, L.h_term_scales);
+  p.late_factors = debug_late_factors();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int weights = few_weights(s);
   FewMaps maps{};
