@@ -416,6 +416,10 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
       for (int o = from; o < end; o += 64)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(scales + (int64_t)(32 * i) * pitch + o) : "memory");
   };
+  // tiles that a test withholds: these and all later ones
+  int withheld = 0x7fffffff;
+  if (p.withhold == 1) withheld = ring.n;
+  if (p.withhold == 2 && DOWN && !SHARED && blockIdx.x == 0) withheld = ring.n + 1;
   int id = blockIdx.x;
   while (id < share.total) {
     int claimed = 0;
@@ -431,7 +435,9 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
           ptx::mbar_arrive_expect_tx(&c.full[s], bytes);
           c.chunk[ring.n % (2 * S)] = id;
           ptx::mbar_arrive(&c.issued[ring.n % (2 * S)]);
-          load_tile<WT, SHARED>(m, p, q, step, sm.stages + s * Cfg<RT>::kStageBytes, &c.full[s], q.again ? more : once);
+          if (ring.n < withheld)
+            load_tile<WT, SHARED>(m, p, q, step, sm.stages + s * Cfg<RT>::kStageBytes, &c.full[s],
+                                  q.again ? more : once);
         }
         __syncwarp();
         if (!fetched && (step == q.step0 + 1 || step == q.step1 - 1)) {
@@ -574,9 +580,19 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
   uint32_t cols = 0;
   // A wait that fails raises the abort flag, which ends all later ones at once, and
   // the piece goes on with whatever the buffers hold: its barriers need every
-  // warp, and the share ends at the next chunk.
+  // warp, and the share ends at the next chunk.  But the warp releases nothing more:
+  // a stage or buffer whose copies have not landed must not be armed again, which
+  // counts its barrier below zero.
+  bool releases = lane == 0;
   auto arrived = [&](uint64_t* bar, uint32_t parity) {
-    if (!ptx::wait_bounded(bar, parity, &ct.abort)) raise_status(p.status, &ct.abort, kStatusTimeout);
+    if (!ptx::wait_bounded(bar, parity, &ct.abort)) {
+      raise_status(p.status, &ct.abort, kStatusTimeout);
+      releases = false;
+    }
+  };
+  auto release = [&](uint64_t* bar) {
+    __syncwarp();
+    if (releases) ptx::mbar_arrive(bar);
   };
   for (int step = q.step0; step < q.step1; ++step) {
     if (left == 0) {
@@ -596,8 +612,7 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
       float sums[NT][4] = {};
       stage_bf16<NT>(tile, cols, plan.pitch, last, sums);
       before_release<NT>(sums);
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&ct.empty[slot]);
+      release(&ct.empty[slot]);
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -606,8 +621,7 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
     cols += ColumnPlan<RT>::kUnitBytes;
     ++ring.n;
     if (--left == 0) {
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&ct.col_empty[ring.cols & 1]);
+      release(&ct.col_empty[ring.cols & 1]);
       ++ring.cols;
     }
   }

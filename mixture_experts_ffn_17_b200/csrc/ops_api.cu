@@ -87,6 +87,14 @@ bool debug_late_factors() {
   return v && v[0] == '1';
 }
 
+// MOE_DEBUG_WITHHOLD_LOADS=1 makes the producers issue no loads, 2 one CTA of the
+// few-token layer only, in its routed down products (tests: the waits run out and
+// the call reports MOE_ERR_DEVICE_TIMEOUT).
+int debug_withhold() {
+  const char* v = std::getenv("MOE_DEBUG_WITHHOLD_LOADS");
+  return v && (v[0] == '1' || v[0] == '2') ? v[0] - '0' : 0;
+}
+
 moe_status check_few(const moe_shape* shape) {
   if (!shape) return MOE_ERR_INVALID_ARG;
   moe_shape s = *shape;
@@ -255,6 +263,7 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.x_term_scales = at<uint8_t>(ws, L.x_term_scales);
   p.h_term_scales = at<uint8_t>(ws, L.h_term_scales);
   p.late_factors = debug_late_factors();
+  p.withhold = debug_withhold();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int weights = few_weights(s);
   FewMaps maps{};

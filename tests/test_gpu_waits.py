@@ -1,6 +1,6 @@
 """The waits inside moe_forward_few: warps that come late, and waits that run out.
 Neither faults nor hangs: every wait is bounded, and debug switches of the library
-hold a warp up."""
+hold a warp up or withhold loads."""
 import pytest
 import torch
 
@@ -55,6 +55,24 @@ def test_late_factors_are_waited_for(monkeypatch, T, d, inter, shared):
     want, rc = layer.run()
     assert rc == B.MOE_OK and torch.isfinite(want).all()
     monkeypatch.setenv("MOE_DEBUG_LATE_FACTORS", "1")
+    got, rc = layer.run()
+    assert rc == B.MOE_OK
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("shared", [0, 256])
+@pytest.mark.parametrize("kind", ["bf16"])
+@pytest.mark.parametrize("withheld", ["1", "2"])
+def test_waits_run_out_and_the_next_call_is_right(monkeypatch, kind, shared, withheld):
+    """Tiles that never come, all of them or one CTA's of the down products: the call
+    ends by itself with the status, and the next one, in the same workspace, is right."""
+    layer = Layer(kind, 3, inter=1024, shared=shared)
+    want, rc = layer.run()
+    assert rc == B.MOE_OK and torch.isfinite(want).all()
+    monkeypatch.setenv("MOE_DEBUG_WITHHOLD_LOADS", withheld)
+    _, rc = layer.run()
+    assert rc == B.MOE_ERR_DEVICE_TIMEOUT
+    monkeypatch.delenv("MOE_DEBUG_WITHHOLD_LOADS")
     got, rc = layer.run()
     assert rc == B.MOE_OK
     assert torch.equal(got, want)
