@@ -138,6 +138,7 @@ struct Control {
   uint64_t issued[2 * kMaxStages];
   uint64_t scaled[kFactors];    // MXFP4: a stage's scales are in TMEM; e4m3: a pass's factors are there
   uint64_t acc_full[kAccs], acc_empty[kAccs];
+  uint64_t landed[kIssuers];  // a call that gave up: the MMAs issued so far are done
   uint64_t ready;   // h is there, in all CTAs
   uint64_t routed;  // the lists are there
   int chunk[2 * kMaxStages];  // which chunk a stage belongs to; -1: the share is done
@@ -1590,6 +1591,16 @@ __device__ void combine(const FewParams& p, const Lists& ls) {
   }
 }
 
+// Of a whole call the accumulators' drain has seen every MMA done.  Of one that gave up
+// they must land before TMEM and the CTA go: each issuer waits for its own.  (A call:
+// inlined, it moved the code of the e4m3 layer so that T = 8 took 254 instead of 249 us.)
+__device__ __noinline__ void land_mmas(Control& c, uint32_t* status) {
+  const int who = (int)(threadIdx.x >> 5) - 8;
+  if (who < 0 || who >= kIssuers || (threadIdx.x & 31) != 0) return;
+  ptx::mma_commit(&c.landed[who]);
+  if (!ptx::wait_bounded(&c.landed[who], 0, &c.never)) raise_status(status, &c.abort, kStatusTimeout);
+}
+
 // ------------------------------------------------------------ the kernel
 template <int RT>
 __global__ void __launch_bounds__(kAllThreads, 1)
@@ -1626,6 +1637,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
       ptx::mbar_init(&ct.acc_full[b], 2);
       ptx::mbar_init(&ct.acc_empty[b], 128);
     }
+    for (int i = 0; i < kIssuers; ++i) ptx::mbar_init(&ct.landed[i], 1);
     ptx::mbar_init(&ct.ready, 1);
     ptx::mbar_init(&ct.routed, 32 * kRouterWarps);
     ct.abort = 0u;
@@ -1711,7 +1723,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     Ring ring, coded;
     logits_share(p, reinterpret_cast<double*>(sm.red));
     grid_arrive(p.bar + 0);
-    bool ok = true;
+    bool ok = true, whole = false;
     if (p.S > 0) ok = consume<RT, true, false>(p, ls, sm, ring);
     // all consumers agree on whether there are lists
     ok = ptx::named_barrier_and(9, kThreads, ok && ptx::wait_bounded(&ct.routed, 0, abort) && *abort == 0);
@@ -1734,9 +1746,11 @@ __global__ void __launch_bounds__(kAllThreads, 1)
           consume<RT, true, true>(p, ls, sm, ring);
         }
         grid_arrive(p.bar + 3);
-        if (grid_wait(p.bar + 3, p.status, abort)) combine(p, ls);
+        whole = grid_wait(p.bar + 3, p.status, abort);
+        if (whole) combine(p, ls);
       }
     }
+    if (kCoded && !whole) land_mmas(ct, p.status);
   }
   if constexpr (kCoded) {
     ptx::tc_fence_before();

@@ -61,7 +61,7 @@ def test_late_factors_are_waited_for(monkeypatch, T, d, inter, shared):
 
 
 @pytest.mark.parametrize("shared", [0, 256])
-@pytest.mark.parametrize("kind", ["bf16"])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "mxfp4"])
 @pytest.mark.parametrize("withheld", ["1", "2"])
 def test_waits_run_out_and_the_next_call_is_right(monkeypatch, kind, shared, withheld):
     """Tiles that never come, all of them or one CTA's of the down products: the call
