@@ -65,14 +65,27 @@ def test_late_factors_are_waited_for(monkeypatch, T, d, inter, shared):
 @pytest.mark.parametrize("withheld", ["1", "2"])
 def test_waits_run_out_and_the_next_call_is_right(monkeypatch, kind, shared, withheld):
     """Tiles that never come, all of them or one CTA's of the down products: the call
-    ends by itself with the status, and the next one, in the same workspace, is right."""
+    ends by itself with the status and leaves y as it was, and the next one, in the same
+    workspace, is right."""
     layer = Layer(kind, 3, inter=1024, shared=shared)
     want, rc = layer.run()
     assert rc == B.MOE_OK and torch.isfinite(want).all()
     monkeypatch.setenv("MOE_DEBUG_WITHHOLD_LOADS", withheld)
-    _, rc = layer.run()
+    y, rc = layer.run(fill=7.0)
     assert rc == B.MOE_ERR_DEVICE_TIMEOUT
+    assert torch.all(y == 7.0)
     monkeypatch.delenv("MOE_DEBUG_WITHHOLD_LOADS")
     got, rc = layer.run()
     assert rc == B.MOE_OK
     assert torch.equal(got, want)
+
+
+def test_a_cta_that_gave_up_is_missed(monkeypatch):
+    """One CTA's down products fail at their start and the others go on for a while, so
+    that they are still waiting for it when it has given up.  They must not take its
+    sums, which were never written, for an answer."""
+    layer = Layer("mxfp4", 16, d=7168, E=64, inter=8192, shared=0)
+    monkeypatch.setenv("MOE_DEBUG_WITHHOLD_LOADS", "2")
+    y, rc = layer.run(fill=7.0)
+    assert rc == B.MOE_ERR_DEVICE_TIMEOUT
+    assert torch.all(y == 7.0)
