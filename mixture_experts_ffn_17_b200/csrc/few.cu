@@ -1595,6 +1595,17 @@ __device__ void combine(const FewParams& p, const Lists& ls) {
   }
 }
 
+// Waits for the last copies of a ring of `size` barriers that was armed `n` times.  All
+// were issued before the first wait, so that its limit is the limit of all of them.
+__device__ __noinline__ void land_copies(uint64_t* bars, int size, int n, Control& c, uint32_t* status) {
+  for (int j = max(0, n - size); j < n; ++j) {
+    if (!ptx::wait_bounded(&bars[j % size], (j / size) & 1, &c.never)) {
+      raise_status(status, &c.abort, kStatusTimeout);
+      return;
+    }
+  }
+}
+
 // Of a whole call the accumulators' drain has seen every MMA done.  Of one that gave up
 // they must land before TMEM and the CTA go: each issuer waits for its own.  (A call:
 // inlined, it moved the code of the e4m3 layer so that T = 8 took 254 instead of 249 us.)
@@ -1677,9 +1688,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     if (ok) ok = produce<RT, RT, false, true>(maps, p, ls, sm, ring, p.bar + 6);
     if (ok && p.S > 0) produce<kFewBf16, RT, true, true>(maps, p, ls, sm, ring, p.bar + 7);
     // every issued copy must land before the CTA may exit
-    if ((threadIdx.x & 31) == 0)
-      for (int j = ring.n > S ? ring.n - S : 0; j < ring.n; ++j)
-        if (!ptx::wait_bounded(&ct.full[j % S], (j / S) & 1, &ct.never)) raise_status(p.status, abort, kStatusTimeout);
+    if ((threadIdx.x & 31) == 0) land_copies(ct.full, S, ring.n, ct, p.status);
   } else if (warp == kWarps + 1) {
     // ---------------------------------------------- columns
     Ring ring;
@@ -1702,9 +1711,7 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     }
     if (ok && p.S > 0) bring_columns<RT, true, true>(p, ls, sm, ring);
     // every issued copy must land before the CTA may exit
-    for (int j = ring.cols > 2 ? ring.cols - 2 : 0; j < ring.cols; ++j)
-      if (!ptx::wait_bounded(&ct.col_full[j & 1], (j >> 1) & 1, &ct.never))
-        raise_status(p.status, abort, kStatusTimeout);
+    land_copies(ct.col_full, 2, ring.cols, ct, p.status);
   } else if (warp > kWarps) {
     // ---------------------------------------------- router
     if constexpr (kCoded) {

@@ -31,6 +31,7 @@ struct MxProduct {
   const int32_t* offsets;    // [E + 1]
   void* Y;                   // [rows, N]
   uint32_t* status;
+  bool withhold;             // tests: no operands are loaded
 };
 
 // Tensor maps over the codes as bytes, 128-byte boxes with the 128-byte

@@ -222,16 +222,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           uint8_t* st = stage0 + s * kStageBytes;
           ptx::mbar_arrive_expect_tx(&sh.full[s], kWBytes + boxes * box_bytes);
+          if (p.withhold) continue;
           ptx::tma_load_2d(st, &tmW, &sh.full[s], kb * (kK / 2), wrow, pol_w);
           for (int b = 0; b < boxes; ++b)
             ptx::tma_load_2d(st + kWBytes + b * box_bytes, small ? &tmA16 : &tmA64, &sh.full[s], kb * (kK / 2),
                              (int)ti.row0 + b * (small ? 16 : 64), pol_t);
         }
       }
-      // every issued copy must land before the CTA may exit
-      for (int j = (kg > kStages ? kg - kStages : 0); j < kg; ++j)
-        if (!ptx::wait_bounded(&sh.full[j % kStages], (j / kStages) & 1, &sh.never))
+      // every issued copy must land before the CTA may exit; all were issued before the
+      // first wait, so that its limit is the limit of all of them
+      for (int j = (kg > kStages ? kg - kStages : 0); j < kg; ++j) {
+        if (!ptx::wait_bounded(&sh.full[j % kStages], (j / kStages) & 1, &sh.never)) {
           raise_status(p.status, abort, kStatusTimeout);
+          break;
+        }
+      }
     }
   } else if (warp == 9) {
     // ------------------------------------------------ MMA

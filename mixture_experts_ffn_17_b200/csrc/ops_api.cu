@@ -364,6 +364,7 @@ moe_status moe_mx_grouped_product(int64_t rows, int E, int K, int N, const void*
   p.offsets = offsets;
   p.Y = Y;
   p.status = at<uint32_t>(ws, 0);
+  p.withhold = debug_withhold() == 1;
   MOE_CUDA(launch_mx_product(w, a16, a64, p, y_dtype == MOE_BF16, device_sms(), st));
   return MOE_OK;
 }

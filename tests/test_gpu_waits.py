@@ -1,6 +1,9 @@
-"""The waits inside moe_forward_few: warps that come late, and waits that run out.
+"""The waits inside moe_forward_few and moe_mx_grouped_product: warps that come late,
+and waits that run out.
 Neither faults nor hangs: every wait is bounded, and debug switches of the library
 hold a warp up or withhold loads."""
+import time
+
 import pytest
 import torch
 
@@ -8,6 +11,9 @@ from mixture_experts_ffn_17_b200 import binding as B
 from mixture_experts_ffn_17_b200 import build as libbuild
 
 pytestmark = pytest.mark.gpu
+# A wait's limit is 2 s.  A call that gives up waits twice: for what it was withheld,
+# and for the copies that it may have under way; a second more for the host.
+GIVEN_UP = 5.0
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -71,8 +77,10 @@ def test_waits_run_out_and_the_next_call_is_right(monkeypatch, kind, shared, wit
     want, rc = layer.run()
     assert rc == B.MOE_OK and torch.isfinite(want).all()
     monkeypatch.setenv("MOE_DEBUG_WITHHOLD_LOADS", withheld)
+    t0 = time.monotonic()
     y, rc = layer.run(fill=7.0)
     assert rc == B.MOE_ERR_DEVICE_TIMEOUT
+    assert time.monotonic() - t0 < GIVEN_UP
     assert torch.all(y == 7.0)
     monkeypatch.delenv("MOE_DEBUG_WITHHOLD_LOADS")
     got, rc = layer.run()
@@ -89,3 +97,31 @@ def test_a_cta_that_gave_up_is_missed(monkeypatch):
     y, rc = layer.run(fill=7.0)
     assert rc == B.MOE_ERR_DEVICE_TIMEOUT
     assert torch.all(y == 7.0)
+
+
+@pytest.mark.parametrize("rows", [3, 700])
+def test_a_product_without_operands_gives_up(monkeypatch, rows):
+    E, K, N = 3, 2048, 256
+    g = torch.Generator(device="cuda").manual_seed(1)
+    u8 = lambda *s, lo=0, hi=256: torch.randint(lo, hi, s, generator=g, device="cuda", dtype=torch.uint8)
+    args = (u8(rows, K // 2), u8(rows, K // 32, lo=120, hi=128),
+            torch.tensor([0, rows // 3, rows // 3, rows], dtype=torch.int32, device="cuda"),
+            u8(E, N, K // 2), u8(E, N, K // 32, lo=120, hi=128))
+    ws = B.alloc_mx_product_workspace(rows, E)
+
+    def product():
+        Y = torch.full((rows, N), 7.0, device="cuda")
+        B.mx_grouped_product(*args, Y, ws)
+        return Y, B.check_device_status(ws)[0]
+
+    want, rc = product()
+    assert rc == B.MOE_OK
+    monkeypatch.setenv("MOE_DEBUG_WITHHOLD_LOADS", "1")
+    t0 = time.monotonic()
+    Y, rc = product()
+    assert rc == B.MOE_ERR_DEVICE_TIMEOUT
+    assert time.monotonic() - t0 < GIVEN_UP
+    assert torch.all(Y == 7.0)
+    monkeypatch.delenv("MOE_DEBUG_WITHHOLD_LOADS")
+    got, rc = product()
+    assert rc == B.MOE_OK and torch.equal(got, want)
