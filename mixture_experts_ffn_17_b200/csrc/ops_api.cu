@@ -265,6 +265,9 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.late_factors = debug_late_factors();
   p.withhold = debug_withhold();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // before the maps: the driver makes none in a thread that has no context yet, and
+  // this call gives it one
+  MOE_CUDA(cudaMemsetAsync(ws, 0, kAlign, st));
   const int weights = few_weights(s);
   FewMaps maps{};
   const void* routed[] = {W1, W3, W2};
@@ -285,7 +288,6 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
         !map_bytes(&maps.h_terms, p.h_r, s.inter / per_byte, (uint64_t)s.T * s.k * rows, rows))
       return MOE_ERR_CUDA;
   }
-  MOE_CUDA(cudaMemsetAsync(ws, 0, kAlign, st));
   MOE_CUDA(launch_few(p, maps, weights, device_sms(), st));
   return MOE_OK;
 }
