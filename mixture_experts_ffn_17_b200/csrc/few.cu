@@ -1777,10 +1777,16 @@ template <int RT>
 cudaError_t launch(const FewParams& p, const FewMaps& maps, int sms, cudaStream_t stream) {
   // stages, the columns, the pairs' joins; a routing key and a logit per expert and
   // router warp, or the scales' exchange
-  const size_t smem = 1024 + Cfg<RT>::kStages * Cfg<RT>::kStageBytes + 2 * Cfg<RT>::kColBytes + 8 * kRedFloats * 4 +
-                      std::max<size_t>((size_t)kRouterWarps * p.E * 12, Cfg<RT>::kCoded ? kExchangeBytes : 0);
+  auto bytes = [](size_t experts) {
+    return 1024 + Cfg<RT>::kStages * Cfg<RT>::kStageBytes + 2 * Cfg<RT>::kColBytes + 8 * kRedFloats * 4 +
+           std::max<size_t>(kRouterWarps * experts * 12, Cfg<RT>::kCoded ? kExchangeBytes : 0);
+  };
+  const size_t smem = bytes(p.E);
   auto kernel = few_kernel<RT>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the most that any call takes: a limit of its own could be lowered by another
+  // thread's call before this one's launch
+  cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(kMaxExperts));
   if (err != cudaSuccess) return err;
   void* args[] = {const_cast<FewParams*>(&p), const_cast<FewMaps*>(&maps)};
   return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(sms), dim3(kAllThreads), args, smem,

@@ -1,4 +1,7 @@
 """Calls of moe_forward_few that the batches of its other tests do not make."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -60,3 +63,33 @@ def test_a_threads_first_cuda_call():
     assert not run_threads(lambda: layer.run(layer.stream))
     torch.cuda.synchronize()
     assert torch.equal(layer.y, want)
+
+
+@pytest.mark.parametrize("process", range(2))
+def test_threads_with_layers_of_different_sizes(process):
+    """A layer with more experts takes more shared memory, whatever another thread's
+    layer takes at that moment.  In processes of their own, whose first launches these
+    are: they take long, so that the threads' calls overlap (a limit on shared memory
+    that each call sets for itself refused one or more of them in two of three runs)."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    child = subprocess.run([sys.executable, "-c", "import test_gpu_few_calls as t; t.first_calls_of_threads()"],
+                           cwd=here, env={**os.environ, "PYTHONPATH": os.path.dirname(here)}, timeout=120,
+                           capture_output=True, text=True)
+    assert child.returncode == 0, child.stdout + child.stderr
+
+
+def first_calls_of_threads():
+    layers = [Layer(E) for E in (32,) * 4 + (1024,) * 4]
+    torch.cuda.synchronize()
+    start = threading.Barrier(len(layers))
+
+    def calls(layer):
+        start.wait()
+        for _ in range(100):
+            layer.run(layer.stream)
+        layer.stream.synchronize()
+
+    errors = run_threads(*[lambda layer=layer: calls(layer) for layer in layers])
+    assert not errors, errors
+    for i in (0, 4):  # equal layers, equal results
+        assert all(torch.equal(layer.y, layers[i].y) for layer in layers[i:i + 4])
