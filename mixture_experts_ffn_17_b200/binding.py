@@ -324,7 +324,8 @@ def backward_saved(shape, x, Wg, W1, W3, W2, W1s, W3s, W2s, dy, dx, dWg, dW1, dW
 # ------------------------------------------------------------------ few tokens, MXFP4, gradients
 # The calls below run on the device of their tensors, whichever is current, and
 # by default on that device's current stream.
-_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+_DTYPES = {_F32: MOE_F32, _BF16: MOE_BF16}
 
 
 def _on(device, stream, call):
@@ -354,6 +355,16 @@ def _adr(t, device):
     return t.data_ptr()
 
 
+def _fit(t, device, n, dtype, what):
+    """_adr of a tensor with at least n elements of a type (an int: of any type of so many bytes)."""
+    if t is None:
+        return None  # the library's to refuse
+    if t.numel() < n or (t.dtype is not dtype and t.element_size() != dtype):
+        kind = f"{dtype}-byte values" if isinstance(dtype, int) else dtype
+        raise ValueError(f"{what} has {t.numel()} elements of {t.dtype}, {n} of {kind} needed")
+    return _adr(t, device)
+
+
 def _dtype(t):
     try:
         return _DTYPES[t.dtype]
@@ -380,9 +391,27 @@ def alloc_few_workspace(shape: MoeShape, device="cuda") -> torch.Tensor:
 def forward_few(shape, x, Wg, bias, W1, W3, W2, s1, s3, s2, W1s, W3s, W2s, y, ws, topk_idx=None, topk_w=None,
                 counts=None, stream=None):
     """The layer for at most MOE_FEW_MAX_TOKENS tokens (moe_forward_few), bf16,
-    e4m3 or MXFP4 experts; arguments as forward()."""
-    dev = x.device
-    a = [_adr(t, dev) for t in (x, Wg, bias, W1, W3, W2, s1, s3, s2, W1s, W3s, W2s, y, topk_idx, topk_w, counts, ws)]
+    e4m3 or MXFP4 experts; arguments as forward().  Tensors that are shorter than
+    the shape needs, or of another type, are refused."""
+    dev, kind = x.device, shape.w_dtype
+    T, d, E, k, I, S = shape.T, shape.d, shape.E, shape.k, shape.inter, shape.shared_inter
+    n = E * d * I  # values of a matrix; its codes and scales
+    codes, wide, scales, per_scale = ((n, _BF16, 0, None) if kind == MOE_BF16 else
+                                      (n, 1, n // 16384, _F32) if kind == MOE_E4M3 else (n // 2, 1, n // 32, 1))
+    if not scales:
+        s1 = s3 = s2 = None
+    if not S:
+        W1s = W3s = W2s = None
+    if shape.route != MOE_ROUTE_SIGMOID_GROUP:
+        bias = None
+    a = (_fit(x, dev, T * d, _BF16, "x"), _fit(Wg, dev, E * d, _BF16, "Wg"), _fit(bias, dev, E, _F32, "bias"),
+         _fit(W1, dev, codes, wide, "W1"), _fit(W3, dev, codes, wide, "W3"), _fit(W2, dev, codes, wide, "W2"),
+         _fit(s1, dev, scales, per_scale, "s1"), _fit(s3, dev, scales, per_scale, "s3"),
+         _fit(s2, dev, scales, per_scale, "s2"), _fit(W1s, dev, d * S, _BF16, "W1s"),
+         _fit(W3s, dev, d * S, _BF16, "W3s"), _fit(W2s, dev, S * d, _BF16, "W2s"),
+         _fit(y, dev, T * d, _F32 if shape.y_dtype == MOE_F32 else _BF16, "y"),
+         _fit(topk_idx, dev, T * k, _I32, "topk_idx"), _fit(topk_w, dev, T * k, _F32, "topk_w"),
+         _fit(counts, dev, E, _I32, "counts"), _adr(ws, dev))
     fn, size = lib().moe_forward_few, ws.numel()
     _check(_on(dev, stream, lambda st: fn(ctypes.byref(shape), *a, size, st)), "moe_forward_few")
 
