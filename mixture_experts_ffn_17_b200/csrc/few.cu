@@ -153,14 +153,13 @@ __device__ __forceinline__ void consumer_sync() { ptx::named_barrier(9, kThreads
 __device__ __forceinline__ void router_sync() { ptx::named_barrier(10, 32 * kRouterWarps); }
 
 // ------------------------------------------------------------ grid barrier
-// Functions of their own: inlined four times they cost the e4m3 layer 1% (T = 8, 251.8
-// instead of 248.8 us).
-
 // The consumers' writes so far are visible to who waits.  A CTA one of whose consumers
-// gave up is missed: the others must not read what it has not written.
-__device__ __noinline__ void grid_arrive(uint32_t* bar, bool ok) {
-  ok = ptx::named_barrier_and(9, kThreads, ok);
-  if (ok && threadIdx.x == 0) {
+// gave up (and raised the flag before it came here) is missed: the others must not read
+// what it has not written.  (A call: inlined it took the coded layers 1% longer, at T = 8
+// e4m3 252.7 instead of 248.3 us and MXFP4 178.0 instead of 175.6.)
+__device__ __noinline__ void grid_arrive(uint32_t* bar, const volatile uint32_t* abort) {
+  consumer_sync();
+  if (threadIdx.x == 0 && *abort == 0) {
     __threadfence();
     atomicAdd(bar, 1u);
   }
@@ -187,7 +186,7 @@ __device__ __forceinline__ bool grid_poll(const uint32_t* bar, uint32_t count, u
 }
 
 // All consumers' wait: they go on, or none of them.
-__device__ __noinline__ bool grid_wait(const uint32_t* bar, uint32_t* status, volatile uint32_t* abort) {
+__device__ bool grid_wait(const uint32_t* bar, uint32_t* status, volatile uint32_t* abort) {
   if (threadIdx.x == 0) grid_poll(bar, gridDim.x, status, abort);
   return ptx::named_barrier_and(9, kThreads, *abort == 0);
 }
@@ -421,18 +420,16 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
       for (int o = from; o < end; o += 64)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(scales + (int64_t)(32 * i) * pitch + o) : "memory");
   };
-  // tiles that a test withholds: these and all later ones
-  int withheld = 0x7fffffff;
-  if (p.withhold == 1) withheld = ring.n;
-  if (p.withhold == 2 && DOWN && !SHARED && blockIdx.x == 0) withheld = ring.n + 1;
   int id = blockIdx.x;
   while (id < share.total) {
     int claimed = 0;
     if (lane == 0) claimed = (int)atomicAdd(counter, 1u) + gridDim.x;  // used after this chunk
     bool fetched = WT != kFewMxfp4;
     const bool ok = share.passes(share.chunk(p, ls, id), [&](const Piece& q) {
-      // the columns' warp adds the terms to a stage of codes
-      const uint32_t bytes = kTileBytes + (WT == kFewBf16 ? 0 : q.rows * few_term_rows(WT) * 128);
+      // the columns' warp adds the terms to a stage of codes; tests have stages wait for
+      // more than comes
+      uint32_t bytes = kTileBytes + (WT == kFewBf16 ? 0 : q.rows * few_term_rows(WT) * 128) + p.missing;
+      if (DOWN && !SHARED && blockIdx.x == 0) bytes += p.missing_down;
       for (int step = q.step0; step < q.step1; ++step, ++ring.n) {
         const int s = ring.n % S;
         if (!slot_free()) return false;
@@ -440,9 +437,7 @@ __device__ bool produce(const FewMaps& m, const FewParams& p, const Lists& ls, c
           ptx::mbar_arrive_expect_tx(&c.full[s], bytes);
           c.chunk[ring.n % (2 * S)] = id;
           ptx::mbar_arrive(&c.issued[ring.n % (2 * S)]);
-          if (ring.n < withheld)
-            load_tile<WT, SHARED>(m, p, q, step, sm.stages + s * Cfg<RT>::kStageBytes, &c.full[s],
-                                  q.again ? more : once);
+          load_tile<WT, SHARED>(m, p, q, step, sm.stages + s * Cfg<RT>::kStageBytes, &c.full[s], q.again ? more : once);
         }
         __syncwarp();
         if (!fetched && (step == q.step0 + 1 || step == q.step1 - 1)) {
@@ -1733,30 +1728,30 @@ __global__ void __launch_bounds__(kAllThreads, 1)
     // ---------------------------------------------- consumers
     Ring ring, coded;
     logits_share(p, reinterpret_cast<double*>(sm.red));
-    grid_arrive(p.bar + 0, true);
+    grid_arrive(p.bar + 0, abort);
     bool ok = true, whole = false;
     if (p.S > 0) ok = consume<RT, true, false>(p, ls, sm, ring);
     // all consumers agree on whether there are lists
     ok = ptx::named_barrier_and(9, kThreads, ok && ptx::wait_bounded(&ct.routed, 0, abort) && *abort == 0);
-    if (ok) ok = consume_routed<RT, false>(p, ls, sm, ring, coded);
-    grid_arrive(p.bar + 1, ok && *abort == 0);
+    if (ok) consume_routed<RT, false>(p, ls, sm, ring, coded);
+    grid_arrive(p.bar + 1, abort);
     if (grid_wait(p.bar + 1, p.status, abort)) {
       if (kCoded) ring.n = ct.position;
       activations<RT>(p);
       ptx::fence_proxy_async_all();  // bulk copies will read h
-      grid_arrive(p.bar + 2, true);
+      grid_arrive(p.bar + 2, abort);
       if (grid_wait(p.bar + 2, p.status, abort)) {
         if (threadIdx.x == 0) ptx::mbar_arrive(&ct.ready);
-        ok = consume_routed<RT, true>(p, ls, sm, ring, coded);
+        consume_routed<RT, true>(p, ls, sm, ring, coded);
         if (p.S > 0) {
           if (kCoded) {
             // the ring's position is known to the warp that issued the MMAs
             consumer_sync();
             ring.n = ct.position;
           }
-          ok = consume<RT, true, true>(p, ls, sm, ring) && ok;
+          consume<RT, true, true>(p, ls, sm, ring);
         }
-        grid_arrive(p.bar + 3, ok && *abort == 0);
+        grid_arrive(p.bar + 3, abort);
         whole = grid_wait(p.bar + 3, p.status, abort);
         if (whole) combine(p, ls);
       }

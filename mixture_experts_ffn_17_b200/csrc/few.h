@@ -70,10 +70,10 @@ struct FewParams {
   uint8_t* x_terms;
   float *x_scale, *h_scale;                // e4m3: the power of two that undoes the scaling of 128 values
   uint8_t *x_term_scales, *h_term_scales;  // MXFP4: [row][few_term_rows][K / 32]
-  // for tests: e4m3's factors' warp is held up before every stage; no weight tiles are
-  // loaded (1), or by the first CTA none of the routed down products but one (2)
+  // for tests: e4m3's factors' warp is held up before every stage; bytes that never come
+  // of every tile, and of the first CTA's tiles of the routed down products
   bool late_factors;
-  int withhold;
+  uint32_t missing, missing_down;
 };
 
 // Tensor maps of W1, W3 and W2, all with the 128-byte swizzle.  bf16: [E, K, N]

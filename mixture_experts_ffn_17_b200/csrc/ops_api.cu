@@ -87,9 +87,9 @@ bool debug_late_factors() {
   return v && v[0] == '1';
 }
 
-// MOE_DEBUG_WITHHOLD_LOADS=1 makes the producers issue no loads, 2 one CTA of the
-// few-token layer only, in its routed down products (tests: the waits run out and
-// the call reports MOE_ERR_DEVICE_TIMEOUT).
+// MOE_DEBUG_WITHHOLD_LOADS=1 withholds a part of every load, 2 of one CTA's in the
+// routed down products of the few-token layer (tests: the waits run out and the call
+// reports MOE_ERR_DEVICE_TIMEOUT).
 int debug_withhold() {
   const char* v = std::getenv("MOE_DEBUG_WITHHOLD_LOADS");
   return v && (v[0] == '1' || v[0] == '2') ? v[0] - '0' : 0;
@@ -263,7 +263,8 @@ moe_status moe_forward_few(const moe_shape* shape, const void* x, const void* Wg
   p.x_term_scales = at<uint8_t>(ws, L.x_term_scales);
   p.h_term_scales = at<uint8_t>(ws, L.h_term_scales);
   p.late_factors = debug_late_factors();
-  p.withhold = debug_withhold();
+  p.missing = debug_withhold() == 1 ? 16 : 0;
+  p.missing_down = debug_withhold() == 2 ? 16 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // before the maps: the driver makes none in a thread that has no context yet, and
   // this call gives it one
