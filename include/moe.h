@@ -383,7 +383,8 @@ moe_status moe_forward_profiled(const moe_shape* shape, const void* x, const voi
  *     rounds both to bf16); y is rounded once, to shape->y_dtype;
  *   - with e4m3 and MXFP4 experts x and h enter the products as sums of terms of
  *     the weights' own type, together good to 2^-24 of the largest value of 128
- *     (e4m3) or 32 (MXFP4) neighbouring ones; an infinity enters as NaN.
+ *     (e4m3) or 32 (MXFP4) neighbouring ones; an infinity enters as NaN.  With
+ *     bf16 experts infinities go the way that fp32 arithmetic gives them.
  *   shape: as moe_forward; w_dtype may also be MOE_MXFP4.
  *   W1, W3, W2, s1, s3, s2: bf16 and e4m3 weights (with fp32 block scales) as
  *     moe_grouped_swiglu; MOE_MXFP4 weights with the contraction innermost, as

@@ -640,8 +640,10 @@ __device__ __forceinline__ void consume_piece(const FewParams& p, const Piece& q
   ptx::named_barrier(1 + pair, 64);
   for (int i = team * 32 + lane; i < q.rows * 16; i += 64) {
     const int r = i >> 4, col = i & 15;
+    // An infinite weight makes the leading term's sum infinite, and NaN of the sums of the
+    // lower terms where those are zero: the leading one is the sum then.
     float a = 0.0f;
-    for (int t = 0; t < q.group; ++t) {
+    for (int t = 0; t < q.group && fabsf(a) < __uint_as_float(0x7f800000u); ++t) {
       const float* x = red + (r * q.group + t) * kRedPitch + col;
       a += x[0] + x[kMaxCols * kRedPitch];
     }
