@@ -93,9 +93,16 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) 
   }
 }
 
-// silu(g) * u: the exponential is good to one step of fp32, the reciprocal and the
-// products add four halves.  silu(g) first: g * u may overflow where it does not.
-__device__ __forceinline__ float gated(float g, float u) { return g * __fdividef(1.0f, 1.0f + expf(-g)) * u; }
+// silu(g) * u, silu(g) = g / (1 + e^-g) = g e^g / (1 + e^g), of which the form whose
+// exponential is at most 1 is taken: the denominator stays between 1 and 2, where the fast
+// reciprocal is good, and silu(g) small instead of 0 down to the smallest fp32 numbers.
+// The exponential is good to one step of fp32 (2^-149 at least), the sum, the reciprocal
+// and the products add some five halves.  silu(g) first: g * u may overflow where it does
+// not.
+__device__ __forceinline__ float gated(float g, float u) {
+  const float e = expf(-fabsf(g));
+  return (g < 0.0f ? g * e : g) * __fdividef(1.0f, 1.0f + e) * u;
+}
 
 // Groups of 8 values in flight per thread: 2048 threads of an SM with 16 bytes each
 // do not cover HBM's latency (58% of its rate, with 64 bytes 84%).
