@@ -13,8 +13,11 @@
 // in the opposite order, so that what the norm read last is still in L2.
 //
 // Sums: the 4 or 8 squares of one 16-byte vector are added in fp32 and the
-// result goes to an fp64 accumulator (one conversion per vector instead of one
-// per element, which the fp64 pipe would not keep up with).  A vector whose sum
+// result goes to an fp64 accumulator: at most 4 (fp32) or 7 roundings of 2^-24
+// in a sum of squares, half as much in the norm.  With every square in fp64
+// norm and clipping of 750M bf16 values took 899 us instead of 736 (conversions;
+// with the fp64 numbers made from the bits 758, with the fp32 sums' errors
+// carried along 760).  A vector whose sum
 // leaves [1e-30, 1e30] is done again in fp64 element by element, so neither
 // tiny gradients vanish nor large ones overflow; all-zero vectors (experts no
 // token chose) are skipped.
