@@ -479,10 +479,13 @@ moe_status moe_grad_norm(const moe_tensor* tensors, int n, float* norm_out, void
 
 /* Clipping by the global norm: out = data * min(1, max_norm / (norm + 1e-6)),
  * one fp32 product rounded to the tensor's type; norm_out as moe_grad_norm
- * (may be NULL).  An infinite norm gives the factor 0 and a NaN norm a NaN
- * factor, so norm_out tells whether a step is to be skipped.  In place and with
- * factor 1 the tensors are not written.  max_norm >= 0.  No written range may
- * overlap another tensor's range, or its own source other than exactly in place
+ * (may be NULL).  The norm is that of this call's tensors: it takes all that
+ * are to be clipped together, and where several processes hold parts of them
+ * each would clip by its own part's norm.  With a finite max_norm an infinite
+ * norm gives the factor 0; a NaN norm, or both infinite, a NaN factor, so
+ * norm_out tells whether a step is to be skipped.  In place and with factor 1
+ * the tensors are not written.  max_norm >= 0.  No written range may overlap
+ * another tensor's range, or its own source other than exactly in place
  * (MOE_ERR_INVALID_ARG). */
 moe_status moe_grad_clip(const moe_tensor* tensors, int n, float max_norm, float* norm_out, void* ws, size_t ws_bytes,
                          void* stream);
