@@ -528,7 +528,7 @@ def grad_norm(grads, norm, ws, stream=None):
     """norm [1] fp32 = the global norm of the tensors of `grads` (moe_grad_norm)."""
     dev = norm.device
     arr, n = _tensor_list(grads, None, dev), len(grads)
-    o, w, size = _adr(norm, dev), _adr(ws, dev), ws.numel()
+    o, w, size = _fit(norm, dev, 1, _F32, "norm"), _adr(ws, dev), ws.numel()
     fn = lib().moe_grad_norm
     _check(_on(dev, stream, lambda st: fn(arr, n, o, w, size, st)), "moe_grad_norm")
 
@@ -539,7 +539,7 @@ def grad_clip(grads, max_norm, norm, ws, out=None, stream=None):
     fp32 receives the norm before clipping (None: not returned)."""
     dev = ws.device
     arr, n = _tensor_list(grads, out, dev), len(grads)
-    o, w, size = _adr(norm, dev), _adr(ws, dev), ws.numel()
+    o, w, size = _fit(norm, dev, 1, _F32, "norm"), _adr(ws, dev), ws.numel()
     fn = lib().moe_grad_clip
     _check(_on(dev, stream, lambda st: fn(arr, n, max_norm, o, w, size, st)), "moe_grad_clip")
 

@@ -76,3 +76,14 @@ def test_few_refuses_another_kinds_weights():
         few(B.MOE_BF16, y_dtype=B.MOE_BF16)
     with pytest.raises(ValueError, match="^y has"):
         few(B.MOE_BF16, y=torch.zeros(T, D, dtype=BF16))
+
+
+@pytest.mark.parametrize("bad", [torch.zeros(0), torch.zeros(1, dtype=BF16), torch.zeros(1, dtype=torch.float64)])
+def test_norm_needs_room_for_an_fp32_number(bad):
+    ws = torch.zeros(1 << 16, dtype=U8)
+    with pytest.raises(ValueError, match="^norm has"):
+        B.grad_norm([torch.zeros(4)], bad, ws)
+    with pytest.raises(ValueError, match="^norm has"):
+        B.grad_clip([torch.zeros(4)], 1.0, bad, ws)
+    with pytest.raises(ValueError, match="CUDA"):
+        B.grad_clip([torch.zeros(4)], 1.0, None, ws)
