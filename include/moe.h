@@ -484,9 +484,9 @@ moe_status moe_grad_norm(const moe_tensor* tensors, int n, float* norm_out, void
  * each would clip by its own part's norm.  With a finite max_norm an infinite
  * norm gives the factor 0; a NaN norm, or both infinite, a NaN factor, so
  * norm_out tells whether a step is to be skipped.  In place and with factor 1
- * the tensors are not written.  max_norm >= 0.  No written range may overlap
- * another tensor's range, or its own source other than exactly in place
- * (MOE_ERR_INVALID_ARG). */
+ * the tensors are not written.  max_norm >= 0.  No written range (norm_out's
+ * too) may overlap another tensor's range, or its own source other than exactly
+ * in place (MOE_ERR_INVALID_ARG). */
 moe_status moe_grad_clip(const moe_tensor* tensors, int n, float max_norm, float* norm_out, void* ws, size_t ws_bytes,
                          void* stream);
 

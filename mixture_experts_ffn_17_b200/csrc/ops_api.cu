@@ -114,14 +114,17 @@ moe_status check_few(const moe_shape* shape) {
 }
 
 // ------------------------------------------------------------ gradients
-// Ranges that a clipping call writes must be disjoint from all others.
-bool ranges_overlap(const moe_tensor* t, int n) {
+// Ranges that a clipping call writes, the norm's among them, must be disjoint from all
+// others.
+bool ranges_overlap(const moe_tensor* t, int n, const float* norm_out) {
   struct Range {
     uintptr_t begin, end;
     bool write;
   };
-  Range r[2 * kGradMaxTensors];
+  Range r[2 * kGradMaxTensors + 1];
   int m = 0;
+  const uintptr_t norm = reinterpret_cast<uintptr_t>(norm_out);
+  if (norm_out) r[m++] = Range{norm, norm + sizeof(float), true};
   for (int i = 0; i < n; ++i) {
     if (t[i].count == 0) continue;
     const uintptr_t bytes = (uintptr_t)t[i].count * (t[i].dtype == MOE_BF16 ? 2 : 4);
@@ -140,7 +143,7 @@ bool ranges_overlap(const moe_tensor* t, int n) {
   return false;
 }
 
-moe_status check_tensors(const moe_tensor* t, int n, bool clip) {
+moe_status check_tensors(const moe_tensor* t, int n, bool clip, const float* norm_out) {
   if (n < 0 || (n > 0 && !t)) return MOE_ERR_INVALID_ARG;
   if (n > kGradMaxTensors) return MOE_ERR_UNSUPPORTED;
   for (int i = 0; i < n; ++i) {
@@ -151,7 +154,7 @@ moe_status check_tensors(const moe_tensor* t, int n, bool clip) {
     if (!t[i].data || !aligned(t[i].data, size)) return MOE_ERR_INVALID_ARG;
     if (clip && t[i].out && !aligned(t[i].out, size)) return MOE_ERR_INVALID_ARG;
   }
-  return clip && ranges_overlap(t, n) ? MOE_ERR_INVALID_ARG : MOE_OK;
+  return clip && ranges_overlap(t, n, norm_out) ? MOE_ERR_INVALID_ARG : MOE_OK;
 }
 
 int grad_batches(int n) { return std::max(1, (n + kGradBatch - 1) / kGradBatch); }
@@ -378,7 +381,7 @@ size_t moe_grad_workspace_size(int n) {
 }
 
 moe_status moe_grad_norm(const moe_tensor* tensors, int n, float* norm_out, void* ws, size_t ws_bytes, void* stream) {
-  const moe_status v = check_tensors(tensors, n, false);
+  const moe_status v = check_tensors(tensors, n, false, norm_out);
   if (v != MOE_OK) return v;
   if (!norm_out || !aligned(norm_out, 4)) return MOE_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes, grad_ws_bytes(n))) return MOE_ERR_WORKSPACE;
@@ -393,7 +396,7 @@ moe_status moe_grad_norm(const moe_tensor* tensors, int n, float* norm_out, void
 
 moe_status moe_grad_clip(const moe_tensor* tensors, int n, float max_norm, float* norm_out, void* ws, size_t ws_bytes,
                          void* stream) {
-  const moe_status v = check_tensors(tensors, n, true);
+  const moe_status v = check_tensors(tensors, n, true, norm_out);
   if (v != MOE_OK) return v;
   if (!(max_norm >= 0.0f) || !aligned(norm_out, 4)) return MOE_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes, grad_ws_bytes(n))) return MOE_ERR_WORKSPACE;

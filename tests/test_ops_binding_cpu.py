@@ -1,5 +1,7 @@
 """Tensors that do not fit a call are refused by the binding, before the library sees
-their addresses."""
+their addresses; and a norm that would land among the gradients, by the library."""
+import ctypes
+
 import pytest
 import torch
 
@@ -87,3 +89,20 @@ def test_norm_needs_room_for_an_fp32_number(bad):
         B.grad_clip([torch.zeros(4)], 1.0, bad, ws)
     with pytest.raises(ValueError, match="CUDA"):
         B.grad_clip([torch.zeros(4)], 1.0, None, ws)
+
+
+def test_clip_refuses_a_norm_among_the_tensors():
+    buf = ctypes.create_string_buffer((1 << 16) + 256)
+    p = ctypes.addressof(buf) + (-ctypes.addressof(buf)) % 256
+    size = B.lib().moe_grad_workspace_size(1)
+
+    def clip(norm, data=p, out=None):
+        arr = (B.MoeTensor * 1)()
+        arr[0] = (data, out, 16, B.MOE_F32)
+        return B.lib().moe_grad_clip(arr, 1, 1.0, norm, p + 8192, size - 1, None)
+
+    for norm, out in ((p, None), (p + 60, None), (p + 4, p + 4096), (p + 4096 + 60, p + 4096)):
+        assert clip(norm, out=out) == B.MOE_ERR_INVALID_ARG
+    # beside them: the workspace that is a byte short is what is left to refuse
+    for norm, out in ((p + 64, None), (p + 4096 + 64, p + 4096), (None, None)):
+        assert clip(norm, out=out) == B.MOE_ERR_WORKSPACE
