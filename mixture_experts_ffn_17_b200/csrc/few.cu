@@ -57,12 +57,17 @@
 //   two threads issue MMAs, and eight warps (MXFP4) bring the scales to TMEM, or one
 //   (e4m3) the factors of the sums.
 //
-// Measured, d = 7168, inner 2048, top-8 of 32 with a shared expert, T = 8 (28
-// experts): bf16 387 us, 6.6 TB/s and the measured copy rate of HBM; e4m3 262 us,
-// 5.0 TB/s, where its tiles' rows of 128 bytes alone allow no more (with the MMAs,
-// scales and terms left out it takes as long); MXFP4 184 us, 4.0 TB/s (160 us
-// without them).  T = 1: 146, 114 and 90 us, of which the phases outside the
-// streams (router, four barriers of 2 us, activations, combine) take some 25.
+// Measured in runs of calls, d = 7168, inner 2048, top-8 of 32 with a shared expert,
+// T = 8 (28 experts): bf16 382 us, 6.7 TB/s and the measured copy rate of HBM; e4m3
+// 248 us, 5.3 TB/s (230 us with the MMAs and terms left out: its tiles' rows of 128
+// bytes); MXFP4 176 us, 4.2 TB/s (159 us without them and the scales).  T = 1: 136, 101
+// and 75 us, of which the phases outside the streams (router, four barriers of 2 us,
+// activations, combine) take some 25.
+//
+// Waits.  Every wait ends after a limit.  Who gives up raises the CTA's abort flag, which
+// ends the CTA's other waits, and releases nothing more; the CTA then misses the grid's
+// next barrier, so that the others give up too and y is not written.  Before the CTA
+// goes, its copies and MMAs under way have landed.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_fp16.h>

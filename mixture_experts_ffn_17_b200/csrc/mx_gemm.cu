@@ -31,9 +31,9 @@
 //
 // Bound: HBM by the weights (17/32 byte a value) up to several hundred rows an
 // expert.  Measured: 512 rows, 226 experts of 7168 x 2048: 297 us, 0.92 of the copy
-// rate; 32768 rows, 256 experts of 2048 x 7168: 485 us alone (0.79), some 610 us in a
-// run of such calls, under the power cap; 32768 rows, 8 experts of 7168 x 2048: 252 us,
-// 3.8 PFLOP/s.
+// rate; 32768 rows, 256 experts of 2048 x 7168, loads as e^(z/2): 491 us in a run of ten
+// calls at 1965 MHz (0.78), 564 us in a run of 4000 at 1477 MHz, under the power cap;
+// 32768 rows, 8 experts of 7168 x 2048: 252 to 265 us, 3.6 to 3.8 PFLOP/s.
 #include <algorithm>
 #include <cstdint>
 

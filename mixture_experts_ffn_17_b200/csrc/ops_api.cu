@@ -87,9 +87,9 @@ bool debug_late_factors() {
   return v && v[0] == '1';
 }
 
-// MOE_DEBUG_WITHHOLD_LOADS=1 withholds a part of every load, 2 of one CTA's in the
-// routed down products of the few-token layer (tests: the waits run out and the call
-// reports MOE_ERR_DEVICE_TIMEOUT).
+// MOE_DEBUG_WITHHOLD_LOADS=1 withholds the product's loads and a part of every tile of
+// the few-token layer, 2 of one CTA's tiles in its routed down products (tests: the
+// waits run out and the call reports MOE_ERR_DEVICE_TIMEOUT).
 int debug_withhold() {
   const char* v = std::getenv("MOE_DEBUG_WITHHOLD_LOADS");
   return v && (v[0] == '1' || v[0] == '2') ? v[0] - '0' : 0;
